@@ -24,6 +24,8 @@
  *   ATTN_MASK_CAUSAL   j <= i                        (requires Sq == Skv)
  *   ATTN_MASK_SLIDING  j <= i and i - j < window     (requires Sq == Skv)
  *   ATTN_MASK_BLOCK    block_mask[b, h, i / bx, j / by] != 0
+ *   ATTN_MASK_SLIDING_FIRST  j <= i and (i - j < window or j < first)
+ *                                                    (requires Sq == Skv)
  *
  * Memory: every tensor argument is a DEVICE pointer owned by the caller,
  * contiguous, 16-byte aligned.  q, o, dO, dq: [B,Hq,Sq,128]; k, v, dk, dv:
@@ -76,7 +78,8 @@ typedef enum {
   ATTN_MASK_NONE = 0,
   ATTN_MASK_CAUSAL = 1,
   ATTN_MASK_SLIDING = 2, /* causal with a window of `window` keys including the diagonal */
-  ATTN_MASK_BLOCK = 3
+  ATTN_MASK_BLOCK = 3,
+  ATTN_MASK_SLIDING_FIRST = 4 /* the same window, and the first `first` keys stay visible */
 } attn_mask_kind_t;
 
 /* Shapes of one call; tensors are contiguous BHSD.  flags: 0, or
@@ -103,12 +106,15 @@ typedef struct {
  * partials written and read per step: the workspace grows by 32 KB + 1 byte
  * per (query head, key tile, query sub-tile) step the key tiles can take at
  * the full lengths (all of them for block masks).  Same results up to
- * rounding order.  ATTN_ERR_UNSUPPORTED with ATTN_FLAG_COMPENSATED or the
- * packed layout.  attn_fwd ignores it (its workspace need is unchanged). */
+ * rounding order.  ATTN_ERR_UNSUPPORTED with ATTN_FLAG_COMPENSATED, the
+ * packed layout or ATTN_MASK_SLIDING_FIRST.  attn_fwd ignores it (its workspace need is unchanged). */
 typedef enum { ATTN_FLAG_COMPENSATED = 1, ATTN_FLAG_SINGLE_PASS = 2 } attn_flag_t;
 
-/* Mask description.  window is read for ATTN_MASK_SLIDING only; bx, by and
- * block_mask for ATTN_MASK_BLOCK only (block_mask is a device pointer).
+/* Mask description.  window is read for ATTN_MASK_SLIDING and
+ * ATTN_MASK_SLIDING_FIRST only; bx, by and block_mask for ATTN_MASK_BLOCK only
+ * (block_mask is a device pointer); first (>= 0) for ATTN_MASK_SLIDING_FIRST
+ * only.  first counts from each sequence's start, as the window does; with
+ * first = 0 the mask is ATTN_MASK_SLIDING.
  *
  * Variable lengths: seqlen_q and seqlen_k, when not NULL, are device int32
  * arrays [B] of the valid query rows and keys of each batch element (values
@@ -145,6 +151,7 @@ typedef struct {
   const int* cu_seqlens_q; /* device [B + 1] or NULL: packed layout */
   const int* cu_seqlens_k; /* device [B + 1] or NULL */
   int total_q, total_k;    /* packed layout: tokens in the query / key tensors */
+  int first;               /* ATTN_MASK_SLIDING_FIRST: first keys that stay visible */
 } attn_mask_desc_t;
 
 /* Workspace bytes needed by attn_fwd and attn_bwd for this shape and mask.

@@ -18,7 +18,8 @@ from . import build as _build
 ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_WORKSPACE, ATTN_ERR_CUDA, \
     ATTN_ERR_TIMEOUT = range(6)
 ATTN_F16, ATTN_BF16 = 0, 1
-ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_SLIDING, ATTN_MASK_BLOCK = range(4)
+ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_SLIDING, ATTN_MASK_BLOCK, \
+    ATTN_MASK_SLIDING_FIRST = range(5)
 
 # Every symbol include/maskattn.h declares.
 EXPORTS = ("attn_workspace_size", "attn_fwd", "attn_bwd", "attn_bwd_noalloc",
@@ -41,7 +42,8 @@ class attn_mask_desc_t(ctypes.Structure):
                 ("by", ctypes.c_int), ("block_mask", ctypes.c_void_p),
                 ("seqlen_q", ctypes.c_void_p), ("seqlen_k", ctypes.c_void_p),
                 ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
-                ("total_q", ctypes.c_int), ("total_k", ctypes.c_int)]
+                ("total_q", ctypes.c_int), ("total_k", ctypes.c_int),
+                ("first", ctypes.c_int)]
 
 
 class AttnError(RuntimeError):
@@ -163,6 +165,7 @@ class Mask:
     max_seqlen_k: int = 0
     total_q: int = 0
     total_k: int = 0
+    first: int = 0   # ATTN_MASK_SLIDING_FIRST: first keys that stay visible
 
     @property
     def packed(self) -> bool:
@@ -177,7 +180,8 @@ class Mask:
                 raise ValueError(f"{n} must be a contiguous int32 tensor")
         return attn_mask_desc_t(self.kind, self.window, self.bx, self.by, ptr(self.block_mask),
                                 ptr(self.seqlen_q), ptr(self.seqlen_k), ptr(self.cu_seqlens_q),
-                                ptr(self.cu_seqlens_k), self.total_q, self.total_k)
+                                ptr(self.cu_seqlens_k), self.total_q, self.total_k,
+                                self.first)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -204,7 +208,7 @@ def shape_of(q: torch.Tensor, k: torch.Tensor, flags: int = 0,
 
 
 def packed_mask(kind: int, seqlens_q, seqlens_k, device, window: int = 0, bx: int = 1,
-                by: int = 1, block_mask: Optional[torch.Tensor] = None) -> Mask:
+                by: int = 1, block_mask: Optional[torch.Tensor] = None, first: int = 0) -> Mask:
     """Mask for the packed layout from per-sequence lengths (host integers)."""
     import itertools
     lq, lk = [int(x) for x in seqlens_q], [int(x) for x in seqlens_k]
@@ -213,7 +217,8 @@ def packed_mask(kind: int, seqlens_q, seqlens_k, device, window: int = 0, bx: in
     return Mask(kind=kind, window=window, bx=bx, by=by, block_mask=block_mask,
                 cu_seqlens_q=torch.tensor(cq, dtype=torch.int32, device=device),
                 cu_seqlens_k=torch.tensor(ck, dtype=torch.int32, device=device),
-                max_seqlen_q=max(lq), max_seqlen_k=max(lk), total_q=cq[-1], total_k=ck[-1])
+                max_seqlen_q=max(lq), max_seqlen_k=max(lk), total_q=cq[-1], total_k=ck[-1],
+                first=first)
 
 
 def _ptr(t: Optional[torch.Tensor]):

@@ -58,6 +58,9 @@ attn_status_t check_shape_mask(const attn_shape_t* sh, const attn_mask_desc_t* m
     case ATTN_MASK_BLOCK:
       if (mk->bx < 1 || mk->by < 1) return ATTN_ERR_INVALID_ARG;
       break;
+    case ATTN_MASK_SLIDING_FIRST:
+      if (sh->Sq != sh->Skv || mk->window < 1 || mk->first < 0) return ATTN_ERR_INVALID_ARG;
+      break;
     default:
       return ATTN_ERR_INVALID_ARG;
   }
@@ -72,9 +75,11 @@ attn_status_t check_shape_mask(const attn_shape_t* sh, const attn_mask_desc_t* m
       return ATTN_ERR_INVALID_ARG;
   }
   if (sh->D != HEAD_DIM) return ATTN_ERR_UNSUPPORTED;
-  // the single-pass kernels have neither the compensated nor the packed form
+  // the single-pass kernels have neither the compensated nor the packed form,
+  // nor the window with first keys
   if ((sh->flags & ATTN_FLAG_SINGLE_PASS) &&
-      ((sh->flags & ATTN_FLAG_COMPENSATED) || mk->cu_seqlens_q))
+      ((sh->flags & ATTN_FLAG_COMPENSATED) || mk->cu_seqlens_q ||
+       mk->kind == ATTN_MASK_SLIDING_FIRST))
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
@@ -191,6 +196,15 @@ AttnParams params_of(const attn_shape_t* sh, const attn_mask_desc_t* mk, const W
   p.Sq_pad = d.Sq_pad;
   p.mask_kind = mk->kind;
   p.window = mk->kind == ATTN_MASK_SLIDING ? mk->window : 0;
+  if (mk->kind == ATTN_MASK_SLIDING_FIRST) {
+    // a window or first keys as long as the sequence see every earlier key;
+    // without first keys it is the plain window
+    p.window = mk->window;
+    p.first = mk->first;
+    p.mask_kind = mk->window >= sh->Sq || mk->first >= sh->Skv ? MK_CAUSAL
+                  : mk->first == 0                             ? MK_SLIDING
+                                                               : MK_FIRST;
+  }
   p.bx = mk->kind == ATTN_MASK_BLOCK ? mk->bx : 1;
   p.by = mk->kind == ATTN_MASK_BLOCK ? mk->by : 1;
   p.inv_bx = 1.0f / (float)p.bx;

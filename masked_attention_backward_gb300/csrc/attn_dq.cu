@@ -55,6 +55,8 @@
 // is spread over twice the elements).
 #include <math.h>
 
+#include <type_traits>
+
 #include "tiles.cuh"
 
 namespace mab {
@@ -115,9 +117,10 @@ struct Ring {
 };
 
 // Coordinates of work unit u: heaviest causal query tiles first.
-struct DqUnit {
+template <bool FIRST>
+struct DqUnitT {
   int bh, q0, kvh, h;
-  QWalk walk;
+  std::conditional_t<FIRST, QWalkFirst, QWalk> walk;
   // VARLEN: the call gave per-batch lengths (otherwise every batch element
   // has all Sq rows and Skv keys, and none is read)
   template <bool VARLEN>
@@ -135,8 +138,8 @@ struct DqUnit {
 
 }  // namespace dq_side
 
-// MK: the mask kind (MK_NONE, MK_CAUSAL, MK_SLIDING or MK_BLOCK); each instance keeps
-// only its own visibility code in the softmax loop (measured 1.5 to 3.5 %
+// MK: the mask kind (MK_NONE, MK_CAUSAL, MK_SLIDING, MK_BLOCK or MK_FIRST); each instance
+// keeps only its own visibility code in the softmax loop (measured 1.5 to 3.5 %
 // faster on the short-walk and variable-length workloads).
 // HILO: dS enters the dQ contraction as a 16-bit high part (columns
 // 32 g .. 32 g + 15 of group g's slice) plus a 16-bit remainder (columns
@@ -147,7 +150,8 @@ k_dq(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap
      const __grid_constant__ CUtensorMap tK, const __grid_constant__ CUtensorMap tV,
      uint16_t* __restrict__ dq, const AttnParams p) {
   using namespace dq_side;
-  constexpr bool BLOCK = MK == MK_BLOCK;
+  constexpr bool BLOCK = MK == MK_BLOCK, FIRST = MK == MK_FIRST;
+  using DqUnit = DqUnitT<FIRST>;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                      ~uintptr_t(1023));
@@ -606,7 +610,8 @@ k_dq(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap
       // keys past the batch's length are masked here; rows past its length
       // need no mask: their -lse log2 e is -inf, so their P and dS are 0
       const int Lk = VARLEN ? len_k(p, un.bh / p.Hq) : 0;
-      full_range_q(p.mask_kind, p.window, p.Sq, VARLEN ? Lk : p.Skv, un.q0, &flo, &fhi);
+      full_range_q(FIRST ? (int)MK_SLIDING : p.mask_kind, p.window, p.Sq, VARLEN ? Lk : p.Skv,
+                   un.q0, &flo, &fhi);
       for (int n = 0; ok && n < un.walk.cnt; ++n, ++m, rg.next()) {
         const int bf = m & 1, st = rg.st;
         // s_full implies the stage's loads landed; waiting on kv_full as well
@@ -619,7 +624,8 @@ k_dq(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap
         }
         const int t = s.step_t[st];
         // warp-uniform: the whole 128 x 64 sub-tile is visible
-        const bool full = !BLOCK && t >= flo && t <= fhi;  // (block masks: never)
+        bool full = !BLOCK && t >= flo && t <= fhi;  // (block masks: never)
+        if constexpr (FIRST) full = full || t <= un.walk.full_hi;
         uint32_t vis;
         if (full) {
           vis = 0xffffffffu;
@@ -741,8 +747,8 @@ cudaError_t launch_dq(bool bf16, const AttnParams& p, const CUtensorMap& tQ, con
   using Kern = decltype(&k_dq<true, false, false, MK_NONE>);
 #define MAB_DQ_ROW(BF, VL, HL)                                                                  \
   {k_dq<BF, VL, HL, MK_NONE>, k_dq<BF, VL, HL, MK_CAUSAL>, k_dq<BF, VL, HL, MK_SLIDING>,       \
-   k_dq<BF, VL, HL, MK_BLOCK>}
-  static const Kern table[2][2][2][4] = {
+   k_dq<BF, VL, HL, MK_BLOCK>, k_dq<BF, VL, HL, MK_FIRST>}
+  static const Kern table[2][2][2][5] = {
       {{MAB_DQ_ROW(false, false, false), MAB_DQ_ROW(false, false, true)},
        {MAB_DQ_ROW(false, true, false), MAB_DQ_ROW(false, true, true)}},
       {{MAB_DQ_ROW(true, false, false), MAB_DQ_ROW(true, false, true)},

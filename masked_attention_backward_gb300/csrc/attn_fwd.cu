@@ -53,6 +53,8 @@
 // lanes 32 sp .. 32 sp + 31 (query rows), grp = (warp - 3) / 4.
 #include <math.h>
 
+#include <type_traits>
+
 #include "tiles.cuh"
 
 namespace mab {
@@ -116,9 +118,10 @@ struct Cyc {
 };
 
 // Coordinates of work unit u: heaviest causal query tiles first.
-struct FwdUnit {
+template <bool FIRST>
+struct FwdUnitT {
   int bh, q0, kvh, h, Lq, Lk;  // Lq, Lk: valid rows and keys of the batch
-  QWalk walk;
+  std::conditional_t<FIRST, QWalkFirst, QWalk> walk;
   __device__ __forceinline__ void init(const AttnParams& p, int u) {
     const int BH = p.B * p.Hq;
     const int qt = p.nQT_q - 1 - u / BH;
@@ -141,13 +144,15 @@ struct FwdDone {
 }  // namespace fwd_side
 
 // PACKED: the token-major layout with cumulative sequence offsets (the BHSD
-// instance keeps its plain row addressing).
-template <bool BF16, bool PACKED>
+// instance keeps its plain row addressing).  FIRST: the sliding window with
+// first keys (the other kinds share an instance).
+template <bool BF16, bool PACKED, bool FIRST>
 __global__ void __launch_bounds__(fwd_side::NUM_THREADS, 1)
 k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
            const __grid_constant__ CUtensorMap tV, uint16_t* __restrict__ out,
            const AttnParams p) {
   using namespace fwd_side;
+  using FwdUnit = FwdUnitT<FIRST>;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                      ~uintptr_t(1023));
@@ -475,7 +480,8 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUten
       const float sink2 = p.sink ? p.sink[un.h] * LOG2E : -INFINITY;
       float M = sink2, l = 0.f;
       int flo, fhi;  // key sub-tiles that are entirely visible
-      full_range_q(p.mask_kind, p.window, un.Lq, un.Lk, un.q0, &flo, &fhi);
+      full_range_q(FIRST ? (int)MK_SLIDING : p.mask_kind, p.window, un.Lq, un.Lk, un.q0, &flo,
+                   &fhi);
       int last_bf = 0;       // buffer of this group's previous step of the unit
       uint32_t last_ph = 0;  // and the parity of its use
       for (int n = 0; ok && n < un.walk.cnt; ++n, ++m, rg.next(), bc.next()) {
@@ -496,11 +502,14 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUten
         tmem_ld32(lane_base + col + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
         const int t = s.step_t[st];
         // warp-uniform: the whole 128 x 64 sub-tile is visible
-        const bool full = t >= flo && t <= fhi;
-        const uint32_t vis0 =
-            full ? 0xffffffffu : vis_query_row(p, un.bh, i, t * Q_SUB, un.Lq, un.Lk);
-        const uint32_t vis1 =
-            full ? 0xffffffffu : vis_query_row(p, un.bh, i, t * Q_SUB + 32, un.Lq, un.Lk);
+        bool full = t >= flo && t <= fhi;
+        if constexpr (FIRST) full = full || t <= un.walk.full_hi;
+        auto row_vis = [&](int j0) -> uint32_t {
+          if constexpr (FIRST) return vis_query_row_closed<MK_FIRST>(p, i, j0, un.Lq, un.Lk);
+          else return vis_query_row(p, un.bh, i, j0, un.Lq, un.Lk);
+        };
+        const uint32_t vis0 = full ? 0xffffffffu : row_vis(t * Q_SUB);
+        const uint32_t vis1 = full ? 0xffffffffu : row_vis(t * Q_SUB + 32);
         tmem_wait_ld_regs(sv);
         // row maximum of the visible raw logits (the scale is positive, so
         // it is applied once afterwards); eight partial maxima and sums keep
@@ -593,8 +602,13 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUten
 cudaError_t launch_fwd(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
                        const CUtensorMap& tK, const CUtensorMap& tV, void* o, cudaStream_t st) {
   const bool packed = p.cu_q != nullptr;
-  auto kern = bf16 ? (packed ? k_attn_fwd<true, true> : k_attn_fwd<true, false>)
-                   : (packed ? k_attn_fwd<false, true> : k_attn_fwd<false, false>);
+  using Kern = decltype(&k_attn_fwd<true, false, false>);
+  static const Kern table[2][2][2] = {
+      {{k_attn_fwd<false, false, false>, k_attn_fwd<false, false, true>},
+       {k_attn_fwd<false, true, false>, k_attn_fwd<false, true, true>}},
+      {{k_attn_fwd<true, false, false>, k_attn_fwd<true, false, true>},
+       {k_attn_fwd<true, true, false>, k_attn_fwd<true, true, true>}}};
+  const Kern kern = table[bf16 ? 1 : 0][packed ? 1 : 0][p.mask_kind == MK_FIRST ? 1 : 0];
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)fwd_side::SMEM_BYTES);
   if (e != cudaSuccess) return e;

@@ -101,7 +101,8 @@ enum { TAG_KV = 0x201, TAG_Q_EMPTY = 0x203, TAG_Q_FULL, TAG_S_FREE, TAG_P_FULL, 
 // own columns.
 // PACKED: the token-major layout with cumulative sequence offsets (the BHSD
 // instances keep their plain row addressing).
-template <bool BF16, bool HILO, bool PACKED>
+// FIRST: the sliding window with first keys (the other kinds share an instance).
+template <bool BF16, bool HILO, bool PACKED, bool FIRST>
 __global__ void __launch_bounds__(kv_side::NUM_THREADS, 1)
 k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tdO,
        const __grid_constant__ CUtensorMap tK, const __grid_constant__ CUtensorMap tV,
@@ -342,7 +343,10 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
       if (lane == 0) mbar_arrive(smem_u32(bar));
     };
     int flo, fhi;  // query sub-tiles that are entirely visible
-    full_range_kv(p.mask_kind, p.window, Lq, Lk, k0, &flo, &fhi);
+    full_range_kv(!FIRST                   ? p.mask_kind
+                  : k0 + KV_TILE <= p.first ? (int)MK_CAUSAL
+                                            : (int)MK_SLIDING,
+                  p.window, Lq, Lk, k0, &flo, &fhi);
     for (int n = 0; ok && n < N; ++n) {
       const int st = n % NST, bf = n & 1;
       const uint32_t colS = COL_BUF + 128 * bf + 16 * g;  // this warp's S^T / P^T columns
@@ -367,6 +371,8 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
         vis = ((s.step_vis[st] >> (4 * sp + g)) & 1u) && j < Lk
                   ? bit_range(0, Lq - 1 - (r * KV_SUB + 16 * g))
                   : 0u;
+      } else if constexpr (FIRST) {
+        vis = vis_key_row_closed<MK_FIRST>(p, j, r * KV_SUB + 16 * g, Lq, Lk);
       } else {
         vis = vis_key_row(p, b * p.Hq + c * p.group + s.step_hh[st], j, r * KV_SUB + 16 * g, Lq,
                           Lk);
@@ -458,7 +464,7 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
 // 64 steps at the full lengths -- where a CTA per unit would spend much of
 // its time starting and storing.  On long walks the per-tile grid is faster.
 static bool use_units(const AttnParams& p) {
-  if (p.cu_q) return false;
+  if (p.cu_q || p.mask_kind == MK_FIRST) return false;
   if (p.kv_schedule != 0) return p.kv_schedule == 2;
   const long long units = (long long)p.nKT_k * p.B * p.Hkv;
   if (units < 2LL * (p.num_sms > 0 ? p.num_sms : 1)) return false;
@@ -475,13 +481,15 @@ cudaError_t launch_dkdv(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
                         const CUtensorMap& tdO, const CUtensorMap& tK, const CUtensorMap& tV,
                         void* dk, void* dv, cudaStream_t st) {
   if (use_units(p)) return launch_dkdv_units(bf16, p, tQ, tdO, tK, tV, dk, dv, st);
-  using Kern = decltype(&k_dkdv<true, false, false>);
-  static const Kern table[2][2][2] = {
-      {{k_dkdv<false, false, false>, k_dkdv<false, false, true>},
-       {k_dkdv<false, true, false>, k_dkdv<false, true, true>}},
-      {{k_dkdv<true, false, false>, k_dkdv<true, false, true>},
-       {k_dkdv<true, true, false>, k_dkdv<true, true, true>}}};
-  const Kern kern = table[bf16 ? 1 : 0][p.compensated ? 1 : 0][p.cu_q ? 1 : 0];
+  using Kern = decltype(&k_dkdv<true, false, false, false>);
+#define MAB_KV_ROW(BF, HL)                                           \
+  {{k_dkdv<BF, HL, false, false>, k_dkdv<BF, HL, false, true>},      \
+   {k_dkdv<BF, HL, true, false>, k_dkdv<BF, HL, true, true>}}
+  static const Kern table[2][2][2][2] = {{MAB_KV_ROW(false, false), MAB_KV_ROW(false, true)},
+                                         {MAB_KV_ROW(true, false), MAB_KV_ROW(true, true)}};
+#undef MAB_KV_ROW
+  const Kern kern = table[bf16 ? 1 : 0][p.compensated ? 1 : 0][p.cu_q ? 1 : 0]
+                         [p.mask_kind == MK_FIRST ? 1 : 0];
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kv_side::SMEM_BYTES);
   if (e != cudaSuccess) return e;

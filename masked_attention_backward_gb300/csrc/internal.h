@@ -21,7 +21,11 @@ constexpr int PREP_ROWS = 128;  // padding unit of the per-row statistics
 constexpr int PREP_BLOCK_ROWS = 64;  // rows per preprocess block (divides PREP_ROWS)
 constexpr float LOG2E = 1.4426950408889634f;
 
-enum MaskKind { MK_NONE = 0, MK_CAUSAL = 1, MK_SLIDING = 2, MK_BLOCK = 3 };
+// MK_FIRST: the sliding window whose first `first` keys stay visible
+// (0 <= i - j < window, or j <= i and j < first).  The host turns the cases
+// that another kind covers into that kind, so that 1 <= first < Skv and
+// 1 <= window < Sq hold for it.
+enum MaskKind { MK_NONE = 0, MK_CAUSAL = 1, MK_SLIDING = 2, MK_BLOCK = 3, MK_FIRST = 4 };
 
 // Byte offsets of the workspace regions (each 256-byte aligned).
 struct WsLayout {
@@ -86,6 +90,7 @@ struct AttnParams {
   float* dq_part;
   uint8_t* dq_flag;
   long long dq_steps_head;  // slots per query head
+  int first;  // MK_FIRST: keys j < first stay visible to every later query
 };
 
 #ifdef __CUDACC__

@@ -87,6 +87,8 @@ __device__ __forceinline__ uint32_t vis_key_row_closed(const AttnParams& p, int 
   const uint32_t inrange = bit_range(0, Lq - 1 - i0);
   if constexpr (MK == MK_NONE) return inrange;
   else if constexpr (MK == MK_CAUSAL) return inrange & bit_range(j - i0, 31);
+  else if constexpr (MK == MK_FIRST)
+    return inrange & bit_range(j - i0, j < p.first ? 31 : j + p.window - 1 - i0);
   else return inrange & bit_range(j - i0, j + p.window - 1 - i0);
 }
 // The closed-form half of vis_query_row, for instances that know the mask
@@ -98,6 +100,9 @@ __device__ __forceinline__ uint32_t vis_query_row_closed(const AttnParams& p, in
   const uint32_t inrange = bit_range(0, Lk - 1 - j0);
   if constexpr (MK == MK_NONE) return inrange;
   else if constexpr (MK == MK_CAUSAL) return inrange & bit_range(0, i - j0);
+  else if constexpr (MK == MK_FIRST)
+    return inrange & bit_range(0, i - j0) &
+           (bit_range(i - p.window + 1 - j0, 31) | bit_range(0, p.first - 1 - j0));
   else return inrange & bit_range(i - p.window + 1 - j0, i - j0);
 }
 
@@ -173,6 +178,30 @@ struct QWalk {
   __device__ __forceinline__ int tile(int n) const { return list ? list[n] : lo + n; }
 };
 
+// The same walk under MK_FIRST: the key sub-tiles that hold the first keys,
+// then the window's (those from `lo` on, which may begin among the first
+// ones).  Sub-tiles t <= full_hi lie wholly among the first keys and before
+// every query of the tile.
+struct QWalkFirst {
+  int lo, cnt, nfirst, full_hi;
+  __device__ __forceinline__ void init(const AttnParams& p, int, int qt, int Lq, int Lk) {
+    const int q0 = qt * Q_TILE;
+    lo = cnt = nfirst = 0;
+    full_hi = -1;
+    if (q0 >= Lq || Lk <= 0) return;
+    int hi;
+    partner_range(MK_SLIDING, p.window, true, q0, min(q0 + Q_TILE, Lq), Q_SUB, Lk, &lo, &hi);
+    if (hi < lo) {  // every key of the batch lies before the window
+      lo = (Lk + Q_SUB - 1) / Q_SUB;
+      hi = lo - 1;
+    }
+    nfirst = min((min(p.first, Lk) + Q_SUB - 1) / Q_SUB, lo);
+    cnt = nfirst + hi - lo + 1;
+    if (q0 + Q_TILE <= Lq) full_hi = min(min(p.first, Lk), q0 + 1) / Q_SUB - 1;
+  }
+  __device__ __forceinline__ int tile(int n) const { return n < nfirst ? n : lo + n - nfirst; }
+};
+
 // Walk of a key-tile CTA (KV_TILE rows of kv head (b, c)) over (query head of
 // the group, query sub-tile of KV_SUB rows) pairs, head-major; Lq, Lk are the
 // valid rows and keys of batch b (a tile that starts past Lk walks nothing).
@@ -191,8 +220,11 @@ struct KVWalk {
     none = k0 >= Lk || Lq <= 0;
     if (!none && p.mask_kind != MK_BLOCK) {
       int hi;
-      partner_range(p.mask_kind, p.window, false, k0, min(k0 + KV_TILE, Lk), KV_SUB, Lq, &lo,
-                    &hi);
+      // a tile that holds first keys meets every later query
+      const int kind = p.mask_kind != MK_FIRST ? p.mask_kind
+                       : k0 < p.first          ? (int)MK_CAUSAL
+                                               : (int)MK_SLIDING;
+      partner_range(kind, p.window, false, k0, min(k0 + KV_TILE, Lk), KV_SUB, Lq, &lo, &hi);
       cnt_closed = hi - lo + 1;
       if (cnt_closed < 0) cnt_closed = 0;
     }
