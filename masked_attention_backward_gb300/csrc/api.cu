@@ -98,6 +98,14 @@ long long single_pass_steps_head(const attn_shape_t* sh, const attn_mask_desc_t*
   return n;
 }
 
+// The kernels' mask kind.  A window or first keys as long as the sequence see
+// every earlier key; without first keys the mask is the plain window.
+int mask_kind_of(const attn_shape_t* sh, const attn_mask_desc_t* mk) {
+  if (mk->kind != ATTN_MASK_SLIDING_FIRST) return mk->kind;
+  if (mk->window >= sh->Sq || mk->first >= sh->Skv) return MK_CAUSAL;
+  return mk->first == 0 ? MK_SLIDING : MK_FIRST;
+}
+
 struct Dims {
   int Sq_pad, nqb, nkb, nQT_k, nKT_k, nQT_q, nKT_q, nparts;
 };
@@ -141,6 +149,17 @@ WsLayout layout_of(const attn_shape_t* sh, const attn_mask_desc_t* mk) {
     off = align256(off + BH * d.nQT_q * d.nKT_q * sizeof(int));
     L.cnt_q = off;
     off = align256(off + BH * d.nQT_q * sizeof(int));
+  }
+  L.first_ticket = L.first_part = off;
+  if (mk->kind == ATTN_MASK_SLIDING_FIRST && mask_kind_of(sh, mk) == MK_FIRST) {
+    const size_t pieces = kv_first_pieces(sh->B, sh->Hq, sh->Hkv, sh->Sq, mk->first);
+    if (pieces > 1) {
+      const size_t units = (size_t)kv_first_tiles(mk->first) * sh->B * sh->Hkv;
+      L.first_ticket = off;
+      off = align256(off + units * KV_FIRST_WARPS * sizeof(int));
+      L.first_part = off;
+      off = align256(off + units * pieces * KV_FIRST_PIECE_FLOATS * sizeof(float));
+    }
   }
   L.dq_flag = L.dq_part = off;
   if (sh->flags & ATTN_FLAG_SINGLE_PASS) {
@@ -194,16 +213,11 @@ AttnParams params_of(const attn_shape_t* sh, const attn_mask_desc_t* mk, const W
   p.Skv = sh->Skv;
   p.group = sh->Hq / sh->Hkv;
   p.Sq_pad = d.Sq_pad;
-  p.mask_kind = mk->kind;
   p.window = mk->kind == ATTN_MASK_SLIDING ? mk->window : 0;
+  p.mask_kind = mask_kind_of(sh, mk);
   if (mk->kind == ATTN_MASK_SLIDING_FIRST) {
-    // a window or first keys as long as the sequence see every earlier key;
-    // without first keys it is the plain window
     p.window = mk->window;
     p.first = mk->first;
-    p.mask_kind = mk->window >= sh->Sq || mk->first >= sh->Skv ? MK_CAUSAL
-                  : mk->first == 0                             ? MK_SLIDING
-                                                               : MK_FIRST;
   }
   p.bx = mk->kind == ATTN_MASK_BLOCK ? mk->bx : 1;
   p.by = mk->kind == ATTN_MASK_BLOCK ? mk->by : 1;
@@ -236,6 +250,11 @@ AttnParams params_of(const attn_shape_t* sh, const attn_mask_desc_t* mk, const W
     p.dq_part = reinterpret_cast<float*>(ws + L.dq_part);
     p.dq_flag = ws + L.dq_flag;
     p.dq_steps_head = single_pass_steps_head(sh, mk);
+  }
+  if (L.first_part != L.first_ticket) {
+    p.first_parts = kv_first_pieces(sh->B, sh->Hq, sh->Hkv, sh->Sq, mk->first);
+    p.first_part = reinterpret_cast<float*>(ws + L.first_part);
+    p.first_ticket = reinterpret_cast<int*>(ws + L.first_ticket);
   }
   p.seqlen_q = mk->seqlen_q;
   p.seqlen_k = mk->seqlen_k;
@@ -441,6 +460,7 @@ attn_status_t attn_bwd(const attn_shape_t* shape, const void* q, const void* k, 
                           reinterpret_cast<float*>(w + L.dsink_part), shape->B, shape->Hq,
                           shape->Sq, d.Sq_pad, mask->seqlen_q, mask->cu_seqlens_q,
                           mask->total_q, reinterpret_cast<DevStatus*>(w + L.status),
+                          p.first_ticket, p.first_ticket ? (int)((L.first_part - L.first_ticket) / 4) : 0,
                           blk && !prof, st);
   }
   if (e == cudaSuccess && single) {
@@ -459,12 +479,26 @@ attn_status_t attn_bwd(const attn_shape_t* shape, const void* q, const void* k, 
       p.dsink_part = reinterpret_cast<const float*>(w + L.dsink_part);
       p.dsink_nparts = d.nparts;
     }
-    {
+    if (p.mask_kind == MK_FIRST) {
+      // the tiles that hold first keys, then the others under the plain window
+      const int tile0 = kv_first_tiles(p.first);
+      AttnParams pf = p;
+      if (tile0 < p.nKT_k) pf.dsink = nullptr;  // the last grid sums it
+      {
+        ProfScope ps(prof, "k_dkdv_first", st);
+        e = launch_dkdv_first(bf16, pf, tQs, tdOs, tKt, tVt, dk, dv, st);
+      }
+      p.mask_kind = MK_SLIDING;
+      p.kv_tile0 = tile0;
+      p.after_first = 1;
+    }
+    if (e == cudaSuccess && p.kv_tile0 < p.nKT_k) {
       ProfScope ps(prof, "k_dkdv", st);
       e = launch_dkdv(bf16, p, tQs, tdOs, tKt, tVt, dk, dv, st);
     }
     if (e == cudaSuccess) {
       ProfScope ps(prof, "k_dq", st);
+      if (p.after_first) p.mask_kind = MK_FIRST;
       e = launch_dq(bf16, p, tQt, tdOt, tKs, tVs, dq, st);
     }
   }

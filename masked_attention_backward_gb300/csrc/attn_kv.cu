@@ -114,8 +114,11 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
                                      ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int BHkv = p.B * p.Hkv;
-  const int t = (int)(blockIdx.x / BHkv);  // low key tiles (longest causal walks) first
-  const int bc = (int)(blockIdx.x % BHkv);
+  // FIRST: the tiles that hold first keys, each walk in first_parts pieces
+  const int parts = FIRST ? max(p.first_parts, 1) : 1;
+  const int unit = (int)blockIdx.x / parts;
+  const int t = unit / BHkv + p.kv_tile0;  // low key tiles (longest causal walks) first
+  const int bc = unit % BHkv;
   const int b = bc / p.Hkv, c = bc % p.Hkv;
   const int k0 = t * KV_TILE;
   const int Lq = len_q(p, b), Lk = len_k(p, b);  // valid rows and keys of the batch
@@ -124,7 +127,16 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
   if (p.mask_kind == MK_BLOCK) grid_dependency_wait();
   KVWalk walk;
   walk.init(p, b, c, t, Lq, Lk);
-  const int N = walk.total(p);
+  int N = walk.total(p);
+  // this CTA's steps of the walk, [n0, n0 + N); pieces that a shorter batch
+  // does not need stay empty and store nothing
+  int n0 = 0, used = 1;
+  const int piece = FIRST ? (int)blockIdx.x % parts : 0;
+  if constexpr (FIRST) {
+    used = min(parts, max(N / KV_FIRST_STEPS, 1));
+    n0 = piece < used ? (int)((long long)N * piece / used) : 0;
+    N = piece < used ? (int)((long long)N * (piece + 1) / used) - n0 : 0;
+  }
   // a block mask whose blocks hold whole softmax-warp regions (32 keys x 16
   // queries): each region is visible entirely or not at all
   const bool blk_regions = p.mask_kind == MK_BLOCK && (p.by & 31) == 0 && (p.bx & 15) == 0;
@@ -176,7 +188,9 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
   // of its results are read (block masks waited above already).  Only then let the dQ
   // kernel that follows start (it needs nothing from this grid, but reads the
   // preprocess results): it may take the SMs this grid's last CTAs leave idle.
-  grid_dependency_wait();
+  // Behind the first-key tiles' grid nothing of that one is read, and it
+  // waited for the preprocess kernel before it let this one start.
+  if (!p.after_first) grid_dependency_wait();
   grid_launch_dependents();
 
   if (warp == 0) {
@@ -190,7 +204,7 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
       // SM) into L2 now, so that its first wait is for L2 rather than HBM
       const int succ = (int)blockIdx.x + p.num_sms;
       if (N <= 64 && succ < (int)gridDim.x) {
-        const int t2 = succ / BHkv, bc2 = succ % BHkv;
+        const int t2 = succ / parts / BHkv + p.kv_tile0, bc2 = succ / parts % BHkv;
         const RowAddr a2 = PACKED ? row_k(p, bc2 / p.Hkv, bc2 % p.Hkv, t2 * KV_TILE)
                                   : RowAddr{t2 * KV_TILE, bc2, 0, HEAD_DIM};
         tma_prefetch_l2_3d(&tK, 0, a2.c1, a2.c2);
@@ -200,6 +214,12 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
       }
       KVCursor cur;
       cur.start(p, walk);
+      if constexpr (FIRST) {
+        if (N > 0) {
+          cur.hh = n0 / walk.cnt_closed;
+          cur.idx = n0 % walk.cnt_closed;
+        }
+      }
       int issued = 0;  // steps whose loads were issued
       for (int n = 0; n < N; ++n) {
         const int st = n % NST;
@@ -360,7 +380,7 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
       }
       tc_fence_after();
       float sv[16];
-      tmem_ld16(lane_base + colS, sv);
+      if constexpr (!FIRST) tmem_ld16(lane_base + colS, sv);
       const int r = s.step_r[st];
       // warp-uniform: the whole 64 x 128 sub-tile is visible
       const bool full = r >= flo && r <= fhi;
@@ -377,11 +397,19 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
         vis = vis_key_row(p, b * p.Hq + c * p.group + s.step_hh[st], j, r * KV_SUB + 16 * g, Lq,
                           Lk);
       }
-      float lv[16];
-      load16_shared(&s.nlse2[st][16 * g], lv);
-      tmem_wait_ld_regs(sv);
+      // no logit of the warp's region is visible (most of a first-key tile's
+      // rows against the queries past their window): P^T and dS^T are zero
+      const bool none = FIRST && !full && __all_sync(0xffffffffu, vis == 0u);
       float pv[16];
-      kv_write_p<BF16, HILO>(lane_base + colS, sv, lv, full, vis, p.scale_log2, pv);
+      if (none) {
+        kv_write_zero<HILO>(lane_base + colS);
+      } else {
+        if constexpr (FIRST) tmem_ld16(lane_base + colS, sv);
+        float lv[16];
+        load16_shared(&s.nlse2[st][16 * g], lv);
+        tmem_wait_ld_regs(sv);
+        kv_write_p<BF16, HILO>(lane_base + colS, sv, lv, full, vis, p.scale_log2, pv);
+      }
       warp_arrive(&s.bar_p_full[bf]);
 
       // ---- dS^T(n) = P^T(n) (dP^T(n) - Delta)
@@ -392,11 +420,15 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
         break;
       }
       tc_fence_after();
-      float dp[16];
-      tmem_ld16(lane_base + colS + 64, dp);
-      tmem_wait_ld_regs(dp);
-      uint32_t pk[8];
-      kv_write_ds<BF16, HILO>(lane_base + colS + 64, pv, dp, dl, pk);
+      if (none) {
+        kv_write_zero<HILO>(lane_base + colS + 64);
+      } else {
+        float dp[16];
+        tmem_ld16(lane_base + colS + 64, dp);
+        tmem_wait_ld_regs(dp);
+        uint32_t pk[8];
+        kv_write_ds<BF16, HILO>(lane_base + colS + 64, pv, dp, dl, pk);
+      }
       warp_arrive(&s.bar_ds_full[bf]);
     }
     // ---------------------------------------------------------- epilogue
@@ -415,8 +447,42 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
                               : RowAddr{r0, bc, ((size_t)bc * p.Skv + r0) * HEAD_DIM, HEAD_DIM};
     uint8_t* stage = s.Q[0] + (warp - SM_WARP0) * 2048;
     const bool staged = __all_sync(0xffffffffu, have || (ok && N == 0));
+    // A piece of a split walk leaves its fp32 sums in the workspace, and the
+    // last piece to finish adds them up, in the pieces' order whichever it is
+    // (each warp for its own 32 rows and 32 columns: no barrier between
+    // warps).  It stores the sum below; the other pieces store nothing.
+    bool store = true;
+    const float* parts0 = nullptr;  // piece 0's sums of this warp's rows and columns
+    if constexpr (FIRST) {
+      if (piece >= used) {
+        store = false;
+      } else if (used > 1) {
+        const int w = warp - SM_WARP0;
+        float* mine = p.first_part + ((size_t)unit * parts + piece) * KV_FIRST_PIECE_FLOATS +
+                      w * (KV_FIRST_PIECE_FLOATS / KV_FIRST_WARPS) + lane;
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {  // 0: dV, 1: dK
+        for (int which = 0; which < 2; ++which) {
+          float v[32];
+#pragma unroll
+          for (int cc = 0; cc < 32; ++cc) v[cc] = 0.f;
+          if (have) {
+            tmem_ld32(lane_base + (which ? COL_DK : COL_DV) + 32 * g, v);
+            tmem_wait_ld_regs(v);
+          }
+#pragma unroll
+          for (int cc = 0; cc < 32; ++cc) mine[which * 1024 + cc * 32] = v[cc];
+        }
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(p.first_ticket + unit * KV_FIRST_WARPS + w, 1);
+        store = __shfl_sync(0xffffffffu, before, 0) == used - 1;
+        __threadfence();
+        parts0 = mine - (size_t)piece * KV_FIRST_PIECE_FLOATS;
+      }
+    }
+#pragma unroll 1
+    for (int which = 0; which < 2 && store; ++which) {  // 0: dV, 1: dK
       uint16_t* base = which ? dk : dv;
       uint16_t* orow = base + oa.elem + 32 * g;
       if (!staged) {
@@ -427,8 +493,18 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
       if (have) {
         const float sc = which ? p.scale : 1.f;
         float v[32];
-        tmem_ld32(lane_base + (which ? COL_DK : COL_DV) + 32 * g, v);
-        tmem_wait_ld_regs(v);
+        if (FIRST && parts0) {
+#pragma unroll
+          for (int cc = 0; cc < 32; ++cc) v[cc] = 0.f;
+          for (int i = 0; i < used; ++i) {
+            const float* src = parts0 + (size_t)i * KV_FIRST_PIECE_FLOATS + which * 1024;
+#pragma unroll
+            for (int cc = 0; cc < 32; ++cc) v[cc] += __ldcg(src + cc * 32);
+          }
+        } else {
+          tmem_ld32(lane_base + (which ? COL_DK : COL_DV) + 32 * g, v);
+          tmem_wait_ld_regs(v);
+        }
 #pragma unroll
         for (int cc = 0; cc < 16; ++cc) pk[cc] = pack2<BF16>(v[2 * cc] * sc, v[2 * cc + 1] * sc);
       } else {
@@ -456,6 +532,9 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
         if (lane == 0) p.dsink[h] = v;
       }
   }
+  // launched over the first-key tiles' grid: this one does not complete
+  // before that one has
+  if (p.after_first && blockIdx.x == 0 && threadIdx.x == 0) grid_dependency_wait();
 }
 
 // Whether the persistent form (attn_kv_units.cu) runs the dK/dV walk: for the
@@ -464,23 +543,23 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
 // 64 steps at the full lengths -- where a CTA per unit would spend much of
 // its time starting and storing.  On long walks the per-tile grid is faster.
 static bool use_units(const AttnParams& p) {
-  if (p.cu_q || p.mask_kind == MK_FIRST) return false;
+  if (p.cu_q) return false;
   if (p.kv_schedule != 0) return p.kv_schedule == 2;
-  const long long units = (long long)p.nKT_k * p.B * p.Hkv;
+  const long long units = (long long)(p.nKT_k - p.kv_tile0) * p.B * p.Hkv;
   if (units < 2LL * (p.num_sms > 0 ? p.num_sms : 1)) return false;
   if (p.mask_kind == MK_BLOCK) return true;
   long long steps = 0;
-  for (int t = 0; t < p.nKT_k; ++t) {
+  for (int t = p.kv_tile0; t < p.nKT_k; ++t) {
     int lo;
     steps += kv_tile_range_full(p.mask_kind, p.window, p.Sq, p.Skv, t, &lo);
   }
-  return steps * p.group <= 64LL * p.nKT_k;
+  return steps * p.group <= 64LL * (p.nKT_k - p.kv_tile0);
 }
 
-cudaError_t launch_dkdv(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
-                        const CUtensorMap& tdO, const CUtensorMap& tK, const CUtensorMap& tV,
-                        void* dk, void* dv, cudaStream_t st) {
-  if (use_units(p)) return launch_dkdv_units(bf16, p, tQ, tdO, tK, tV, dk, dv, st);
+static cudaError_t launch_tiles(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
+                                const CUtensorMap& tdO, const CUtensorMap& tK,
+                                const CUtensorMap& tV, void* dk, void* dv, int grid,
+                                cudaStream_t st) {
   using Kern = decltype(&k_dkdv<true, false, false, false>);
 #define MAB_KV_ROW(BF, HL)                                           \
   {{k_dkdv<BF, HL, false, false>, k_dkdv<BF, HL, false, true>},      \
@@ -493,12 +572,11 @@ cudaError_t launch_dkdv(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kv_side::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int nKT = (p.Skv + KV_TILE - 1) / KV_TILE;
   // programmatic stream serialization behind the preprocess kernel, so that
   // this grid's launch and (closed-form masks) set-up and K / V loads overlap
   // its tail; block-mask CTAs wait for it before they read the select tables
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(nKT * p.B * p.Hkv));
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kv_side::NUM_THREADS);
   cfg.dynamicSmemBytes = kv_side::SMEM_BYTES;
   cfg.stream = st;
@@ -508,6 +586,21 @@ cudaError_t launch_dkdv(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, tQ, tdO, tK, tV, (uint16_t*)dk, (uint16_t*)dv, p);
+}
+
+cudaError_t launch_dkdv(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
+                        const CUtensorMap& tdO, const CUtensorMap& tK, const CUtensorMap& tV,
+                        void* dk, void* dv, cudaStream_t st) {
+  if (use_units(p)) return launch_dkdv_units(bf16, p, tQ, tdO, tK, tV, dk, dv, st);
+  return launch_tiles(bf16, p, tQ, tdO, tK, tV, dk, dv, (p.nKT_k - p.kv_tile0) * p.B * p.Hkv, st);
+}
+
+cudaError_t launch_dkdv_first(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
+                              const CUtensorMap& tdO, const CUtensorMap& tK,
+                              const CUtensorMap& tV, void* dk, void* dv, cudaStream_t st) {
+  return launch_tiles(bf16, p, tQ, tdO, tK, tV, dk, dv,
+                      kv_first_tiles(p.first) * p.B * p.Hkv * (p.first_parts > 1 ? p.first_parts : 1),
+                      st);
 }
 
 }  // namespace mab

@@ -100,7 +100,7 @@ struct KvUnit {
   KVWalk walk;
   __device__ __forceinline__ void init(const AttnParams& p, int u) {
     const int BHkv = p.B * p.Hkv;
-    t = u / BHkv;
+    t = u / BHkv + p.kv_tile0;
     bc = u % BHkv;
     b = bc / p.Hkv;
     c = bc % p.Hkv;
@@ -111,17 +111,6 @@ struct KvUnit {
     N = walk.total(p);
   }
 };
-
-// Zero P^T (or dS^T) of a softmax warp's 16 columns at TMEM address `taddr`
-// (and, compensated, a zero remainder over the next 8), then waits for the
-// store: the packed values of a region none of whose logits is visible.
-template <bool HILO>
-__device__ __forceinline__ void kv_write_zero(uint32_t taddr) {
-  const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-  tmem_st8(taddr, z);
-  if constexpr (HILO) tmem_st8(taddr + 8, z);
-  tmem_wait_st();
-}
 
 }  // namespace kvu_side
 
@@ -140,7 +129,7 @@ k_dkdv_units(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUt
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                      ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int U = p.nKT_k * p.B * p.Hkv;
+  const int U = (p.nKT_k - p.kv_tile0) * p.B * p.Hkv;
   const bool blk_regions = BLOCK && (p.by & 31) == 0 && (p.bx & 15) == 0;
   WaitCtx wc{p.status, &s.abort_flag, p.timeout_ns};
 
@@ -184,7 +173,9 @@ k_dkdv_units(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUt
   // any of their results is read; then let the dQ kernel behind this one be
   // scheduled (its CTAs take the SMs this grid's CTAs leave when no unit is
   // left).
-  grid_dependency_wait();
+  // Behind the first-key tiles' kernel nothing of that one is read, and it
+  // waited for the preprocess kernel before it let this one start.
+  if (!p.after_first) grid_dependency_wait();
   grid_launch_dependents();
 
   // Every warp but the producer takes each published unit in order: it waits
@@ -615,6 +606,9 @@ k_dkdv_units(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUt
         if (lane == 0) p.dsink[h] = v;
       }
   }
+  // launched over the first-key tiles' kernel: this grid does not complete
+  // before that one has
+  if (p.after_first && blockIdx.x == 0 && threadIdx.x == 0) grid_dependency_wait();
 }
 
 cudaError_t launch_dkdv_units(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
@@ -631,7 +625,7 @@ cudaError_t launch_dkdv_units(bool bf16, const AttnParams& p, const CUtensorMap&
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kvu_side::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int units = p.nKT_k * p.B * p.Hkv;
+  const int units = (p.nKT_k - p.kv_tile0) * p.B * p.Hkv;
   const int sms = p.num_sms > 0 ? p.num_sms : 1;
   // programmatic stream serialization behind the preprocess kernel: this
   // grid's launch and set-up overlap its tail

@@ -98,4 +98,15 @@ __device__ __forceinline__ void kv_write_ds(uint32_t taddr, const float (&pv)[16
   tmem_wait_st();
 }
 
+// Zero P^T (or dS^T) of a softmax warp's 16 columns at TMEM address `taddr`
+// (and, compensated, a zero remainder over the next 8), then waits for the
+// store: the packed values of a region none of whose logits is visible.
+template <bool HILO>
+__device__ __forceinline__ void kv_write_zero(uint32_t taddr) {
+  const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  tmem_st8(taddr, z);
+  if constexpr (HILO) tmem_st8(taddr + 8, z);
+  tmem_wait_st();
+}
+
 }  // namespace mab

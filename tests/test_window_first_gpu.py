@@ -192,3 +192,62 @@ def test_backward_against_differences(cuda_lib):
         # output are each rounded to within 2^-11), and e . d with a normal d is normal with the
         # deviation |e|: six of those, and the differences' own truncation
         assert abs(got - want) <= 6 * 2.0 ** -9 * float(grad.double().norm()) + 1e-5 * abs(want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,window,first", [(8, 1, 100, 130), (16, 2, 64, 1)])
+def test_first_key_tiles_in_many_pieces(cuda_lib, Hq, Hkv, window, first):
+    # walks of 256 steps in up to 16 pieces; in the second call a batch element that needs fewer
+    # pieces than the grid has, and one that needs none
+    S = 2048
+    q, k, v, dO, sk = _inputs(1, Hq, Hkv, S, BF16, True, 14)
+    mask = mab.Mask(kind=mab.ATTN_MASK_SLIDING_FIRST, window=window, first=first)
+    _check(*_step(q, k, v, dO, sk, mask), q, k, v, dO, sk, _vis(S, window, first))
+    lens = [700, 0, 129]
+    q, k, v, dO, sk = _inputs(3, Hq, Hkv, S, F16, True, 15)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    mask = mab.Mask(kind=mab.ATTN_MASK_SLIDING_FIRST, window=window, first=first, seqlen_q=ln,
+                    seqlen_k=ln)
+    o, lse, grads = _step(q, k, v, dO, sk, mask)
+    lv = (torch.arange(S, device="cuda")[None, :] < ln[:, None])[:, None, :].expand(lse.shape)
+    ref = attn64.backward(q, k, v, o, dO, torch.where(lv, lse, 0.0), _vis(S, window, first, lens),
+                          sk, SCALE)
+    for n, x in zip(("dq", "dk", "dv", "dsink"), grads):
+        attn64.check(n, x, *ref[n])
+
+
+def test_captured_backward_replays(cuda_lib):
+    S = 1500
+    q, k, v, dO, sk = _inputs(1, 8, 2, S, BF16, True, 16)
+    mask = mab.Mask(kind=mab.ATTN_MASK_SLIDING_FIRST, window=128, first=10)
+    o, lse = mab.fwd(q, k, v, sk, mask, SCALE)
+    ws = mab.workspace(mab.shape_of(q, k), mask, "cuda")
+    want = mab.bwd(q, k, v, o, dO, lse, sk, mask, SCALE, ws=ws)
+    out = tuple(torch.empty_like(x) for x in want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mab.bwd(q, k, v, o, dO, lse, sk, mask, SCALE, ws=ws, out=out)
+    for _ in range(3):
+        for x in out:
+            x.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_wait_that_runs_out_is_reported(cuda_lib, monkeypatch):
+    S = 1100
+    q, k, v, dO, sk = _inputs(1, 8, 1, S, BF16, True, 17)
+    mask = mab.Mask(kind=mab.ATTN_MASK_SLIDING_FIRST, window=128, first=10)
+    o, lse = mab.fwd(q, k, v, sk, mask, SCALE)
+    ws = mab.workspace(mab.shape_of(q, k), mask, "cuda")
+    want = mab.bwd(q, k, v, o, dO, lse, sk, mask, SCALE, ws=ws)
+    monkeypatch.setenv("MASKATTN_TEST_NO_LOADS", "1")
+    monkeypatch.setenv("MASKATTN_WAIT_TIMEOUT_NS", "20000000")
+    mab.bwd(q, k, v, o, dO, lse, sk, mask, SCALE, ws=ws)
+    assert mab.device_status(ws) == mab.ATTN_ERR_TIMEOUT
+    monkeypatch.delenv("MASKATTN_TEST_NO_LOADS")
+    monkeypatch.delenv("MASKATTN_WAIT_TIMEOUT_NS")
+    got = mab.bwd(q, k, v, o, dO, lse, sk, mask, SCALE, ws=ws)
+    assert mab.device_status(ws) == mab.ATTN_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
