@@ -203,6 +203,81 @@ attn_status_t attn_bwd_noalloc(const attn_shape_t* shape, const void* q, const v
                                const float* sink, const attn_mask_desc_t* mask, float scale,
                                void* dq, void* dk, void* dv, float* dsink, void* stream);
 
+/* ---- paged key/value cache (serving) ----
+ *
+ * A cache holds `num_pages` pages of `page_size` tokens for each of K and V.
+ * Request b's token at position x lives in row x % page_size of page
+ * block_table[b, x / page_size]; its slot is page * page_size + row.  The
+ * K and the V pages are two device tensors of the same strides (in elements):
+ * element (page, kv head, row, d) is at page * page_stride + head * head_stride
+ * + row * token_stride + d, so that [pages, Hkv, page_size, 128],
+ * [pages, page_size, Hkv, 128] and both halves of one interleaved tensor are
+ * all described.  Strides are at least 128 and multiples of 8; page_size is a
+ * multiple of 16 up to 65536; num_pages * page_size < 2^31. */
+typedef struct {
+  int num_pages, page_size, Hkv;
+  int dtype; /* attn_dtype_t */
+  long long page_stride, head_stride, token_stride;
+} attn_pages_t;
+
+/* One step's page planning, from request lengths on the device: which pages
+ * the new tokens get, and where each token goes.  Every pointer is a device
+ * pointer; nothing is read back to the host, so the call can be captured.
+ *
+ *   cached[b]      tokens of request b in the cache before the step
+ *   fresh[b]       its new tokens of this step; negative: the request has ended
+ *   free_pages     [num_pages] stack of free pages, of which the first
+ *                  *free_count are free (the top is the last of them)
+ *   block_table    [B, max_pages], rows table_stride apart
+ *
+ * In request order, ended requests first put their ceil(cached / page_size)
+ * pages on the stack; then every other request takes the pages that its new
+ * tokens need from the top, appended to its row of the table.  Written:
+ *
+ *   cu_seqlens_q   [B + 1] offsets of the requests' new tokens (ended: none)
+ *   seqlen_k       [B] cached + fresh; 0 for ended requests
+ *   free_count_out [1] free pages left
+ *   slot_map       [max_tokens] int64: each new token's slot, -1 past the last
+ *   position       [max_tokens] its position in its request, -1 past the last
+ *   refused        [1] requests that were refused
+ *
+ * A request is refused, and keeps its pages and its cached length, when
+ * cached + fresh exceeds max_pages * page_size, when its tokens end past
+ * max_tokens, or when it needs pages and those that the requests up to and
+ * with it need (but for those refused by the first two rules) exceed the free
+ * ones: its slots are -1 and its rows of the step's attention mean nothing.
+ * Entries of the table past a request's pages are left as they were.
+ * seqlen_k may be `cached`, free_count_out may be `free_count`; with outputs
+ * of their own the call may be repeated and does the same again.  Negative
+ * cached counts as 0, *free_count is clamped to [0, num_pages], a page number
+ * outside [0, num_pages) gives slots of -1, and pages that do not fit the
+ * stack are dropped.  Limits: B <= 4096; max_pages * page_size and
+ * num_pages * page_size < 2^31. */
+typedef struct {
+  int B, page_size, num_pages, max_pages, table_stride, max_tokens;
+  const int* cached;
+  const int* fresh;
+  int* free_pages;
+  const int* free_count;
+  int* block_table;
+  int* cu_seqlens_q;
+  int* seqlen_k;
+  int* free_count_out;
+  long long* slot_map;
+  int* position;
+  int* refused;
+} attn_plan_t;
+attn_status_t attn_paged_plan(const attn_plan_t* plan, void* stream);
+
+/* Writes the keys and values of T tokens into their slots: row t of k and v
+ * ([T, Hkv, 128] of the pages' dtype; rows k_stride / v_stride elements apart,
+ * heads 128 apart) goes to slot_map[t] of k_pages / v_pages.  A slot outside
+ * [0, num_pages * page_size) is skipped (-1: a padded row).  Slots must be
+ * distinct: of two rows for one slot either, or parts of each, may stay. */
+attn_status_t attn_paged_store(const attn_pages_t* pages, int T, const void* k, const void* v,
+                               long long k_stride, long long v_stride, const long long* slot_map,
+                               void* k_pages, void* v_pages, void* stream);
+
 /* Synchronizes `stream`, then reads the status word that the last call which
  * used `ws` left in the workspace: ATTN_OK, or ATTN_ERR_TIMEOUT when a device
  * wait ran out.  ATTN_ERR_CUDA if the synchronization itself fails. */

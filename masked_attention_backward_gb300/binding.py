@@ -24,7 +24,7 @@ ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_SLIDING, ATTN_MASK_BLOCK, \
 # Every symbol include/maskattn.h declares.
 EXPORTS = ("attn_workspace_size", "attn_fwd", "attn_bwd", "attn_bwd_noalloc",
            "attn_get_device_status", "attn_noalloc_get_device_status", "attn_profile_enable",
-           "attn_profile_read", "attn_status_string")
+           "attn_profile_read", "attn_status_string", "attn_paged_plan", "attn_paged_store")
 
 
 class attn_shape_t(ctypes.Structure):
@@ -44,6 +44,21 @@ class attn_mask_desc_t(ctypes.Structure):
                 ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
                 ("total_q", ctypes.c_int), ("total_k", ctypes.c_int),
                 ("first", ctypes.c_int)]
+
+
+class attn_pages_t(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("page_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong)]
+
+
+class attn_plan_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "page_size", "num_pages", "max_pages",
+                                            "table_stride", "max_tokens")] + \
+               [(n, ctypes.c_void_p) for n in ("cached", "fresh", "free_pages", "free_count",
+                                               "block_table", "cu_seqlens_q", "seqlen_k",
+                                               "free_count_out", "slot_map", "position",
+                                               "refused")]
 
 
 class AttnError(RuntimeError):
@@ -85,6 +100,11 @@ def load(build: bool = True) -> ctypes.CDLL:
                                               ctypes.POINTER(ctypes.c_float), ctypes.c_int,
                                               ctypes.POINTER(ctypes.c_int)]
             lib.attn_profile_read.restype = ctypes.c_int
+            ll, pp = ctypes.c_longlong, ctypes.POINTER(attn_pages_t)
+            lib.attn_paged_plan.argtypes = [ctypes.POINTER(attn_plan_t), vp]
+            lib.attn_paged_plan.restype = ctypes.c_int
+            lib.attn_paged_store.argtypes = [pp, ctypes.c_int, vp, vp, ll, ll, vp, vp, vp, vp]
+            lib.attn_paged_store.restype = ctypes.c_int
             lib.attn_status_string.argtypes = [ctypes.c_int]
             lib.attn_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -288,6 +308,135 @@ def bwd(q, k, v, o, dO, lse, sink, mask: Mask, scale: float, ws: Optional[torch.
 
 def device_status(ws: torch.Tensor, stream=None) -> int:
     return attn_get_device_status(_ptr(ws), _stream(stream))
+
+
+# ------------------------------------------------------------- paged cache
+
+def attn_paged_plan(plan: attn_plan_t, stream) -> int:
+    return load().attn_paged_plan(ctypes.byref(plan), stream)
+
+
+def attn_paged_store(pages: attn_pages_t, T, k, v, k_stride, v_stride, slot_map, k_pages, v_pages,
+                     stream) -> int:
+    return load().attn_paged_store(ctypes.byref(pages), T, k, v, k_stride, v_stride, slot_map,
+                                   k_pages, v_pages, stream)
+
+
+def _one_device(*tensors):
+    """All tensors on one CUDA device: a guard that makes it current."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return torch.cuda.device(dev)
+
+
+def _int_tensor(t: torch.Tensor, name: str, numel: int, dtype=torch.int32):
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel}")
+
+
+class PagedCache:
+    """The pages of a key/value cache: k_pages and v_pages of one shape,
+    [pages, Hkv, page_size, 128] (layout "HND") or [pages, page_size, Hkv, 128]
+    ("NHD"), possibly slices of a larger tensor, with the same strides."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, layout: str = "HND"):
+        if layout not in ("HND", "NHD"):
+            raise ValueError(f"unknown layout {layout!r}")
+        if k_pages.dim() != 4 or k_pages.shape[3] != 128 or v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must be [pages, ., ., 128] of one shape")
+        if v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device:
+            raise ValueError("k_pages and v_pages must have one type and one device")
+        hd, td = (1, 2) if layout == "HND" else (2, 1)
+
+        def strides(t):   # a dimension of one element may have any stride
+            return [128 if t.shape[i] == 1 else t.stride(i) for i in (0, hd, td)]
+        if k_pages.stride(3) != 1 or v_pages.stride(3) != 1 or strides(k_pages) != strides(v_pages):
+            raise ValueError("k_pages and v_pages must have the same strides, 1 for the last")
+        self.k_pages, self.v_pages, self.layout = k_pages, v_pages, layout
+        self.num_pages, self.Hkv, self.page_size = (k_pages.shape[i] for i in (0, hd, td))
+        self.desc = attn_pages_t(self.num_pages, self.page_size, self.Hkv, _dtype_code(k_pages),
+                                 *strides(k_pages))
+
+
+@dataclass
+class PagedPlan:
+    """What attn_paged_plan wrote for one step (all on the device)."""
+    cu_seqlens_q: torch.Tensor   # int32 [B + 1]
+    seqlen_k: torch.Tensor       # int32 [B]
+    free_count: torch.Tensor     # int32 [1]
+    slot_map: torch.Tensor       # int64 [max_tokens]
+    position: torch.Tensor       # int32 [max_tokens]
+    refused: torch.Tensor        # int32 [1]
+
+    @staticmethod
+    def empty(B: int, max_tokens: int, device) -> "PagedPlan":
+        e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=device)
+        return PagedPlan(e(B + 1), e(B), e(1), e(max_tokens, torch.int64), e(max_tokens), e(1))
+
+
+def paged_plan(cached, fresh, free_pages, free_count, block_table, page_size: int,
+               max_tokens: int, out: Optional[PagedPlan] = None, stream=None) -> PagedPlan:
+    """Pages, slots and offsets of one step from the request lengths cached
+    and fresh (int32 [B]); free_pages (int32, one entry per page of the cache)
+    and block_table (int32 [B, max_pages]) are updated in place.  out: buffers
+    of an earlier plan to write (its seqlen_k may be `cached` and its
+    free_count `free_count`)."""
+    B = cached.numel()
+    for t, n, m in ((cached, "cached", B), (fresh, "fresh", B),
+                    (free_pages, "free_pages", free_pages.numel()),
+                    (free_count, "free_count", 1)):
+        _int_tensor(t, n, m)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_pages] with rows of stride 1")
+    if out is None:
+        out = PagedPlan.empty(B, max_tokens, cached.device)
+    else:
+        for t, n, m in ((out.cu_seqlens_q, "cu_seqlens_q", B + 1), (out.seqlen_k, "seqlen_k", B),
+                        (out.free_count, "out.free_count", 1), (out.refused, "refused", 1),
+                        (out.position, "position", max_tokens)):
+            _int_tensor(t, n, m)
+        _int_tensor(out.slot_map, "slot_map", max_tokens, torch.int64)
+    cols = block_table.shape[1]
+    plan = attn_plan_t(B, page_size, free_pages.numel(), cols,
+                       block_table.stride(0) if B > 1 else cols, max_tokens, cached.data_ptr(),
+                       fresh.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                       block_table.data_ptr(), out.cu_seqlens_q.data_ptr(),
+                       out.seqlen_k.data_ptr(), out.free_count.data_ptr(),
+                       out.slot_map.data_ptr(), out.position.data_ptr(), out.refused.data_ptr())
+    with _one_device(cached, fresh, free_pages, free_count, block_table, out.cu_seqlens_q,
+                     out.seqlen_k, out.free_count, out.slot_map, out.position, out.refused):
+        r = attn_paged_plan(plan, _stream(stream))
+    if r != ATTN_OK:
+        raise AttnError(r, "attn_paged_plan")
+    return out
+
+
+def paged_store(cache: PagedCache, k, v, slot_map, stream=None) -> None:
+    """Rows of k and v ([T, Hkv, 128], possibly slices of a larger tensor) into
+    their slots of the cache (int64 [T]; negative: skipped)."""
+    T = slot_map.numel()
+    for t, n in ((k, "k"), (v, "v")):
+        if t.dtype != cache.k_pages.dtype or tuple(t.shape) != (T, cache.Hkv, 128) or \
+                t.stride(2) != 1 or (cache.Hkv > 1 and t.stride(1) != 128):
+            raise ValueError(f"{n} must be [T, Hkv, 128] of the cache's type, its heads 128 apart")
+    _int_tensor(slot_map, "slot_map", T, torch.int64)
+    row = cache.Hkv * 128
+    with _one_device(cache.k_pages, k, v, slot_map):
+        r = attn_paged_store(cache.desc, T, k.data_ptr(), v.data_ptr(),
+                             k.stride(0) if T > 1 else row, v.stride(0) if T > 1 else row,
+                             slot_map.data_ptr(), cache.k_pages.data_ptr(),
+                             cache.v_pages.data_ptr(), _stream(stream))
+    if r != ATTN_OK:
+        raise AttnError(r, "attn_paged_store")
 
 
 class HostBackward:
