@@ -278,6 +278,46 @@ attn_status_t attn_paged_store(const attn_pages_t* pages, int T, const void* k, 
                                long long k_stride, long long v_stride, const long long* slot_map,
                                void* k_pages, void* v_pages, void* stream);
 
+/* Workspace bytes of attn_paged_fwd for this shape (host only): B requests
+ * (<= 4096), Sq the longest run of new tokens, Skv the longest context.  The
+ * need does not grow with the lengths.  Errors: ATTN_ERR_INVALID_ARG, and
+ * ATTN_ERR_UNSUPPORTED for D != 128 or Hq / Hkv > 128. */
+attn_status_t attn_paged_workspace_size(const attn_shape_t* shape, size_t* bytes);
+
+/* Attention of each request's new tokens over its paged cache, in which their
+ * own keys and values are stored already (attn_paged_store).
+ *
+ * q and o are packed rows [total_q, Hq, 128]; request b's new tokens are rows
+ * [cu_seqlens_q[b], cu_seqlens_q[b + 1]), its keys are the first seqlen_k[b]
+ * of its pages, and of n new tokens over L keys token i stands at position
+ * x = L - n + i (the masks' i): the new tokens end where the keys end.  lse is
+ * float32 [Hq, total_q], or NULL when it is not wanted.  A row that sees no
+ * key (L = 0, or x < 0) gets O = 0 and LSE = the sink, or +inf without one.
+ *
+ * mask: kind NONE, CAUSAL, SLIDING or SLIDING_FIRST (Sq and Skv need not be
+ * equal); cu_seqlens_q, seqlen_k and total_q are set, seqlen_q and
+ * cu_seqlens_k NULL.  Offsets are clamped to [0, total_q], new tokens to Sq,
+ * keys to min(Skv, max_pages * page_size); rows of q that no request owns
+ * leave o and lse as they were.  block_table is int32 [B, max_pages], rows
+ * table_stride apart; only entries that hold a seen key are read.
+ *
+ * Pages may hold anything, NaN included, in rows past a request's keys, and in
+ * those that none of its new tokens sees any more (before the window, past the
+ * first keys): pages that left the window may be given back.  Keys and values
+ * that some new token sees must be finite.  A page number outside [0,
+ * num_pages) that holds seen keys is not read: it stands for zeros, and
+ * attn_get_device_status then returns ATTN_ERR_INVALID_ARG.
+ *
+ * The lengths stay on the device: one call's grid and workspace serve any
+ * lengths within the shape, so a captured call may be replayed with others.
+ * Results do not depend on the order in which CTAs finish.  shape.flags must
+ * be 0 and scale positive. */
+attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* pages, const void* q,
+                             const void* k_pages, const void* v_pages, const int* block_table,
+                             int table_stride, int max_pages, const float* sink,
+                             const attn_mask_desc_t* mask, float scale, void* o, float* lse,
+                             void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronizes `stream`, then reads the status word that the last call which
  * used `ws` left in the workspace: ATTN_OK, or ATTN_ERR_TIMEOUT when a device
  * wait ran out.  ATTN_ERR_CUDA if the synchronization itself fails. */

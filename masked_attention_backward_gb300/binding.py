@@ -24,7 +24,8 @@ ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_SLIDING, ATTN_MASK_BLOCK, \
 # Every symbol include/maskattn.h declares.
 EXPORTS = ("attn_workspace_size", "attn_fwd", "attn_bwd", "attn_bwd_noalloc",
            "attn_get_device_status", "attn_noalloc_get_device_status", "attn_profile_enable",
-           "attn_profile_read", "attn_status_string", "attn_paged_plan", "attn_paged_store")
+           "attn_profile_read", "attn_status_string", "attn_paged_plan", "attn_paged_store",
+           "attn_paged_workspace_size", "attn_paged_fwd")
 
 
 class attn_shape_t(ctypes.Structure):
@@ -105,6 +106,11 @@ def load(build: bool = True) -> ctypes.CDLL:
             lib.attn_paged_plan.restype = ctypes.c_int
             lib.attn_paged_store.argtypes = [pp, ctypes.c_int, vp, vp, ll, ll, vp, vp, vp, vp]
             lib.attn_paged_store.restype = ctypes.c_int
+            lib.attn_paged_workspace_size.argtypes = [ps, ctypes.POINTER(sz)]
+            lib.attn_paged_workspace_size.restype = ctypes.c_int
+            lib.attn_paged_fwd.argtypes = [ps, pp, vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, vp,
+                                           pm, ctypes.c_float, vp, vp, vp, sz, vp]
+            lib.attn_paged_fwd.restype = ctypes.c_int
             lib.attn_status_string.argtypes = [ctypes.c_int]
             lib.attn_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -322,6 +328,19 @@ def attn_paged_store(pages: attn_pages_t, T, k, v, k_stride, v_stride, slot_map,
                                    k_pages, v_pages, stream)
 
 
+def attn_paged_workspace_size(shape: attn_shape_t):
+    n = ctypes.c_size_t(0)
+    r = load().attn_paged_workspace_size(ctypes.byref(shape), ctypes.byref(n))
+    return r, n.value
+
+
+def attn_paged_fwd(shape, pages, q, k_pages, v_pages, block_table, table_stride, max_pages, sink,
+                   mask, scale, o, lse, ws, ws_bytes, stream) -> int:
+    return load().attn_paged_fwd(ctypes.byref(shape), ctypes.byref(pages), q, k_pages, v_pages,
+                                 block_table, table_stride, max_pages, sink, ctypes.byref(mask),
+                                 ctypes.c_float(scale), o, lse, ws, ws_bytes, stream)
+
+
 def _one_device(*tensors):
     """All tensors on one CUDA device: a guard that makes it current."""
     dev = None
@@ -437,6 +456,69 @@ def paged_store(cache: PagedCache, k, v, slot_map, stream=None) -> None:
                              cache.v_pages.data_ptr(), _stream(stream))
     if r != ATTN_OK:
         raise AttnError(r, "attn_paged_store")
+
+
+def paged_mask(kind: int, plan: PagedPlan, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
+               window: int = 0, first: int = 0) -> Mask:
+    """Mask of paged_fwd from a plan's offsets and lengths; total_q: rows of q
+    (those past the plan's last token are left alone), max_seqlen_q and
+    max_seqlen_k: bounds of the new tokens and keys of a request."""
+    return Mask(kind=kind, window=window, first=first, cu_seqlens_q=plan.cu_seqlens_q,
+                seqlen_k=plan.seqlen_k, total_q=total_q, max_seqlen_q=max_seqlen_q,
+                max_seqlen_k=max_seqlen_k)
+
+
+def paged_shape(q: torch.Tensor, cache: PagedCache, mask: Mask) -> attn_shape_t:
+    return attn_shape_t(mask.seqlen_k.numel(), q.shape[1], cache.Hkv, mask.max_seqlen_q,
+                        mask.max_seqlen_k, q.shape[2], _dtype_code(q), 0)
+
+
+def paged_workspace(q: torch.Tensor, cache: PagedCache, mask: Mask) -> torch.Tensor:
+    r, n = attn_paged_workspace_size(paged_shape(q, cache, mask))
+    if r != ATTN_OK:
+        raise AttnError(r, "attn_paged_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
+              ws: Optional[torch.Tensor] = None, out=None, stream=None):
+    """Attention of the packed new tokens q [total_q, Hq, 128] over the cache;
+    returns (o, lse).  out: (o, lse) to write, of which lse may be None."""
+    if mask.cu_seqlens_q is None or mask.seqlen_k is None or \
+            mask.cu_seqlens_q.numel() != mask.seqlen_k.numel() + 1:
+        raise ValueError("the mask needs cu_seqlens_q [B + 1] and seqlen_k [B]")
+    if q.dim() != 3 or q.shape[0] != mask.total_q or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [total_q, Hq, 128] tensor")
+    if q.dtype != cache.k_pages.dtype:
+        raise ValueError("q and the cache must have one type")
+    B = mask.seqlen_k.numel()
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_pages] with rows of stride 1")
+    if sink is not None:
+        _int_tensor(sink, "sink", q.shape[1], torch.float32)
+    if out is None:
+        out = (torch.empty_like(q),
+               torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device))
+    o, lse = out
+    if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
+        raise ValueError("o must be a contiguous tensor like q")
+    if lse is not None:
+        _int_tensor(lse, "lse", q.shape[0] * q.shape[1], torch.float32)
+    shape = paged_shape(q, cache, mask)
+    cols = block_table.shape[1]
+    with _one_device(q, cache.k_pages, block_table, sink, mask.cu_seqlens_q, mask.seqlen_k, o, lse,
+                     ws):
+        if ws is None:
+            ws = paged_workspace(q, cache, mask)
+        r = attn_paged_fwd(shape, cache.desc, q.data_ptr(), cache.k_pages.data_ptr(),
+                           cache.v_pages.data_ptr(), block_table.data_ptr(),
+                           block_table.stride(0) if B > 1 else cols, cols, _ptr(sink), mask.desc(),
+                           scale, o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
+                           _stream(stream))
+    if r != ATTN_OK:
+        raise AttnError(r, "attn_paged_fwd")
+    return o, lse
 
 
 class HostBackward:

@@ -25,11 +25,33 @@
 #include "internal.h"
 #include "tmap.h"
 
+namespace mab {
+
+constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;  // 2 s per wait
+
+// Test hook (MASKATTN_TEST_NO_LOADS=1): the producer warps of the tcgen05
+// kernels issue no loads and signal nothing, so the first wait of every CTA
+// runs out with nothing in flight -- the way the tests reach the bounded-wait
+// error path without disturbing the GPU.
+int test_no_loads() {
+  const char* e = getenv("MASKATTN_TEST_NO_LOADS");
+  return (e && e[0] == '1') ? 1 : 0;
+}
+
+unsigned long long wait_timeout_ns() {
+  const char* e = getenv("MASKATTN_WAIT_TIMEOUT_NS");
+  if (e && *e) {
+    unsigned long long v = strtoull(e, nullptr, 10);
+    if (v > 0) return v;
+  }
+  return kDefaultTimeoutNs;
+}
+
+}  // namespace mab
+
 using namespace mab;
 
 namespace {
-
-constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;  // 2 s per wait
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -173,15 +195,6 @@ WsLayout layout_of(const attn_shape_t* sh, const attn_mask_desc_t* mk) {
   return L;
 }
 
-// Test hook (MASKATTN_TEST_NO_LOADS=1): the producer warps of the tcgen05
-// kernels issue no loads and signal nothing, so the first wait of every CTA
-// runs out with nothing in flight -- the way the tests reach the bounded-wait
-// error path without disturbing the GPU.
-int test_no_loads() {
-  const char* e = getenv("MASKATTN_TEST_NO_LOADS");
-  return (e && e[0] == '1') ? 1 : 0;
-}
-
 // Test hook (MASKATTN_DKDV_SCHEDULE=tile|units): forces the dK/dV kernel's
 // form, so that the tests run both on any shape.
 int dkdv_schedule() {
@@ -190,15 +203,6 @@ int dkdv_schedule() {
   if (strcmp(e, "tile") == 0) return 1;
   if (strcmp(e, "units") == 0) return 2;
   return 0;
-}
-
-unsigned long long wait_timeout_ns() {
-  const char* e = getenv("MASKATTN_WAIT_TIMEOUT_NS");
-  if (e && *e) {
-    unsigned long long v = strtoull(e, nullptr, 10);
-    if (v > 0) return v;
-  }
-  return kDefaultTimeoutNs;
 }
 
 AttnParams params_of(const attn_shape_t* sh, const attn_mask_desc_t* mk, const WsLayout& L,

@@ -186,6 +186,11 @@ inline int kv_first_pieces(int B, int Hq, int Hkv, int Sq, int first) {
   return n < 1 ? 1 : (int)n;
 }
 
+// Environment hooks read at each call (api.cu): the limit of a device wait,
+// and whether the loaders issue nothing.
+unsigned long long wait_timeout_ns();
+int test_no_loads();
+
 // ---- launchers (each returns the launch error, if any) ----
 cudaError_t launch_preprocess(bool bf16, const void* O, const void* dO, const float* lse,
                               const float* sink, float* nlse2, float* delta, float* part, int B,

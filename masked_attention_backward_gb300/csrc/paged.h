@@ -6,12 +6,46 @@
 
 namespace mab {
 
-constexpr int PAGED_MAX_B = 4096;  // requests of one call
+constexpr int PAGED_MAX_B = 4096;    // requests of one call
+constexpr int PAGED_MAX_CTAS = 152;  // CTAs of the attention grid at most (one per SM)
+constexpr int PAGED_TICKETS = 8;     // softmax warps, each its own ticket of a unit
+// A warp's share of a piece in the workspace: O [32 rows, 64 columns], then
+// (M, l) [32 rows].
+constexpr int PAGED_WARP_FLOATS = 32 * 64 + 32 * 2;
+// On the line that the schedule cuts, in steps of 64 keys: what a unit costs
+// beside its steps, and the least part that a CTA gets.
+constexpr int PAGED_UNIT_COST = 2;
+constexpr int PAGED_MIN_COST = 8;
+
+// Everything the attention over the pages reads besides the tensor maps.
+struct PagedParams {
+  int B, Hq, Hkv, group, Sq, Skv, total_q;
+  int tile_tokens, tile_rows;  // tokens of a query tile, and its rows (times group)
+  int causal, window, first;   // window and first keys of the causal rule
+  const int* cu_q;
+  const int* seqlen_k;
+  const int* table;
+  int table_stride, num_pages, page_size, box_rows;  // box_rows: rows of one load
+  const float* sink;
+  uint16_t* out;
+  float* lse;  // or nullptr
+  float scale_log2;
+  DevStatus* status;
+  unsigned long long timeout_ns;
+  int test_no_loads;
+  int grid;          // CTAs
+  int4* start;       // [grid + 1] where each CTA begins: request, kv head, tile, step
+  int* ticket;       // [grid, PAGED_TICKETS] pieces done of the unit that the CTA's part ends in
+  float* part;       // [2 grid, slot_floats] pieces
+  int slot_floats;
+};
 
 cudaError_t launch_paged_plan(const attn_plan_t& p, cudaStream_t st);
 cudaError_t launch_paged_store(const attn_pages_t& pg, int T, const void* k, const void* v,
                                long long k_stride, long long v_stride, const long long* slot_map,
                                void* k_pages, void* v_pages, cudaStream_t st);
+cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap& tQ,
+                             const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ uint32_t cluster_rank() {

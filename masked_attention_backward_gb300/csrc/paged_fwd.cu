@@ -1,0 +1,955 @@
+// paged_fwd.cu -- attention of each request's new tokens over its paged cache.
+//
+// Request b brings n new tokens (rows cu_q[b] .. of q) and has L keys in its
+// cache, the new tokens' own among them; new token i stands at position
+// x = L - n + i and sees key j < L when
+//   j <= x and (x - j < window or j < first)      (or every key, MK_NONE)
+//   O = sum_j P_j v_j / l,  P_j = exp2(s_j scale log2e - M),
+//   l = sum_j P_j + exp2(sink log2e - M),  LSE = (M + log2 l) ln 2.
+//
+// One kernel for single tokens and long chunks.  The rows of a query tile are
+// (token, query head of the group) pairs, so that one pass over a kv head's
+// keys serves all of its query heads: 128 / group tokens fill the 128 rows of
+// the matrix unit for a chunk, and a single token has `group` rows, the rest
+// of the tile idle.  Work: unit = (request, kv head, query tile), walked over
+// key sub-tiles of 64.
+//
+// Bounds: chunks, the tensor cores (4 * 128 FLOP per pair and query head);
+// single tokens, HBM (512 bytes per key and kv head).  A step of a single
+// token moves 32 KB and costs the tensor pipe 540 cycles, an SM's share of the
+// HBM rate 1400, so the idle rows cost nothing there.
+//
+// Balance: k_paged_schedule lays all units end to end, in steps, and cuts the
+// line into equal parts, one per CTA of a persistent grid: a unit that a cut
+// falls into is done in pieces, each leaving its fp32 O, M and l in the
+// workspace, and the last piece to finish (a ticket per warp) joins them in
+// order, whichever it is.  So a single request's keys spread over the whole
+// GPU, ragged batches load every SM alike, and the workspace is bounded by two
+// pieces per CTA whatever the lengths, which stay on the device.
+//
+// The inner loop is that of the BHSD forward kernel (attn_fwd.cu): warp 0
+// loads (one lane per page run and tile half, page numbers fetched a step
+// ahead), warp 1 issues S = Q K^T, warp 2 O += P V, two groups of four softmax
+// warps take alternate steps.  Rows of V that no row of the unit sees (past
+// the last key, before the window, between the first keys and it) may hold
+// anything, NaN included, and 0 * NaN is NaN in the matrix unit: the page runs
+// without a seen key are not loaded (zeros stand in), and warp 2 clears the
+// other unseen rows in shared memory before it multiplies.
+#include <math.h>
+
+#include "paged.h"
+#include "tiles.cuh"
+
+namespace mab {
+
+namespace paged_side {
+
+constexpr int STAGES = 5;        // K/V ring depth
+constexpr int NBUF = 3;          // S / P buffers
+constexpr int COL_O = 0;         // O accumulator of group g at COL_O + 128 g
+constexpr int COL_QA = 256;      // Q as the A operand, 64 columns of 16-bit pairs
+constexpr int COL_S = 320;       // S buffer b at COL_S + 64 b
+constexpr int SM_WARP0 = 3;      // first softmax warp
+constexpr int SM_WARPS = 8;      // softmax warps, two groups of four
+constexpr int NUM_THREADS = 32 * (SM_WARP0 + SM_WARPS);
+constexpr float RESCALE_LOG2 = 8.f;  // M moves when a row maximum exceeds it by this
+constexpr int SCHED_THREADS = 1024;
+constexpr int NO_PAGE = (int)0x80000000;
+
+// A unit's piece, as the loader publishes it.
+struct Unit {
+  int kvh, off, n, L, tok0;  // kv head; the request's first row, new tokens, keys; first token
+  int N;                     // steps of the piece
+  int pieces, slot, c0;      // pieces of the unit; this one's slot; CTA of the first one
+};
+
+struct __align__(1024) Smem {
+  uint8_t Q[2 * Q_TILE * 128];  // two 64-column chunks, 128B swizzle; once copied
+                                // into TMEM, the epilogue staging (4 KB per warp)
+  uint8_t K[STAGES][2 * Q_SUB * 128];
+  uint8_t V[STAGES][2 * Q_SUB * 128];
+  float xml[2][2][Q_TILE][2];   // [unit parity][group][row]: (M, l) at the piece's end
+  int step_t[STAGES];           // key sub-tile of the step in the stage
+  Unit unit;                    // piece of the latest Q load, N < 0: none left
+  uint64_t bar_q_full;
+  uint64_t bar_qa_full;         // Q copied into TMEM (all softmax warps)
+  uint64_t bar_kv_full[STAGES];
+  uint64_t bar_kv_empty[STAGES];
+  uint64_t bar_s_full[2][2];    // [group][its step count parity]: S of the step complete
+  uint64_t bar_p_full[NBUF];    // P of the buffer packed (the four warps of its group)
+  uint64_t bar_p_free[NBUF];    // O += P V that read the buffer complete
+  uint64_t bar_xml[4][2];       // [row quarter][unit parity]: both groups posted (M, l)
+  uint64_t bar_acc_full;        // every O MMA of the piece complete
+  uint64_t bar_acc_empty;       // its accumulators read (all softmax warps)
+  uint64_t bar_unit_free;       // every other warp took the unit (and, softmax warps,
+                                // stored the previous unit's epilogue)
+  uint64_t bar_x_done[2];       // every MMA of the S / O warp complete
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+constexpr size_t SMEM_BYTES = sizeof(Smem) + 1024;
+static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
+
+enum { TAG_Q = 0x501, TAG_QA, TAG_KV_EMPTY, TAG_KV_FULL, TAG_S_FULL, TAG_P_FULL, TAG_P_FREE,
+       TAG_ACC, TAG_ACC_EMPTY, TAG_UNIT_FREE, TAG_XML };
+
+template <int NS>
+struct Cyc {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == NS) {
+      i = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// New tokens and keys of request b.
+__device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
+  return packed_len(p.cu_q, b, p.total_q, p.Sq);
+}
+__device__ __forceinline__ int keys_of(const PagedParams& p, int b) {
+  return min(max(p.seqlen_k[b], 0), p.Skv);
+}
+
+// Keys that some row of a query tile sees, [0, f) and [wlo, hi], and the walk
+// over their sub-tiles: the nfirst ones that hold first keys, then those from
+// lo on.  cnt = 0 when no row sees a key.
+struct Walk {
+  int f, wlo, hi, nfirst, lo, cnt;
+  __device__ __forceinline__ Walk(const PagedParams& p, int n, int L, int tok0) {
+    const int x0 = L - n + tok0;
+    hi = p.causal ? L - n + min(tok0 + p.tile_tokens, n) - 1 : L - 1;
+    wlo = p.causal ? max(x0 - p.window + 1, 0) : 0;
+    f = min(p.first, hi + 1);
+    lo = wlo / Q_SUB;
+    nfirst = min((max(f, 0) + Q_SUB - 1) / Q_SUB, lo);
+    cnt = hi < 0 ? 0 : nfirst + hi / Q_SUB - lo + 1;
+  }
+  __device__ __forceinline__ int tile(int s) const { return s < nfirst ? s : lo + s - nfirst; }
+  // whether a row sees any key of [a, b), or every one
+  __device__ __forceinline__ bool any(int a, int b) const { return a < f || (a <= hi && b > wlo); }
+  __device__ __forceinline__ bool all(int a, int b) const {
+    return b <= f || (a >= wlo && b <= hi + 1);
+  }
+  __device__ __forceinline__ bool sees(int j) const { return j < f || (j >= wlo && j <= hi); }
+};
+
+// What a unit costs on the line that is cut: its steps, and PAGED_UNIT_COST
+// for its start and end.
+__device__ __forceinline__ int unit_cost(const PagedParams& p, int n, int L, int tile) {
+  return Walk(p, n, L, tile * p.tile_tokens).cnt + PAGED_UNIT_COST;
+}
+
+}  // namespace paged_side
+
+// One block.  Lays the units (request, kv head, query tile) end to end and
+// writes where each CTA's part begins: {request, kv head, tile, step}.
+__global__ void __launch_bounds__(paged_side::SCHED_THREADS)
+k_paged_schedule(const PagedParams p, int grid) {
+  using namespace paged_side;
+  grid_launch_dependents();
+  __shared__ long long base[PAGED_MAX_B + 1];  // cost of the requests before b
+  __shared__ long long warp_tot[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < (int)(sizeof(DevStatus) / 4)) reinterpret_cast<unsigned*>(p.status)[tid] = 0u;
+  for (int i = tid; i < grid * PAGED_TICKETS; i += SCHED_THREADS) p.ticket[i] = 0;
+  long long carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += SCHED_THREADS) {
+    const int b = b0 + tid;
+    int n = 0, L = 0, tiles = 0;
+    if (b < p.B) {
+      n = new_tokens(p, b);
+      L = keys_of(p, b);
+      tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
+    }
+    long long w = tiles > 0 ? unit_cost(p, n, L, 0) : 0;
+    // several tiles: the warp adds their costs, one request after another
+    for (unsigned todo = __ballot_sync(0xffffffffu, tiles > 1); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int sn = __shfl_sync(0xffffffffu, n, src), sL = __shfl_sync(0xffffffffu, L, src);
+      const int st = __shfl_sync(0xffffffffu, tiles, src);
+      long long sum = 0;
+      for (int t = lane; t < st; t += 32) sum += unit_cost(p, sn, sL, t);
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == src) w = sum;
+    }
+    w *= p.Hkv;
+    // inclusive scan over the block
+    long long v = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) warp_tot[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      long long u = warp_tot[lane];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, u, d);
+        if (lane >= d) u += x;
+      }
+      warp_tot[lane] = u;
+    }
+    __syncthreads();
+    if (warp > 0) v += warp_tot[warp - 1];
+    if (b < p.B) base[b] = carry + v - w;
+    carry += warp_tot[31];
+  }
+  if (tid == 0) base[p.B] = carry;
+  __syncthreads();
+  const long long total = carry;
+  // parts of at least PAGED_MIN_COST: further cuts would cost more to join
+  const long long most = total / PAGED_MIN_COST;
+  const int parts = (int)(most < 1 ? 1 : most < grid ? most : grid);
+  for (int c = warp; c <= grid; c += SCHED_THREADS / 32) {
+    int4 r = make_int4(p.B, 0, 0, 0);  // past the last unit
+    const long long cut = c < parts ? total / parts * c + total % parts * c / parts : total;
+    if (cut < total) {
+      int lo = 0, hi = p.B - 1;  // the request that holds the cut: the last with base <= cut
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (base[mid] <= cut) lo = mid;
+        else hi = mid - 1;
+      }
+      const int b = lo;
+      const long long head = (base[b + 1] - base[b]) / p.Hkv;
+      int kvh = (int)((cut - base[b]) / head);
+      long long rem = (cut - base[b]) - kvh * head;
+      const int n = new_tokens(p, b), L = keys_of(p, b);
+      const int tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
+      int tile = 0, cost = 0;
+      for (int t0 = 0; t0 < tiles; t0 += 32) {
+        const int mine = t0 + lane < tiles ? unit_cost(p, n, L, t0 + lane) : 0;
+        long long v = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long u = __shfl_up_sync(0xffffffffu, v, d);
+          if (lane >= d) v += u;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, v > rem);
+        if (past) {
+          const int src = __ffs(past) - 1;
+          tile = t0 + src;
+          cost = __shfl_sync(0xffffffffu, mine, src);
+          rem -= __shfl_sync(0xffffffffu, v, src) - cost;
+          break;
+        }
+        rem -= __shfl_sync(0xffffffffu, v, 31);
+      }
+      // the unit's own cost stands before its steps; a cut beside its first or
+      // last step moves to the unit's edge
+      int step = (int)rem - PAGED_UNIT_COST;
+      if (step <= 0) step = 0;
+      if (cost - (int)rem <= 1 && step > 0) {
+        step = 0;
+        if (++tile == tiles) {
+          tile = 0;
+          if (++kvh == p.Hkv) {
+            kvh = 0;
+            lo = b + 1;
+            while (lo < p.B && base[lo + 1] == base[lo]) ++lo;
+          }
+        }
+      }
+      r = make_int4(lo, kvh, tile, step);
+    }
+    if (lane == 0) p.start[c] = r;
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(paged_side::NUM_THREADS, 1)
+k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
+            const __grid_constant__ CUtensorMap tV, const PagedParams p) {
+  using namespace paged_side;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                     ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  WaitCtx wc{p.status, &s.abort_flag, p.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    s.abort_flag = 0;
+    mbar_init(smem_u32(&s.bar_q_full), 1);
+    mbar_init(smem_u32(&s.bar_qa_full), SM_WARPS);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&s.bar_kv_full[i]), 1);
+      mbar_init(smem_u32(&s.bar_kv_empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&s.bar_s_full[i >> 1][i & 1]), 1);
+      mbar_init(smem_u32(&s.bar_xml[i][0]), 2);
+      mbar_init(smem_u32(&s.bar_xml[i][1]), 2);
+    }
+    for (int i = 0; i < NBUF; ++i) {
+      mbar_init(smem_u32(&s.bar_p_full[i]), SM_WARPS / 2);
+      mbar_init(smem_u32(&s.bar_p_free[i]), 1);
+    }
+    mbar_init(smem_u32(&s.bar_acc_full), 1);
+    mbar_init(smem_u32(&s.bar_acc_empty), SM_WARPS);
+    mbar_init(smem_u32(&s.bar_unit_free), SM_WARPS + 2);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.bar_x_done[i]), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tQ);
+    tma_prefetch_desc(&tK);
+    tma_prefetch_desc(&tV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s.tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = s.tmem_base;
+  // launched over the schedule kernel: its cuts are read from here on
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loader (whole warp)
+    const int cta = (int)blockIdx.x;
+    const int4 end = __ldcg(p.start + cta + 1);
+    int4 at = __ldcg(p.start + cta);
+    // lane -> one box of a step: half of K or V, run of box_rows keys
+    const int runs = Q_SUB / p.box_rows;
+    const int part = lane & 3, run = lane >> 2;
+    const bool loads = run < runs;
+    const CUtensorMap* tm = part < 2 ? &tK : &tV;
+    const int c0 = (part & 1) * 64;
+    bool ok = !p.test_no_loads;
+    int m = 0;          // steps issued, across units
+    int q_loaded = -1;  // last unit whose Q tile was loaded
+    int b_base = -64;   // lane i holds the lengths of request b_base + i
+    int l_off = 0, l_n = 0, l_L = 0;
+    Cyc<STAGES> rg;
+    const uint32_t qbar = smem_u32(&s.bar_q_full);
+    for (int j = 0; ok; ++j) {
+      if (j >= 1 &&
+          !mbar_wait_warp(smem_u32(&s.bar_unit_free), (j - 1) & 1, wc, TAG_UNIT_FREE)) {
+        ok = false;
+        break;
+      }
+      const bool in_end = at.x == end.x && at.y == end.y && at.z == end.z;
+      if (at.x >= p.B || (in_end && end.w <= at.w)) {
+        if (lane == 0) {
+          s.unit.N = -1;
+          mbar_arrive(qbar);
+        }
+        break;
+      }
+      if (at.x >= b_base + 32) {
+        b_base = at.x;
+        const int b = b_base + lane;
+        l_off = l_n = l_L = 0;
+        if (b < p.B) {
+          l_off = packed_off(p.cu_q, b, p.total_q);
+          l_n = new_tokens(p, b);
+          l_L = keys_of(p, b);
+        }
+      }
+      const int src = at.x - b_base;
+      const int off = __shfl_sync(0xffffffffu, l_off, src);
+      const int n = __shfl_sync(0xffffffffu, l_n, src), L = __shfl_sync(0xffffffffu, l_L, src);
+      const int tok0 = at.z * p.tile_tokens;
+      const Walk w(p, n, L, tok0);
+      const int s0 = at.w, s1 = in_end ? end.w : w.cnt;
+      // cuts inside this unit: the records of the CTAs that go on with it
+      int cuts = 0, first_cut = 0;
+      if (s0 > 0 || in_end) {
+        for (int c = 0; c < p.grid; c += 32) {
+          int4 r = make_int4(-1, 0, 0, 0);
+          if (c + lane < p.grid) r = __ldcg(p.start + c + lane);
+          const unsigned mine = __ballot_sync(
+              0xffffffffu, r.x == at.x && r.y == at.y && r.z == at.z && r.w > 0);
+          if (mine && cuts == 0) first_cut = c + __ffs(mine) - 1;
+          cuts += __popc(mine);
+        }
+      }
+      if (lane == 0) {
+        s.unit.kvh = at.y;
+        s.unit.off = off;
+        s.unit.n = n;
+        s.unit.L = L;
+        s.unit.tok0 = tok0;
+        s.unit.N = s1 - s0;
+        s.unit.pieces = cuts + 1;
+        s.unit.slot = 2 * cta + (s0 > 0 ? 0 : 1);
+        s.unit.c0 = first_cut - 1;
+        if (s1 == s0) {
+          mbar_arrive(qbar);  // no key to see: no Q either
+        } else {
+          mbar_arrive_expect_tx(qbar, 2 * p.tile_rows * 128);
+          tma_load_3d(smem_u32(s.Q), &tQ, 0, at.y * p.group, off + tok0, qbar);
+          tma_load_3d(smem_u32(s.Q + Q_TILE * 128), &tQ, 64, at.y * p.group, off + tok0, qbar);
+        }
+      }
+      if (s1 > s0) q_loaded = j;
+      // this lane's page of step i (NO_PAGE: a run without a seen key), and its
+      // first row in the page
+      const int* row = p.table + (size_t)at.x * p.table_stride;
+      int row0 = 0;
+      auto page_of = [&](int i) -> int {
+        const int k0 = w.tile(i) * Q_SUB + run * p.box_rows;
+        if (!loads || !w.any(k0, k0 + p.box_rows)) return NO_PAGE;
+        const int idx = k0 / p.page_size;
+        row0 = k0 - idx * p.page_size;
+        return __ldg(row + idx);
+      };
+      int next = s1 > s0 ? page_of(s0) : NO_PAGE, next_row = row0;
+      for (int i = s0; i < s1; ++i, ++m, rg.next()) {
+        int page = next;
+        const int prow = next_row, st = rg.i;
+        if (i + 1 < s1) {
+          next = page_of(i + 1);
+          next_row = row0;
+        }
+        if (m >= STAGES &&
+            !mbar_wait_warp(smem_u32(&s.bar_kv_empty[st]), rg.ph ^ 1u, wc, TAG_KV_EMPTY)) {
+          ok = false;
+          break;
+        }
+        if ((unsigned)page >= (unsigned)p.num_pages) {
+          // past the tensor's end, where a load reads zeros
+          if (page != NO_PAGE) atomicCAS(&p.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);
+          page = p.num_pages;
+        }
+        const uint32_t fb = smem_u32(&s.bar_kv_full[st]);
+        if (lane == 0) {
+          s.step_t[st] = w.tile(i);  // published by the arrive
+          mbar_arrive_expect_tx(fb, 4 * Q_SUB * 128);
+        }
+        __syncwarp();
+        if (loads) {
+          uint8_t* dst = (part < 2 ? s.K[st] : s.V[st]) + (part & 1) * (Q_SUB * 128) +
+                         run * p.box_rows * 128;
+          tma_load_4d(smem_u32(dst), tm, c0, prow, at.y, page, fb);
+        }
+      }
+      if (in_end) {
+        at = end;  // nothing of this CTA is left
+      } else {
+        at.w = 0;
+        if (++at.z * p.tile_tokens >= n) {
+          at.z = 0;
+          if (++at.y == p.Hkv) {
+            at.y = 0;
+            // the next request with new tokens
+            for (++at.x; at.x < p.B && at.x < end.x; ++at.x) {
+              if (at.x >= b_base + 32) {
+                b_base = at.x;
+                const int b = b_base + lane;
+                l_off = l_n = l_L = 0;
+                if (b < p.B) {
+                  l_off = packed_off(p.cu_q, b, p.total_q);
+                  l_n = new_tokens(p, b);
+                  l_L = keys_of(p, b);
+                }
+              }
+              if (__shfl_sync(0xffffffffu, l_n, at.x - b_base) > 0) break;
+            }
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      // the CTA gave up: let the copies still in flight land before it exits
+      if (q_loaded >= 0) mbar_drain(qbar, q_loaded & 1, wc.timeout_ns);
+      for (int k = m > STAGES ? m - STAGES : 0; k < m; ++k)
+        mbar_drain(smem_u32(&s.bar_kv_full[k % STAGES]), (k / STAGES) & 1, wc.timeout_ns);
+    }
+  } else if (warp < SM_WARP0) {
+    // ------------------------------------------------------------ MMA issuers (whole warps)
+    bool ok = true;
+    int m = 0;  // step counter across units
+    Cyc<STAGES> rg;
+    Cyc<NBUF> bc;
+    if (warp == 1) {
+      // S(m) = Q K^T into buffer m % NBUF (A = Q from TMEM, B = K tile, K-major)
+      constexpr uint32_t ID_S = idesc_f16(BF16, Q_TILE, Q_SUB, false, false);
+      int cnt0 = 0, cnt1 = 0;  // steps of each group so far
+      for (int j = 0; ok; ++j) {
+        if (!mbar_wait_warp(smem_u32(&s.bar_q_full), j & 1, wc, TAG_Q)) break;
+        const int N = s.unit.N;
+        if (N < 0) break;
+        ok = mbar_wait_warp(smem_u32(&s.bar_qa_full), j & 1, wc, TAG_QA);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
+        for (int i = 0; ok && i < N; ++i, ++m, rg.next(), bc.next()) {
+          const int st = rg.i, bf = bc.i, grp = i & 1;
+          ok = mbar_wait_warp(smem_u32(&s.bar_kv_full[st]), rg.ph, wc, TAG_KV_FULL);
+          // the buffer held P(m - NBUF), read by O += P V
+          if (ok && m >= NBUF)
+            ok = mbar_wait_warp(smem_u32(&s.bar_p_free[bf]), bc.ph ^ 1u, wc, TAG_P_FREE);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bK = sdesc_sw128(smem_u32(s.K[st]), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < HEAD_DIM / 16; ++kk)
+            mma_ts_w(tbase + COL_S + 64 * bf, tbase + COL_QA + 8 * kk,
+                     bK + (uint64_t)(((kk >> 2) * (Q_SUB * 128) + (kk & 3) * 32) >> 4), ID_S,
+                     kk > 0 ? 1u : 0u);
+          const int c = grp ? cnt1 : cnt0;
+          mma_commit_w(smem_u32(&s.bar_s_full[grp][c & 1]));
+          if (grp) ++cnt1; else ++cnt0;
+        }
+      }
+    } else {
+      // O_{i % 2} += P(m) V (A = P packed in buffer m % NBUF, B = V tile, MN-major)
+      constexpr uint32_t ID_O = idesc_f16(BF16, Q_TILE, HEAD_DIM, false, true);
+      for (int j = 0; ok; ++j) {
+        // the unit's first accumulations overwrite the accumulators: the
+        // softmax warps must have read the previous unit's
+        if (j >= 1 &&
+            !mbar_wait_warp(smem_u32(&s.bar_acc_empty), (j - 1) & 1, wc, TAG_ACC_EMPTY))
+          break;
+        if (!mbar_wait_warp(smem_u32(&s.bar_q_full), j & 1, wc, TAG_Q)) break;
+        const int N = s.unit.N;
+        if (N < 0) break;
+        const Walk w(p, s.unit.n, s.unit.L, s.unit.tok0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
+        for (int i = 0; ok && i < N; ++i, ++m, rg.next(), bc.next()) {
+          const int st = rg.i, bf = bc.i;
+          // unseen rows of V cleared while S and the softmax of the step run
+          ok = mbar_wait_warp(smem_u32(&s.bar_kv_full[st]), rg.ph, wc, TAG_KV_FULL);
+          if (!ok) break;
+          const int k0 = s.step_t[st] * Q_SUB;
+          if (!w.all(k0, k0 + Q_SUB)) {
+            // 8 lanes per 128-byte row: four rows of a half at a time
+            for (int r = lane >> 3; r < Q_SUB; r += 4)
+              if (!w.sees(k0 + r)) {
+                uint4* row = reinterpret_cast<uint4*>(s.V[st] + r * 128) + (lane & 7);
+                row[0] = make_uint4(0u, 0u, 0u, 0u);
+                row[Q_SUB * 128 / 16] = make_uint4(0u, 0u, 0u, 0u);
+              }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          ok = mbar_wait_warp(smem_u32(&s.bar_p_full[bf]), bc.ph, wc, TAG_P_FULL);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = tbase + COL_S + 64 * bf;
+          const uint64_t bV = sdesc_sw128(smem_u32(s.V[st]), Q_SUB * 128, 1024);
+#pragma unroll
+          for (int kk = 0; kk < Q_SUB / 16; ++kk)
+            mma_ts_w(tbase + COL_O + 128 * (i & 1), a + 8 * kk,
+                     bV + (uint64_t)((kk * 2048) >> 4), ID_O, (i >= 2 || kk > 0) ? 1u : 0u);
+          // S(m) completed before the softmax warps could signal step m, so
+          // this commit also frees the K / V stage
+          mma_commit_w(smem_u32(&s.bar_kv_empty[st]));
+          mma_commit_w(smem_u32(&s.bar_p_free[bf]));
+        }
+        if (ok) mma_commit_w(smem_u32(&s.bar_acc_full));  // the accumulators are complete
+      }
+    }
+    // this warp's MMAs must be complete before TMEM is freed (also when the
+    // CTA gave up, hence a wait that ignores the abort flag)
+    const uint32_t done = smem_u32(&s.bar_x_done[warp - 1]);
+    mma_commit_w(done);
+    mbar_drain_warp(done, 0, wc.timeout_ns);
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    const int sp = warp & 3, grp = (warp - SM_WARP0) >> 2;
+    const int rloc = sp * 32 + lane;
+    const int tl = rloc / p.group, hh = rloc - tl * p.group;  // the row's token and head
+    const uint32_t lane_base = tbase + ((uint32_t)(sp * 32) << 16);
+    // the epilogue stages through the Q rows this warp itself copies
+    uint8_t* stage = s.Q + grp * (Q_TILE * 128) + sp * 4096;
+    // Combines both groups' accumulators of unit j into columns [64 grp,
+    // 64 grp + 64) of this warp's 32 rows, and stores them (a whole unit), or
+    // leaves them in the workspace, where the last piece's warp joins them.
+    // (M, l) of the own group come in; the other group's are taken from
+    // shared memory.
+    auto epilogue = [&](int j, const Unit& un, float M, float l, float sink2, bool ok) {
+      s.xml[j & 1][grp][rloc][0] = M;
+      s.xml[j & 1][grp][rloc][1] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.bar_xml[sp][j & 1]));
+      const int N = un.N;
+      // rows of the tile that are a token of the request; this warp's share
+      const int rows = min(p.tile_tokens, un.n - un.tok0) * p.group;
+      const int nr = min(32, rows - sp * 32);
+      // (a piece without steps waits too, so that no wait meets these barriers
+      // two phases late)
+      const bool done =
+          ok && mbar_wait_warp(smem_u32(&s.bar_xml[sp][j & 1]), (j >> 1) & 1, wc, TAG_XML) &&
+          mbar_wait_warp(smem_u32(&s.bar_acc_full), j & 1, wc, TAG_ACC);
+      const bool have = done && N > 0, gave_up = !done;
+      tc_fence_after();
+      float w[2] = {0.f, 0.f};  // weights of O_0 and O_1
+      float Mx = -INFINITY, lx = 0.f;
+      if (have) {
+        const float Mo = s.xml[j & 1][grp ^ 1][rloc][0], lo = s.xml[j & 1][grp ^ 1][rloc][1];
+        const float Mg[2] = {grp == 0 ? M : Mo, grp == 0 ? Mo : M};
+        const float lg[2] = {grp == 0 ? l : lo, grp == 0 ? lo : l};
+        Mx = fmaxf(Mg[0], Mg[1]);
+        // group 1 has steps only when the piece has two or more; a group's
+        // weight is zero when its row saw nothing (l = 0)
+        if (lg[0] > 0.f) w[0] = fast_exp2(Mg[0] - Mx);
+        if (N >= 2 && lg[1] > 0.f) w[1] = fast_exp2(Mg[1] - Mx);
+        lx = lg[0] * w[0] + lg[1] * w[1];
+      }
+      const bool whole = un.pieces == 1;
+      // row sums with the sink, and what O is divided by
+      auto finish = [&](float m_row, float l_row, float* inv) -> float {
+        const float top = fmaxf(m_row, sink2);
+        if (top == -INFINITY) {
+          *inv = 0.f;
+          return INFINITY;  // no key and no sink
+        }
+        const float e = l_row > 0.f ? fast_exp2(m_row - top) : 0.f;
+        float lt = l_row * e;
+        if (sink2 > -INFINITY) lt += fast_exp2(sink2 - top);
+        *inv = lt > 0.f ? e / lt : 0.f;
+        return lt > 0.f ? (top + log2f(lt)) * 0.6931471805599453f : INFINITY;
+      };
+      const int tok = un.off + un.tok0 + tl, head = un.kvh * p.group + hh;
+      const bool mine = lane < nr;
+      float inv = 0.f;
+      if (whole) {
+        const float lse = finish(Mx, lx, &inv);
+        if (p.lse && grp == 0 && mine && !gave_up) p.lse[(size_t)head * p.total_q + tok] = lse;
+        w[0] *= inv;
+        w[1] *= inv;
+      }
+      if (nr > 0 && !gave_up) {
+        float* part = nullptr;
+        if (!whole) {
+          part = p.part + (size_t)un.slot * p.slot_floats + (sp * 2 + grp) * PAGED_WARP_FLOATS;
+          if (mine) {
+            part[2048 + 2 * lane] = Mx;
+            part[2048 + 2 * lane + 1] = lx;
+          }
+        }
+        uint32_t pk[32];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float acc[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) acc[c] = 0.f;
+          if (have) {
+#pragma unroll
+            for (int gg = 0; gg < 2; ++gg) {
+              if (__any_sync(0xffffffffu, w[gg] != 0.f)) {
+                float v[32];
+                tmem_ld32(lane_base + COL_O + 128 * gg + 64 * grp + 32 * half, v);
+                tmem_wait_ld_regs(v);
+                // (a row of weight zero may hold anything)
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  acc[c] = w[gg] != 0.f ? fmaf(v[c], w[gg], acc[c]) : acc[c];
+              }
+            }
+          }
+          if (whole) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) pk[16 * half + c] = pack2<BF16>(acc[2 * c], acc[2 * c + 1]);
+          } else if (mine) {
+            float4* dst = reinterpret_cast<float4*>(part + lane * 64 + 32 * half);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              dst[c] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+          }
+        }
+        // where this lane's row goes
+        const long long at = mine ? ((long long)tok * p.Hq + head) * HEAD_DIM + 64 * grp : -1;
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = k * 4 + (lane >> 3), c = lane & 7;
+            const long long to = __shfl_sync(0xffffffffu, at, row);
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
+            if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + c * 8) = v;
+          }
+          __syncwarp();
+          // the next TMA load into the Q tile comes after this warp's generic
+          // accesses to it
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.bar_acc_empty));
+      if (whole || nr <= 0 || gave_up) return;
+
+      // ---- the last piece to get here joins all of them, in their order
+      const int wq = sp * 2 + grp;
+      __threadfence();
+      __syncwarp();
+      int before = 0;
+      if (lane == 0) before = atomicAdd(p.ticket + un.c0 * PAGED_TICKETS + wq, 1);
+      if (__shfl_sync(0xffffffffu, before, 0) != un.pieces - 1) return;
+      __threadfence();
+      // slots: 2 c0 + 1, then 2 c for the CTAs after c0
+      auto piece = [&](int i) -> const float* {
+        return p.part + (size_t)(i == 0 ? 2 * un.c0 + 1 : 2 * (un.c0 + i)) * p.slot_floats +
+               wq * PAGED_WARP_FLOATS;
+      };
+      float top = -INFINITY, lsum = 0.f;
+      for (int i = 0; i < un.pieces; ++i)
+        if (mine) top = fmaxf(top, __ldcg(piece(i) + 2048 + 2 * lane));
+      // lane -> 4 columns of rows 2 k + lane / 16
+      float4 acc[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < un.pieces; ++i) {
+        const float* src = piece(i);
+        float wt = 0.f;
+        if (mine) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + 2048) + lane);
+          wt = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
+          lsum += ml.y * wt;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          if (2 * k < nr) {
+            const float wr = __shfl_sync(0xffffffffu, wt, 2 * k + (lane >> 4));
+            if (2 * k + (lane >> 4) < nr) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + k * 32 + lane);
+              acc[k].x = fmaf(v.x, wr, acc[k].x);
+              acc[k].y = fmaf(v.y, wr, acc[k].y);
+              acc[k].z = fmaf(v.z, wr, acc[k].z);
+              acc[k].w = fmaf(v.w, wr, acc[k].w);
+            }
+          }
+        }
+      }
+      const float lse = finish(top, lsum, &inv);
+      if (p.lse && grp == 0 && mine) p.lse[(size_t)head * p.total_q + tok] = lse;
+      const long long at = mine ? ((long long)tok * p.Hq + head) * HEAD_DIM + 64 * grp : -1;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        if (2 * k < nr) {
+          const int row = 2 * k + (lane >> 4);
+          const float f = __shfl_sync(0xffffffffu, inv, row);
+          const long long to = __shfl_sync(0xffffffffu, at, row);
+          if (to >= 0) {
+            uint2 o;
+            o.x = pack2<BF16>(acc[k].x * f, acc[k].y * f);
+            o.y = pack2<BF16>(acc[k].z * f, acc[k].w * f);
+            *reinterpret_cast<uint2*>(p.out + to + (lane & 15) * 4) = o;
+          }
+        }
+      }
+    };
+    bool ok = true;
+    int m = 0;    // step counter across units
+    int cnt = 0, oth = 0;  // steps of this group and of the other one so far
+    Cyc<STAGES> rg;
+    Cyc<NBUF> bc;
+    Unit prev{};
+    float prev_M = -INFINITY, prev_l = 0.f, prev_sink2 = -INFINITY;
+    int j = 0;
+    for (; ok; ++j) {
+      ok = mbar_wait_warp(smem_u32(&s.bar_q_full), j & 1, wc, TAG_Q);
+      if (!ok) break;
+      const Unit un = s.unit;
+      if (un.N < 0) break;
+      const int rows = min(p.tile_tokens, un.n - un.tok0) * p.group;
+      const bool busy = sp * 32 < rows;  // some row of this warp is a token's
+      // Q rows into TMEM as 16-bit pairs (element 2c in the low half of
+      // column c): this warp copies d columns 64 grp .. 64 grp + 63 of its
+      // rows.  S of this group's last step is complete; the other group's last
+      // one, which may be the later of the two, is waited for.
+      if (oth > 0)
+        ok = mbar_wait_warp(smem_u32(&s.bar_s_full[grp ^ 1][(oth - 1) & 1]), ((oth - 1) >> 1) & 1,
+                            wc, TAG_S_FULL);
+      tc_fence_after();
+      if (ok && busy && un.N > 0) {
+        const uint8_t* src = s.Q + grp * (Q_TILE * 128) + rloc * 128;
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + ((c ^ (rloc & 7)) << 4));
+          w[4 * c] = v.x;
+          w[4 * c + 1] = v.y;
+          w[4 * c + 2] = v.z;
+          w[4 * c + 3] = v.w;
+        }
+        tmem_st32(lane_base + COL_QA + 32 * grp, w);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.bar_qa_full));
+      // the previous unit's epilogue overlaps this unit's first MMAs
+      if (j >= 1) epilogue(j - 1, prev, prev_M, prev_l, prev_sink2, ok);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
+
+      // this group's running maximum M (log2 domain) and its row sum; the sink
+      // joins at the unit's end
+      const float sink2 =
+          p.sink && rloc < rows ? p.sink[un.kvh * p.group + hh] * LOG2E : -INFINITY;
+      float M = -INFINITY, l = 0.f;
+      const Walk w(p, un.n, un.L, un.tok0);
+      // the row's position; rows that are no token's see nothing
+      const int x0 = un.L - un.n + un.tok0;
+      const int x = rloc < rows ? x0 + tl : -1;
+      const int x_last = x0 + (rows - 1) / p.group;
+      int last_bf = 0;       // buffer of this group's previous step of the unit
+      uint32_t last_ph = 0;  // and the parity of its use
+      for (int i = 0; ok && i < un.N; ++i, ++m, rg.next(), bc.next()) {
+        if ((i & 1) != grp) {
+          ++oth;
+          continue;
+        }
+        const int st = rg.i, bf = bc.i;
+        // s_full implies the stage's loads landed; waiting on kv_full as well
+        // makes the step's tile index (written by the loader) visible
+        ok = mbar_wait_warp(smem_u32(&s.bar_s_full[grp][cnt & 1]), (cnt >> 1) & 1, wc,
+                            TAG_S_FULL) &&
+             mbar_wait_warp(smem_u32(&s.bar_kv_full[st]), rg.ph, wc, TAG_KV_FULL);
+        if (!ok) break;
+        ++cnt;
+        if (!busy) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.bar_p_full[bf]));
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t col = COL_S + 64 * bf;
+        float sv[64];
+        tmem_ld32(lane_base + col, *reinterpret_cast<float(*)[32]>(&sv[0]));
+        tmem_ld32(lane_base + col + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
+        const int k0 = s.step_t[st] * Q_SUB;
+        // warp-uniform: every row of the tile sees every key of the sub-tile
+        const bool full =
+            k0 + Q_SUB <= un.L &&
+            (!p.causal || (k0 + Q_SUB - 1 <= x0 &&
+                           (x_last - k0 < p.window || k0 + Q_SUB <= p.first)));
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+        if (!full) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int j0 = k0 + 32 * q;
+            vis[q] = rloc < rows ? bit_range(0, un.L - 1 - j0) : 0u;
+            if (p.causal)
+              vis[q] &= bit_range(0, x - j0) & (bit_range(x - p.window + 1 - j0, 31) |
+                                                bit_range(0, p.first - 1 - j0));
+          }
+        }
+        tmem_wait_ld_regs(sv);
+        // row maximum of the visible raw logits (the scale is positive, so
+        // it is applied once afterwards); eight partial maxima and sums keep
+        // the dependency chains short
+        float mp[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mp[c] = -INFINITY;
+        if (!full) {
+          // invisible logits drop out of the maximum
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            sv[c] = ((vis[0] >> c) & 1u) ? sv[c] : -INFINITY;
+            sv[32 + c] = ((vis[1] >> c) & 1u) ? sv[32 + c] : -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) mp[c & 7] = fmax3f(mp[c & 7], sv[2 * c], sv[2 * c + 1]);
+        const float mx = fmax3f(fmax3f(mp[0], mp[1], mp[2]), fmax3f(mp[3], mp[4], mp[5]),
+                                fmaxf(mp[6], mp[7]));
+        const float mx2 = mx == -INFINITY ? -INFINITY : mx * p.scale_log2;
+        // move M when the row maximum exceeds it by more than 8; a row that
+        // has seen nothing yet (M = -inf, so O and l are still zero) just
+        // takes the new value
+        float alpha = 1.f;
+        if (mx2 > M + RESCALE_LOG2) {
+          if (M != -INFINITY) alpha = fast_exp2(M - mx2);
+          M = mx2;
+          l *= alpha;
+        }
+        // P = exp2(S scale log2e - M): an invisible logit (-inf here) gives 0;
+        // a row with nothing visible keeps M = -inf and all its logits at
+        // -inf, and the finite stand-in keeps -inf - (-inf) out
+        const float Ms = M == -INFINITY ? 0.f : M;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-Ms, -Ms);
+        uint32_t pk[32];
+        float2 lp[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) lp[c] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float2 xx = ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nm2);
+          const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+          lp[c & 3] = fadd2(lp[c & 3], pp);
+          pk[c] = pack2<BF16>(pp.x, pp.y);
+        }
+        const float2 ls = fadd2(fadd2(lp[0], lp[1]), fadd2(lp[2], lp[3]));
+        l += ls.x + ls.y;
+        // rescale this group's O rows whose M moved, once the group's
+        // previous O += P V of the unit has completed (the unit's first
+        // accumulation of the group overwrites instead)
+        if (i >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          ok = mbar_wait_warp(smem_u32(&s.bar_p_free[last_bf]), last_ph, wc, TAG_P_FREE);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v[32];
+            tmem_ld32(lane_base + COL_O + 128 * grp + 32 * q, reinterpret_cast<float(&)[32]>(v));
+            tmem_wait_ld_regs(reinterpret_cast<float(&)[32]>(v));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
+            tmem_st32(lane_base + COL_O + 128 * grp + 32 * q, v);
+          }
+        }
+        tmem_st32(lane_base + col, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.bar_p_full[bf]));
+        last_bf = bf;
+        last_ph = bc.ph;
+      }
+      prev = un;
+      prev_M = M;
+      prev_l = l;
+      prev_sink2 = sink2;
+    }
+    if (j >= 1) epilogue(j - 1, prev, prev_M, prev_l, prev_sink2, ok);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap& tQ,
+                             const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st) {
+  using namespace paged_side;
+  const auto kern = bf16 ? k_paged_fwd<true> : k_paged_fwd<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  k_paged_schedule<<<1, SCHED_THREADS, 0, st>>>(p, p.grid);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.grid);
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tQ, tK, tV, p);
+}
+
+}  // namespace mab

@@ -67,4 +67,42 @@ inline bool make_thd_map(CUtensorMap* m, const void* base, bool bf16, int64_t T,
   return r == CUDA_SUCCESS;
 }
 
+// Rows [T, H, 128] of new tokens, read as (token, head) rows: a box of 64
+// columns, `heads` heads and `tokens` tokens is heads * tokens rows in shared
+// memory, token by token.
+inline bool make_rows_map(CUtensorMap* m, const void* base, bool bf16, int64_t T, int64_t H,
+                          uint32_t heads, uint32_t tokens) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {128, (cuuint64_t)H, (cuuint64_t)T};
+  cuuint64_t strides[2] = {128 * 2, (cuuint64_t)H * 128 * 2};
+  cuuint32_t box[3] = {64, heads, tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                   const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Cache pages as (head dim, row, kv head, page) with the given strides in
+// elements and a box of 64 columns and `rows` rows of one head of one page.
+// A page number past the last reads zeros.
+inline bool make_pages_map(CUtensorMap* m, const void* base, bool bf16, int64_t pages,
+                           int64_t page_size, int64_t heads, int64_t page_stride,
+                           int64_t head_stride, int64_t token_stride, uint32_t rows) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {128, (cuuint64_t)page_size, (cuuint64_t)heads, (cuuint64_t)pages};
+  cuuint64_t strides[3] = {(cuuint64_t)token_stride * 2, (cuuint64_t)head_stride * 2,
+                           (cuuint64_t)page_stride * 2};
+  cuuint32_t box[4] = {64, rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace mab
