@@ -436,7 +436,7 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUten
     };
     bool ok = true;
     int m = 0;    // step counter across units
-    int cnt = 0;  // steps of this group so far
+    int cnt = 0, oth = 0;  // steps of this group and of the other one so far
     Cyc<STAGES> rg;
     Cyc<NBUF> bc;
     FwdDone prev{0, 0, 0, 0};
@@ -450,8 +450,12 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUten
       un.init(p, u);
       // Q rows into TMEM as 16-bit pairs (element 2c in the low half of
       // column c): this warp copies d columns 64 grp .. 64 grp + 63 of its
-      // rows.  Every S MMA of the previous unit completed before its last
-      // step was signalled, so the columns are free.
+      // rows.  S of this group's last step is complete; the other group's last
+      // one, which may be the later of the two, is waited for.
+      if (oth > 0 && !mbar_wait(smem_u32(&s.bar_s_full[grp ^ 1][(oth - 1) & 1]),
+                                ((oth - 1) >> 1) & 1, wc, TAG_S_FULL))
+        ok = false;
+      tc_fence_after();
       {
         const uint8_t* src = s.Q + grp * (Q_TILE * 128) + rloc * 128;
         uint32_t w[32];
@@ -485,7 +489,10 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUten
       int last_bf = 0;       // buffer of this group's previous step of the unit
       uint32_t last_ph = 0;  // and the parity of its use
       for (int n = 0; ok && n < un.walk.cnt; ++n, ++m, rg.next(), bc.next()) {
-        if ((n & 1) != grp) continue;
+        if ((n & 1) != grp) {
+          ++oth;
+          continue;
+        }
         const int st = rg.i, bf = bc.i;
         // s_full implies the stage's loads landed; waiting on kv_full as well
         // makes the step's tile index (written by the producer) visible
