@@ -59,7 +59,7 @@ constexpr int NO_PAGE = (int)0x80000000;
 // A unit's piece, as the loader publishes it.
 struct Unit {
   int kvh, off, n, L, tok0;  // kv head; the request's first row, new tokens, keys; first token
-  int N;                     // steps of the piece
+  int s0, N;                 // first step and steps of the piece
   int pieces, slot, c0;      // pieces of the unit; this one's slot; CTA of the first one
 };
 
@@ -106,6 +106,10 @@ struct Cyc {
   }
 };
 
+// The schedule's shared memory for B requests: costs, new tokens, keys.
+constexpr size_t sched_smem(int B) { return (size_t)(B + 1) * 8 + (size_t)B * 8; }
+static_assert(PAGED_MAX_CTAS < 32 * 32, "one lane of the schedule's block per cut");
+
 // New tokens and keys of request b.
 __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
   return packed_len(p.cu_q, b, p.total_q, p.Sq);
@@ -151,11 +155,11 @@ __global__ void __launch_bounds__(paged_side::SCHED_THREADS)
 k_paged_schedule(const PagedParams p, int grid) {
   using namespace paged_side;
   grid_launch_dependents();
-  __shared__ long long base[PAGED_MAX_B + 1];  // cost of the requests before b
+  extern __shared__ long long base[];  // [B + 1] cost of the requests before b
+  int* s_n = reinterpret_cast<int*>(base + p.B + 1);  // [B] new tokens
+  int* s_L = s_n + p.B;                               // [B] keys
   __shared__ long long warp_tot[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < (int)(sizeof(DevStatus) / 4)) reinterpret_cast<unsigned*>(p.status)[tid] = 0u;
-  for (int i = tid; i < grid * PAGED_TICKETS; i += SCHED_THREADS) p.ticket[i] = 0;
   long long carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += SCHED_THREADS) {
     const int b = b0 + tid;
@@ -164,6 +168,8 @@ k_paged_schedule(const PagedParams p, int grid) {
       n = new_tokens(p, b);
       L = keys_of(p, b);
       tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
+      s_n[b] = n;
+      s_L[b] = L;
     }
     long long w = tiles > 0 ? unit_cost(p, n, L, 0) : 0;
     // several tiles: the warp adds their costs, one request after another
@@ -203,64 +209,80 @@ k_paged_schedule(const PagedParams p, int grid) {
     carry += warp_tot[31];
   }
   if (tid == 0) base[p.B] = carry;
+  if (tid < (int)(sizeof(DevStatus) / 4)) reinterpret_cast<unsigned*>(p.status)[tid] = 0u;
+  for (int i = tid; i < grid * PAGED_TICKETS; i += SCHED_THREADS) p.ticket[i] = 0;
   __syncthreads();
   const long long total = carry;
   // parts of at least PAGED_MIN_COST: further cuts would cost more to join
   const long long most = total / PAGED_MIN_COST;
   const int parts = (int)(most < 1 ? 1 : most < grid ? most : grid);
-  for (int c = warp; c <= grid; c += SCHED_THREADS / 32) {
-    int4 r = make_int4(p.B, 0, 0, 0);  // past the last unit
-    const long long cut = c < parts ? total / parts * c + total % parts * c / parts : total;
-    if (cut < total) {
-      int lo = 0, hi = p.B - 1;  // the request that holds the cut: the last with base <= cut
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (base[mid] <= cut) lo = mid;
-        else hi = mid - 1;
-      }
-      const int b = lo;
-      const long long head = (base[b + 1] - base[b]) / p.Hkv;
-      int kvh = (int)((cut - base[b]) / head);
-      long long rem = (cut - base[b]) - kvh * head;
-      const int n = new_tokens(p, b), L = keys_of(p, b);
-      const int tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
-      int tile = 0, cost = 0;
-      for (int t0 = 0; t0 < tiles; t0 += 32) {
-        const int mine = t0 + lane < tiles ? unit_cost(p, n, L, t0 + lane) : 0;
-        long long v = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long u = __shfl_up_sync(0xffffffffu, v, d);
-          if (lane >= d) v += u;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, v > rem);
-        if (past) {
-          const int src = __ffs(past) - 1;
-          tile = t0 + src;
-          cost = __shfl_sync(0xffffffffu, mine, src);
-          rem -= __shfl_sync(0xffffffffu, v, src) - cost;
-          break;
-        }
-        rem -= __shfl_sync(0xffffffffu, v, 31);
-      }
-      // the unit's own cost stands before its steps; a cut beside its first or
-      // last step moves to the unit's edge
-      int step = (int)rem - PAGED_UNIT_COST;
-      if (step <= 0) step = 0;
-      if (cost - (int)rem <= 1 && step > 0) {
-        step = 0;
-        if (++tile == tiles) {
-          tile = 0;
-          if (++kvh == p.Hkv) {
-            kvh = 0;
-            lo = b + 1;
-            while (lo < p.B && base[lo + 1] == base[lo]) ++lo;
-          }
-        }
-      }
-      r = make_int4(lo, kvh, tile, step);
+  // lane l of warp w places cut w + 32 l
+  const int c = warp + 32 * lane;
+  const long long cut = c < parts ? total / parts * c + total % parts * c / parts : total;
+  int b = p.B, kvh = 0, tile = 0, tiles = 0, cost = 0, n = 0, L = 0;  // past the last unit
+  long long rem = 0;  // the cut's distance from the start of the head, then of the tile
+  if (c <= grid && cut < total) {
+    int lo = 0, hi = p.B - 1;  // the request that holds the cut: the last with base <= cut
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (base[mid] <= cut) lo = mid;
+      else hi = mid - 1;
     }
-    if (lane == 0) p.start[c] = r;
+    b = lo;
+    const long long head = (base[b + 1] - base[b]) / p.Hkv;
+    kvh = (int)((cut - base[b]) / head);
+    rem = (cut - base[b]) - kvh * head;
+    n = s_n[b];
+    L = s_L[b];
+    tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
+    cost = (int)head;  // of the only tile
+  }
+  // several tiles: the warp looks for the cut's, one cut after another
+  for (unsigned todo = __ballot_sync(0xffffffffu, tiles > 1); todo; todo &= todo - 1) {
+    const int src = __ffs(todo) - 1;
+    const int sn = __shfl_sync(0xffffffffu, n, src), sL = __shfl_sync(0xffffffffu, L, src);
+    const int st = __shfl_sync(0xffffffffu, tiles, src);
+    long long srem = __shfl_sync(0xffffffffu, rem, src);
+    for (int t0 = 0; t0 < st; t0 += 32) {
+      const int mine = t0 + lane < st ? unit_cost(p, sn, sL, t0 + lane) : 0;
+      long long v = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += u;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, v > srem);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        const int found = __shfl_sync(0xffffffffu, mine, at);
+        const long long upto = __shfl_sync(0xffffffffu, v, at);
+        if (lane == src) {
+          tile = t0 + at;
+          cost = found;
+          rem = srem - (upto - found);
+        }
+        break;
+      }
+      srem -= __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  if (c <= grid) {
+    // the unit's own cost stands before its steps; a cut beside its first or
+    // last step moves to the unit's edge
+    int step = (int)rem - PAGED_UNIT_COST;
+    if (step <= 0) step = 0;
+    if (step > 0 && cost - (int)rem <= 1) {
+      step = 0;
+      if (++tile == tiles) {
+        tile = 0;
+        if (++kvh == p.Hkv) {
+          kvh = 0;
+          ++b;
+          while (b < p.B && base[b + 1] == base[b]) ++b;
+        }
+      }
+    }
+    p.start[c] = make_int4(b, kvh, tile, step);
   }
 }
 
@@ -378,6 +400,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         s.unit.n = n;
         s.unit.L = L;
         s.unit.tok0 = tok0;
+        s.unit.s0 = s0;
         s.unit.N = s1 - s0;
         s.unit.pieces = cuts + 1;
         s.unit.slot = 2 * cta + (s0 > 0 ? 0 : 1);
@@ -513,15 +536,18 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         const int N = s.unit.N;
         if (N < 0) break;
         const Walk w(p, s.unit.n, s.unit.L, s.unit.tok0);
+        const int s0 = s.unit.s0;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
         for (int i = 0; ok && i < N; ++i, ++m, rg.next(), bc.next()) {
           const int st = rg.i, bf = bc.i;
           // unseen rows of V cleared while S and the softmax of the step run
-          ok = mbar_wait_warp(smem_u32(&s.bar_kv_full[st]), rg.ph, wc, TAG_KV_FULL);
-          if (!ok) break;
-          const int k0 = s.step_t[st] * Q_SUB;
+          // (only these steps wait for their loads here: a wait costs an
+          // issuing warp 150 to 300 cycles)
+          const int k0 = w.tile(s0 + i) * Q_SUB;
           if (!w.all(k0, k0 + Q_SUB)) {
+            ok = mbar_wait_warp(smem_u32(&s.bar_kv_full[st]), rg.ph, wc, TAG_KV_FULL);
+            if (!ok) break;
             // 8 lanes per 128-byte row: four rows of a half at a time
             for (int r = lane >> 3; r < Q_SUB; r += 4)
               if (!w.sees(k0 + r)) {
@@ -699,34 +725,53 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
                wq * PAGED_WARP_FLOATS;
       };
       float top = -INFINITY, lsum = 0.f;
+#pragma unroll 8
       for (int i = 0; i < un.pieces; ++i)
         if (mine) top = fmaxf(top, __ldcg(piece(i) + 2048 + 2 * lane));
       // lane -> 4 columns of rows 2 k + lane / 16
       float4 acc[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < un.pieces; ++i) {
-        const float* src = piece(i);
-        float wt = 0.f;
-        if (mine) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + 2048) + lane);
-          wt = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
-          lsum += ml.y * wt;
+      // the weights of 32 pieces at a time, in this warp's staging space
+      float* wts = reinterpret_cast<float*>(stage);
+      for (int i0 = 0; i0 < un.pieces; i0 += 32) {
+        const int cntp = min(32, un.pieces - i0);
+        __syncwarp();
+#pragma unroll 8
+        for (int i = 0; i < cntp; ++i) {
+          float wt = 0.f;
+          if (mine) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + i) + 2048) + lane);
+            wt = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
+            lsum += ml.y * wt;
+          }
+          wts[i * 32 + lane] = wt;
         }
+        __syncwarp();
+        // 8 rows at a time, several pieces' loads in flight
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          if (2 * k < nr) {
-            const float wr = __shfl_sync(0xffffffffu, wt, 2 * k + (lane >> 4));
-            if (2 * k + (lane >> 4) < nr) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + k * 32 + lane);
-              acc[k].x = fmaf(v.x, wr, acc[k].x);
-              acc[k].y = fmaf(v.y, wr, acc[k].y);
-              acc[k].z = fmaf(v.z, wr, acc[k].z);
-              acc[k].w = fmaf(v.w, wr, acc[k].w);
+        for (int kq = 0; kq < 4; ++kq) {
+          if (8 * kq < nr) {
+#pragma unroll 4
+            for (int i = 0; i < cntp; ++i) {
+              const float4* src = reinterpret_cast<const float4*>(piece(i0 + i)) + lane;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const int k = 4 * kq + kk, row = 2 * k + (lane >> 4);
+                // (rows past nr were not written)
+                const float4 v = row < nr ? __ldcg(src + k * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float wr = wts[i * 32 + row];
+                acc[k].x = fmaf(v.x, wr, acc[k].x);
+                acc[k].y = fmaf(v.y, wr, acc[k].y);
+                acc[k].z = fmaf(v.z, wr, acc[k].z);
+                acc[k].w = fmaf(v.w, wr, acc[k].w);
+              }
             }
           }
         }
       }
+      // the next TMA load into the Q tile comes after these accesses to it
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       const float lse = finish(top, lsum, &inv);
       if (p.lse && grp == 0 && mine) p.lse[(size_t)head * p.total_q + tok] = lse;
       const long long at = mine ? ((long long)tok * p.Hq + head) * HEAD_DIM + 64 * grp : -1;
@@ -936,7 +981,10 @@ cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap&
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  k_paged_schedule<<<1, SCHED_THREADS, 0, st>>>(p, p.grid);
+  e = cudaFuncSetAttribute(k_paged_schedule, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)sched_smem(PAGED_MAX_B));
+  if (e != cudaSuccess) return e;
+  k_paged_schedule<<<1, SCHED_THREADS, sched_smem(p.B), st>>>(p, p.grid);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
