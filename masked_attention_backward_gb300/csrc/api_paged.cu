@@ -65,7 +65,7 @@ PagedLayout paged_layout(const attn_shape_t* sh) {
   L.status = off;
   off = align256(off + sizeof(DevStatus));
   L.start = off;
-  off = align256(off + (PAGED_MAX_CTAS + 1) * sizeof(int4));
+  off = align256(off + (PAGED_MAX_CTAS + 1) * sizeof(PagedStart));
   L.ticket = off;
   off = align256(off + PAGED_MAX_CTAS * PAGED_TICKETS * sizeof(int));
   L.part = off;
@@ -189,6 +189,7 @@ attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* page
   p.table_stride = table_stride;
   p.num_pages = pages->num_pages;
   p.page_size = pages->page_size;
+  p.inv_page_size = 1.0f / (float)pages->page_size;
   p.box_rows = pages->page_size % 64 == 0 ? 64 : pages->page_size % 32 == 0 ? 32 : 16;
   p.sink = sink;
   p.out = static_cast<uint16_t*>(o);
@@ -197,7 +198,7 @@ attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* page
   p.status = reinterpret_cast<DevStatus*>(w + L.status);
   p.timeout_ns = wait_timeout_ns();
   p.test_no_loads = test_no_loads();
-  p.start = reinterpret_cast<int4*>(w + L.start);
+  p.start = reinterpret_cast<PagedStart*>(w + L.start);
   p.ticket = reinterpret_cast<int*>(w + L.ticket);
   p.part = reinterpret_cast<float*>(w + L.part);
   p.slot_floats = L.slot_floats;

@@ -17,6 +17,14 @@ constexpr int PAGED_WARP_FLOATS = 32 * 64 + 32 * 2;
 constexpr int PAGED_UNIT_COST = 2;
 constexpr int PAGED_MIN_COST = 8;
 
+// Where a CTA's part of the line begins, and what the loader needs there: the
+// cuts inside that unit (of CTAs first_cut ..), the request's rows and lengths.
+struct __align__(16) PagedStart {
+  int b, kvh, tile, step;
+  int first_cut, cuts;
+  int off, n, L, pad_[3];
+};
+
 // Everything the attention over the pages reads besides the tensor maps.
 struct PagedParams {
   int B, Hq, Hkv, group, Sq, Skv, total_q;
@@ -26,6 +34,7 @@ struct PagedParams {
   const int* seqlen_k;
   const int* table;
   int table_stride, num_pages, page_size, box_rows;  // box_rows: rows of one load
+  float inv_page_size;
   const float* sink;
   uint16_t* out;
   float* lse;  // or nullptr
@@ -34,7 +43,7 @@ struct PagedParams {
   unsigned long long timeout_ns;
   int test_no_loads;
   int grid;          // CTAs
-  int4* start;       // [grid + 1] where each CTA begins: request, kv head, tile, step
+  PagedStart* start; // [grid + 1]
   int* ticket;       // [grid, PAGED_TICKETS] pieces done of the unit that the CTA's part ends in
   float* part;       // [2 grid, slot_floats] pieces
   int slot_floats;

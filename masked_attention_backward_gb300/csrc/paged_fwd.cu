@@ -28,9 +28,9 @@
 // pieces per CTA whatever the lengths, which stay on the device.
 //
 // The inner loop is that of the BHSD forward kernel (attn_fwd.cu): warp 0
-// loads (one lane per page run and tile half, page numbers fetched a step
-// ahead), warp 1 issues S = Q K^T, warp 2 O += P V, two groups of four softmax
-// warps take alternate steps.  Rows of V that no row of the unit sees (past
+// loads Q and K, warp 11 V (each a box per run of keys in a page, the page
+// numbers looked up 32 at a time, a batch ahead), warp 1 issues S = Q K^T, warp 2 O += P V, two groups
+// of four softmax warps take alternate steps.  Rows of V that no row of the unit sees (past
 // the last key, before the window, between the first keys and it) may hold
 // anything, NaN included, and 0 * NaN is NaN in the matrix unit: the page runs
 // without a seen key are not loaded (zeros stand in), and warp 2 clears the
@@ -51,15 +51,18 @@ constexpr int COL_QA = 256;      // Q as the A operand, 64 columns of 16-bit pai
 constexpr int COL_S = 320;       // S buffer b at COL_S + 64 b
 constexpr int SM_WARP0 = 3;      // first softmax warp
 constexpr int SM_WARPS = 8;      // softmax warps, two groups of four
-constexpr int NUM_THREADS = 32 * (SM_WARP0 + SM_WARPS);
+constexpr int V_WARP = SM_WARP0 + SM_WARPS;  // loader of V
+constexpr int NUM_THREADS = 32 * (V_WARP + 1);
 constexpr float RESCALE_LOG2 = 8.f;  // M moves when a row maximum exceeds it by this
 constexpr int SCHED_THREADS = 1024;
+constexpr unsigned long long DRAIN_NS = 10000000ull;  // a copy in flight lands well within 10 ms
 constexpr int NO_PAGE = (int)0x80000000;
 
 // A unit's piece, as the loader publishes it.
 struct Unit {
   int kvh, off, n, L, tok0;  // kv head; the request's first row, new tokens, keys; first token
   int s0, N;                 // first step and steps of the piece
+  int b;                     // the request
   int pieces, slot, c0;      // pieces of the unit; this one's slot; CTA of the first one
 };
 
@@ -69,8 +72,8 @@ struct __align__(1024) Smem {
   uint8_t K[STAGES][2 * Q_SUB * 128];
   uint8_t V[STAGES][2 * Q_SUB * 128];
   float xml[2][2][Q_TILE][2];   // [unit parity][group][row]: (M, l) at the piece's end
-  int step_t[STAGES];           // key sub-tile of the step in the stage
   Unit unit;                    // piece of the latest Q load, N < 0: none left
+  uint64_t bar_unit;            // unit published (the loader of V does not wait for Q)
   uint64_t bar_q_full;
   uint64_t bar_qa_full;         // Q copied into TMEM (all softmax warps)
   uint64_t bar_kv_full[STAGES];
@@ -92,7 +95,7 @@ constexpr size_t SMEM_BYTES = sizeof(Smem) + 1024;
 static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
 
 enum { TAG_Q = 0x501, TAG_QA, TAG_KV_EMPTY, TAG_KV_FULL, TAG_S_FULL, TAG_P_FULL, TAG_P_FREE,
-       TAG_ACC, TAG_ACC_EMPTY, TAG_UNIT_FREE, TAG_XML };
+       TAG_ACC, TAG_ACC_EMPTY, TAG_UNIT_FREE, TAG_XML, TAG_UNIT };
 
 template <int NS>
 struct Cyc {
@@ -147,10 +150,107 @@ __device__ __forceinline__ int unit_cost(const PagedParams& p, int n, int L, int
   return Walk(p, n, L, tile * p.tile_tokens).cnt + PAGED_UNIT_COST;
 }
 
+// Row sum and LSE of a row with maximum m_row and sum l_row, the sink (log2
+// domain) joined; *inv is what the row's O is multiplied by.
+__device__ __forceinline__ float finish_row(float m_row, float l_row, float sink2, float* inv) {
+  const float top = fmaxf(m_row, sink2);
+  *inv = 0.f;
+  if (top == -INFINITY) return INFINITY;  // no key and no sink
+  const float e = l_row > 0.f ? fast_exp2(m_row - top) : 0.f;
+  float lt = l_row * e;
+  if (sink2 > -INFINITY) lt += fast_exp2(sink2 - top);
+  if (!(lt > 0.f)) return INFINITY;
+  *inv = e / lt;
+  return (top + log2f(lt)) * 0.6931471805599453f;
+}
+
+constexpr size_t NO_LSE = ~(size_t)0;
+
+// Adds up a split unit's pieces, in their order, for one softmax warp's rows
+// and columns, and stores them.  Lane i knows row i: its sink, its place
+// row_at in the packed rows (-1: none) and lse_at in lse.
+template <bool BF16>
+__device__ __forceinline__ void join_pieces(const PagedParams& p, int c0, int pieces, int wq, int nr,
+                                         float sink2, long long row_at, size_t lse_at, int col0,
+                                         float* stage) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < nr;
+  // slots: 2 c0 + 1, then 2 c for the CTAs after c0
+  auto piece = [&](int i) -> const float* {
+    return p.part + (size_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * p.slot_floats +
+           wq * PAGED_WARP_FLOATS;
+  };
+  float top = -INFINITY, lsum = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < pieces; ++i)
+    if (mine) top = fmaxf(top, __ldcg(piece(i) + 2048 + 2 * lane));
+  // lane -> 4 columns of rows 2 k + lane / 16
+  float4 acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the weights of 32 pieces at a time, in this warp's staging space
+  float* wts = stage;
+  for (int i0 = 0; i0 < pieces; i0 += 32) {
+    const int cntp = min(32, pieces - i0);
+    __syncwarp();
+#pragma unroll 8
+    for (int i = 0; i < cntp; ++i) {
+      float wt = 0.f;
+      if (mine) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + i) + 2048) + lane);
+        wt = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
+        lsum += ml.y * wt;
+      }
+      wts[i * 32 + lane] = wt;
+    }
+    __syncwarp();
+    // 8 rows at a time, several pieces' loads in flight
+#pragma unroll
+    for (int kq = 0; kq < 4; ++kq) {
+      if (8 * kq < nr) {
+#pragma unroll 4
+        for (int i = 0; i < cntp; ++i) {
+          const float4* src = reinterpret_cast<const float4*>(piece(i0 + i)) + lane;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int k = 4 * kq + kk, row = 2 * k + (lane >> 4);
+            // (rows past nr were not written)
+            const float4 v = row < nr ? __ldcg(src + k * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float wr = wts[i * 32 + row];
+            acc[k].x = fmaf(v.x, wr, acc[k].x);
+            acc[k].y = fmaf(v.y, wr, acc[k].y);
+            acc[k].z = fmaf(v.z, wr, acc[k].z);
+            acc[k].w = fmaf(v.w, wr, acc[k].w);
+          }
+        }
+      }
+    }
+  }
+  // the next TMA load into the Q tile comes after these accesses to it
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  float inv;
+  const float lse = finish_row(top, lsum, sink2, &inv);
+  if (p.lse && lse_at != NO_LSE && mine) p.lse[lse_at] = lse;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    if (2 * k < nr) {
+      const int row = 2 * k + (lane >> 4);
+      const float f = __shfl_sync(0xffffffffu, inv, row);
+      const long long to = __shfl_sync(0xffffffffu, row_at, row);
+      if (to >= 0) {
+        uint2 o;
+        o.x = pack2<BF16>(acc[k].x * f, acc[k].y * f);
+        o.y = pack2<BF16>(acc[k].z * f, acc[k].w * f);
+        *reinterpret_cast<uint2*>(p.out + to * HEAD_DIM + col0 + (lane & 15) * 4) = o;
+      }
+    }
+  }
+}
+
 }  // namespace paged_side
 
 // One block.  Lays the units (request, kv head, query tile) end to end and
-// writes where each CTA's part begins: {request, kv head, tile, step}.
+// writes where each CTA's part begins.
 __global__ void __launch_bounds__(paged_side::SCHED_THREADS)
 k_paged_schedule(const PagedParams p, int grid) {
   using namespace paged_side;
@@ -159,7 +259,10 @@ k_paged_schedule(const PagedParams p, int grid) {
   int* s_n = reinterpret_cast<int*>(base + p.B + 1);  // [B] new tokens
   int* s_L = s_n + p.B;                               // [B] keys
   __shared__ long long warp_tot[32];
+  __shared__ int s_units;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_units = 0;
+  __syncthreads();
   long long carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += SCHED_THREADS) {
     const int b = b0 + tid;
@@ -184,6 +287,8 @@ k_paged_schedule(const PagedParams p, int grid) {
       if (lane == src) w = sum;
     }
     w *= p.Hkv;
+    const int units = __reduce_add_sync(0xffffffffu, min(tiles, PAGED_MAX_CTAS) * p.Hkv);
+    if (lane == 0 && units) atomicAdd(&s_units, min(units, 1 << 16));
     // inclusive scan over the block
     long long v = w;
 #pragma unroll
@@ -213,14 +318,15 @@ k_paged_schedule(const PagedParams p, int grid) {
   for (int i = tid; i < grid * PAGED_TICKETS; i += SCHED_THREADS) p.ticket[i] = 0;
   __syncthreads();
   const long long total = carry;
-  // parts of at least PAGED_MIN_COST: further cuts would cost more to join
-  const long long most = total / PAGED_MIN_COST;
+  // a CTA for each unit while there are CTAs, and parts of at least
+  // PAGED_MIN_COST: further cuts would cost more to join
+  const long long most = max(total / PAGED_MIN_COST, (long long)s_units);
   const int parts = (int)(most < 1 ? 1 : most < grid ? most : grid);
   // lane l of warp w places cut w + 32 l
   const int c = warp + 32 * lane;
   const long long cut = c < parts ? total / parts * c + total % parts * c / parts : total;
   int b = p.B, kvh = 0, tile = 0, tiles = 0, cost = 0, n = 0, L = 0;  // past the last unit
-  long long rem = 0;  // the cut's distance from the start of the head, then of the tile
+  long long rem = 0;  // the cut's distance from the start of the head, then of the unit
   if (c <= grid && cut < total) {
     int lo = 0, hi = p.B - 1;  // the request that holds the cut: the last with base <= cut
     while (lo < hi) {
@@ -282,14 +388,33 @@ k_paged_schedule(const PagedParams p, int grid) {
         }
       }
     }
-    p.start[c] = make_int4(b, kvh, tile, step);
+    // cuts inside the unit: those that lie more than its own cost past its
+    // start and more than one step before its end (cut c is at
+    // floor(c total / parts))
+    int first = 0, cuts = 0;
+    if (step > 0) {
+      const long long u0 = cut - rem;
+      first = (int)(((u0 + PAGED_UNIT_COST + 1) * parts + total - 1) / total);
+      cuts = (int)(((u0 + cost - 1) * parts + total - 1) / total) - first;
+    }
+    PagedStart r;
+    r.b = b;
+    r.kvh = kvh;
+    r.tile = tile;
+    r.step = step;
+    r.first_cut = first;
+    r.cuts = cuts;
+    r.off = b < p.B ? packed_off(p.cu_q, b, p.total_q) : 0;
+    r.n = b < p.B ? s_n[b] : 0;
+    r.L = b < p.B ? s_L[b] : 0;
+    p.start[c] = r;
   }
 }
 
 template <bool BF16>
 __global__ void __launch_bounds__(paged_side::NUM_THREADS, 1)
 k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
-            const __grid_constant__ CUtensorMap tV, const PagedParams p) {
+            const __grid_constant__ CUtensorMap tV, const __grid_constant__ PagedParams p) {
   using namespace paged_side;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -299,10 +424,11 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
 
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
+    mbar_init(smem_u32(&s.bar_unit), 1);
     mbar_init(smem_u32(&s.bar_q_full), 1);
     mbar_init(smem_u32(&s.bar_qa_full), SM_WARPS);
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&s.bar_kv_full[i]), 1);
+      mbar_init(smem_u32(&s.bar_kv_full[i]), 2);
       mbar_init(smem_u32(&s.bar_kv_empty[i]), 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -316,7 +442,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     }
     mbar_init(smem_u32(&s.bar_acc_full), 1);
     mbar_init(smem_u32(&s.bar_acc_empty), SM_WARPS);
-    mbar_init(smem_u32(&s.bar_unit_free), SM_WARPS + 2);
+    mbar_init(smem_u32(&s.bar_unit_free), SM_WARPS + 3);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.bar_x_done[i]), 1);
     fence_mbar_init();
     tma_prefetch_desc(&tQ);
@@ -334,23 +460,87 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   // launched over the schedule kernel: its cuts are read from here on
   grid_dependency_wait();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loader (whole warp)
-    const int cta = (int)blockIdx.x;
-    const int4 end = __ldcg(p.start + cta + 1);
-    int4 at = __ldcg(p.start + cta);
-    // lane -> one box of a step: half of K or V, run of box_rows keys
+  // Steps [s0, s0 + N) of a unit, K (which = 0) or V: the boxes of each step
+  // into its stage, behind a full wait for the stage to be free.
+  int m_load = 0;  // steps issued, across units
+  Cyc<STAGES> rg_load;
+  auto load_steps = [&](const Walk& w, int which, int b, int kvh, int s0, int N) -> bool {
+    const CUtensorMap* tm = which ? &tV : &tK;
     const int runs = Q_SUB / p.box_rows;
-    const int part = lane & 3, run = lane >> 2;
-    const bool loads = run < runs;
-    const CUtensorMap* tm = part < 2 ? &tK : &tV;
-    const int c0 = (part & 1) * 64;
+    const int batch = 32 / runs;  // steps whose pages the lanes look up at once
+    const int* row = p.table + (size_t)b * p.table_stride;
+    // lane l: page of run l % runs of step i + l / runs (NO_PAGE: a run without
+    // a seen key), and the run's first row in the page
+    const int l_step = lane / runs, l_run = lane - l_step * runs;
+    int row0 = 0;
+    auto pages_of = [&](int i) -> int {
+      i += l_step;
+      const int k0 = w.tile(i) * Q_SUB + l_run * p.box_rows;
+      const int idx = div_by(k0, p.page_size, p.inv_page_size);
+      row0 = k0 - idx * p.page_size;
+      int page = NO_PAGE;
+      if (i < s0 + N && w.any(k0, k0 + p.box_rows)) page = __ldg(row + idx);
+      return page;
+    };
+    int page = NO_PAGE, prow = 0, next = pages_of(s0), next_row = row0, left = 0;
+    for (int i = s0; i < s0 + N; ++i, ++m_load, rg_load.next(), --left) {
+      const int st = rg_load.i;
+      if (left == 0) {
+        page = next;
+        prow = next_row;
+        left = batch;
+        if ((unsigned)page >= (unsigned)p.num_pages) {
+          // past the tensor's end, where a load reads zeros
+          if (page != NO_PAGE) atomicCAS(&p.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);
+          page = p.num_pages;
+        }
+        next = pages_of(i + batch);  // a batch ahead
+        next_row = row0;
+      }
+      if (m_load >= STAGES &&
+          !mbar_wait_warp(smem_u32(&s.bar_kv_empty[st]), rg_load.ph ^ 1u, wc, TAG_KV_EMPTY))
+        return false;
+      const uint32_t fb = smem_u32(&s.bar_kv_full[st]);
+      if (lane == 0) mbar_arrive_expect_tx(fb, 2 * Q_SUB * 128);
+      __syncwarp();
+      const uint32_t dst = smem_u32(which ? s.V[st] : s.K[st]);
+      for (int r = 0; r < runs; ++r) {
+        const int src = (batch - left) * runs + r;
+        const int pg = __shfl_sync(0xffffffffu, page, src);
+        const int pr = __shfl_sync(0xffffffffu, prow, src);
+        const uint32_t to = dst + r * p.box_rows * 128;
+        tma_load_4d_w(to, tm, 0, pr, kvh, pg, fb);
+        tma_load_4d_w(to + Q_SUB * 128, tm, 64, pr, kvh, pg, fb);
+      }
+    }
+    return true;
+  };
+  // A CTA that gives up lets this warp's copies still in flight land first
+  // (the phase may lack the other loader's part, hence the short limit).
+  auto drain_loads = [&]() {
+    for (int k = m_load > STAGES ? m_load - STAGES : 0; k < m_load; ++k)
+      mbar_drain_warp(smem_u32(&s.bar_kv_full[k % STAGES]), (k / STAGES) & 1, DRAIN_NS);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loader of Q and K
+    const int cta = (int)blockIdx.x;
+    const PagedStart at0 = p.start[cta], end = p.start[cta + 1];
+    int b = at0.b, kvh = at0.kvh, tile = at0.tile, step = at0.step;  // where this CTA stands
+    int off = at0.off, n = at0.n, L = at0.L;                         // of request b
     bool ok = !p.test_no_loads;
-    int m = 0;          // steps issued, across units
     int q_loaded = -1;  // last unit whose Q tile was loaded
-    int b_base = -64;   // lane i holds the lengths of request b_base + i
-    int l_off = 0, l_n = 0, l_L = 0;
-    Cyc<STAGES> rg;
+    // lane i holds the lengths of request b_base + i
+    int b_base = b, l_off = 0, l_n = 0, l_L = 0;
+    auto load_lengths = [&]() {
+      l_off = l_n = l_L = 0;
+      if (b_base + lane < p.B) {
+        l_off = packed_off(p.cu_q, b_base + lane, p.total_q);
+        l_n = new_tokens(p, b_base + lane);
+        l_L = keys_of(p, b_base + lane);
+      }
+    };
+    load_lengths();
     const uint32_t qbar = smem_u32(&s.bar_q_full);
     for (int j = 0; ok; ++j) {
       if (j >= 1 &&
@@ -358,44 +548,24 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         ok = false;
         break;
       }
-      const bool in_end = at.x == end.x && at.y == end.y && at.z == end.z;
-      if (at.x >= p.B || (in_end && end.w <= at.w)) {
+      const bool in_end = b == end.b && kvh == end.kvh && tile == end.tile;
+      if (b >= p.B || (in_end && end.step <= step)) {
         if (lane == 0) {
           s.unit.N = -1;
+          mbar_arrive(smem_u32(&s.bar_unit));
           mbar_arrive(qbar);
         }
         break;
       }
-      if (at.x >= b_base + 32) {
-        b_base = at.x;
-        const int b = b_base + lane;
-        l_off = l_n = l_L = 0;
-        if (b < p.B) {
-          l_off = packed_off(p.cu_q, b, p.total_q);
-          l_n = new_tokens(p, b);
-          l_L = keys_of(p, b);
-        }
-      }
-      const int src = at.x - b_base;
-      const int off = __shfl_sync(0xffffffffu, l_off, src);
-      const int n = __shfl_sync(0xffffffffu, l_n, src), L = __shfl_sync(0xffffffffu, l_L, src);
-      const int tok0 = at.z * p.tile_tokens;
+      const int tok0 = tile * p.tile_tokens;
       const Walk w(p, n, L, tok0);
-      const int s0 = at.w, s1 = in_end ? end.w : w.cnt;
-      // cuts inside this unit: the records of the CTAs that go on with it
-      int cuts = 0, first_cut = 0;
-      if (s0 > 0 || in_end) {
-        for (int c = 0; c < p.grid; c += 32) {
-          int4 r = make_int4(-1, 0, 0, 0);
-          if (c + lane < p.grid) r = __ldcg(p.start + c + lane);
-          const unsigned mine = __ballot_sync(
-              0xffffffffu, r.x == at.x && r.y == at.y && r.z == at.z && r.w > 0);
-          if (mine && cuts == 0) first_cut = c + __ffs(mine) - 1;
-          cuts += __popc(mine);
-        }
-      }
+      const int s0 = step, s1 = in_end ? end.step : w.cnt;
+      // cuts inside this unit: the CTAs that go on with it
+      const int cuts = s0 > 0 ? at0.cuts : in_end ? end.cuts : 0;
+      const int first_cut = s0 > 0 ? at0.first_cut : end.first_cut;
       if (lane == 0) {
-        s.unit.kvh = at.y;
+        s.unit.b = b;
+        s.unit.kvh = kvh;
         s.unit.off = off;
         s.unit.n = n;
         s.unit.L = L;
@@ -405,88 +575,59 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         s.unit.pieces = cuts + 1;
         s.unit.slot = 2 * cta + (s0 > 0 ? 0 : 1);
         s.unit.c0 = first_cut - 1;
+        mbar_arrive(smem_u32(&s.bar_unit));
         if (s1 == s0) {
           mbar_arrive(qbar);  // no key to see: no Q either
         } else {
           mbar_arrive_expect_tx(qbar, 2 * p.tile_rows * 128);
-          tma_load_3d(smem_u32(s.Q), &tQ, 0, at.y * p.group, off + tok0, qbar);
-          tma_load_3d(smem_u32(s.Q + Q_TILE * 128), &tQ, 64, at.y * p.group, off + tok0, qbar);
+          tma_load_3d(smem_u32(s.Q), &tQ, 0, kvh * p.group, off + tok0, qbar);
+          tma_load_3d(smem_u32(s.Q + Q_TILE * 128), &tQ, 64, kvh * p.group, off + tok0, qbar);
         }
       }
+      __syncwarp();
       if (s1 > s0) q_loaded = j;
-      // this lane's page of step i (NO_PAGE: a run without a seen key), and its
-      // first row in the page
-      const int* row = p.table + (size_t)at.x * p.table_stride;
-      int row0 = 0;
-      auto page_of = [&](int i) -> int {
-        const int k0 = w.tile(i) * Q_SUB + run * p.box_rows;
-        if (!loads || !w.any(k0, k0 + p.box_rows)) return NO_PAGE;
-        const int idx = k0 / p.page_size;
-        row0 = k0 - idx * p.page_size;
-        return __ldg(row + idx);
-      };
-      int next = s1 > s0 ? page_of(s0) : NO_PAGE, next_row = row0;
-      for (int i = s0; i < s1; ++i, ++m, rg.next()) {
-        int page = next;
-        const int prow = next_row, st = rg.i;
-        if (i + 1 < s1) {
-          next = page_of(i + 1);
-          next_row = row0;
-        }
-        if (m >= STAGES &&
-            !mbar_wait_warp(smem_u32(&s.bar_kv_empty[st]), rg.ph ^ 1u, wc, TAG_KV_EMPTY)) {
-          ok = false;
-          break;
-        }
-        if ((unsigned)page >= (unsigned)p.num_pages) {
-          // past the tensor's end, where a load reads zeros
-          if (page != NO_PAGE) atomicCAS(&p.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);
-          page = p.num_pages;
-        }
-        const uint32_t fb = smem_u32(&s.bar_kv_full[st]);
-        if (lane == 0) {
-          s.step_t[st] = w.tile(i);  // published by the arrive
-          mbar_arrive_expect_tx(fb, 4 * Q_SUB * 128);
-        }
-        __syncwarp();
-        if (loads) {
-          uint8_t* dst = (part < 2 ? s.K[st] : s.V[st]) + (part & 1) * (Q_SUB * 128) +
-                         run * p.box_rows * 128;
-          tma_load_4d(smem_u32(dst), tm, c0, prow, at.y, page, fb);
-        }
+      ok = load_steps(w, 0, b, kvh, s0, s1 - s0);
+      if (in_end) {  // nothing of this CTA is left
+        step = s1;
+        continue;
       }
-      if (in_end) {
-        at = end;  // nothing of this CTA is left
-      } else {
-        at.w = 0;
-        if (++at.z * p.tile_tokens >= n) {
-          at.z = 0;
-          if (++at.y == p.Hkv) {
-            at.y = 0;
-            // the next request with new tokens
-            for (++at.x; at.x < p.B && at.x < end.x; ++at.x) {
-              if (at.x >= b_base + 32) {
-                b_base = at.x;
-                const int b = b_base + lane;
-                l_off = l_n = l_L = 0;
-                if (b < p.B) {
-                  l_off = packed_off(p.cu_q, b, p.total_q);
-                  l_n = new_tokens(p, b);
-                  l_L = keys_of(p, b);
-                }
-              }
-              if (__shfl_sync(0xffffffffu, l_n, at.x - b_base) > 0) break;
-            }
-          }
+      step = 0;
+      if (++tile * p.tile_tokens < n) continue;
+      tile = 0;
+      if (++kvh < p.Hkv) continue;
+      kvh = 0;
+      // the next request with new tokens
+      for (n = 0; n == 0 && ++b < p.B;) {
+        if (b >= b_base + 32) {
+          b_base = b;
+          load_lengths();
         }
+        off = __shfl_sync(0xffffffffu, l_off, b - b_base);
+        n = __shfl_sync(0xffffffffu, l_n, b - b_base);
+        L = __shfl_sync(0xffffffffu, l_L, b - b_base);
+        if (b == end.b) break;
       }
     }
-    if (!ok && lane == 0) {
-      // the CTA gave up: let the copies still in flight land before it exits
-      if (q_loaded >= 0) mbar_drain(qbar, q_loaded & 1, wc.timeout_ns);
-      for (int k = m > STAGES ? m - STAGES : 0; k < m; ++k)
-        mbar_drain(smem_u32(&s.bar_kv_full[k % STAGES]), (k / STAGES) & 1, wc.timeout_ns);
+    if (!ok) {
+      if (q_loaded >= 0) mbar_drain_warp(qbar, q_loaded & 1, DRAIN_NS);
+      drain_loads();
     }
+  } else if (warp == V_WARP) {
+    // ------------------------------------------------------------ loader of V
+    bool ok = true;
+    for (int j = 0; ok; ++j) {
+      if (!mbar_wait_warp(smem_u32(&s.bar_unit), j & 1, wc, TAG_UNIT)) {
+        ok = false;
+        break;
+      }
+      const Unit un = s.unit;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
+      if (un.N < 0) break;
+      const Walk w(p, un.n, un.L, un.tok0);
+      ok = load_steps(w, 1, un.b, un.kvh, un.s0, un.N);
+    }
+    if (!ok) drain_loads();
   } else if (warp < SM_WARP0) {
     // ------------------------------------------------------------ MMA issuers (whole warps)
     bool ok = true;
@@ -623,24 +764,11 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         lx = lg[0] * w[0] + lg[1] * w[1];
       }
       const bool whole = un.pieces == 1;
-      // row sums with the sink, and what O is divided by
-      auto finish = [&](float m_row, float l_row, float* inv) -> float {
-        const float top = fmaxf(m_row, sink2);
-        if (top == -INFINITY) {
-          *inv = 0.f;
-          return INFINITY;  // no key and no sink
-        }
-        const float e = l_row > 0.f ? fast_exp2(m_row - top) : 0.f;
-        float lt = l_row * e;
-        if (sink2 > -INFINITY) lt += fast_exp2(sink2 - top);
-        *inv = lt > 0.f ? e / lt : 0.f;
-        return lt > 0.f ? (top + log2f(lt)) * 0.6931471805599453f : INFINITY;
-      };
       const int tok = un.off + un.tok0 + tl, head = un.kvh * p.group + hh;
       const bool mine = lane < nr;
       float inv = 0.f;
       if (whole) {
-        const float lse = finish(Mx, lx, &inv);
+        const float lse = finish_row(Mx, lx, sink2, &inv);
         if (p.lse && grp == 0 && mine && !gave_up) p.lse[(size_t)head * p.total_q + tok] = lse;
         w[0] *= inv;
         w[1] *= inv;
@@ -719,81 +847,13 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       if (lane == 0) before = atomicAdd(p.ticket + un.c0 * PAGED_TICKETS + wq, 1);
       if (__shfl_sync(0xffffffffu, before, 0) != un.pieces - 1) return;
       __threadfence();
-      // slots: 2 c0 + 1, then 2 c for the CTAs after c0
-      auto piece = [&](int i) -> const float* {
-        return p.part + (size_t)(i == 0 ? 2 * un.c0 + 1 : 2 * (un.c0 + i)) * p.slot_floats +
-               wq * PAGED_WARP_FLOATS;
-      };
-      float top = -INFINITY, lsum = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < un.pieces; ++i)
-        if (mine) top = fmaxf(top, __ldcg(piece(i) + 2048 + 2 * lane));
-      // lane -> 4 columns of rows 2 k + lane / 16
-      float4 acc[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      // the weights of 32 pieces at a time, in this warp's staging space
-      float* wts = reinterpret_cast<float*>(stage);
-      for (int i0 = 0; i0 < un.pieces; i0 += 32) {
-        const int cntp = min(32, un.pieces - i0);
-        __syncwarp();
-#pragma unroll 8
-        for (int i = 0; i < cntp; ++i) {
-          float wt = 0.f;
-          if (mine) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + i) + 2048) + lane);
-            wt = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
-            lsum += ml.y * wt;
-          }
-          wts[i * 32 + lane] = wt;
-        }
-        __syncwarp();
-        // 8 rows at a time, several pieces' loads in flight
-#pragma unroll
-        for (int kq = 0; kq < 4; ++kq) {
-          if (8 * kq < nr) {
-#pragma unroll 4
-            for (int i = 0; i < cntp; ++i) {
-              const float4* src = reinterpret_cast<const float4*>(piece(i0 + i)) + lane;
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const int k = 4 * kq + kk, row = 2 * k + (lane >> 4);
-                // (rows past nr were not written)
-                const float4 v = row < nr ? __ldcg(src + k * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
-                const float wr = wts[i * 32 + row];
-                acc[k].x = fmaf(v.x, wr, acc[k].x);
-                acc[k].y = fmaf(v.y, wr, acc[k].y);
-                acc[k].z = fmaf(v.z, wr, acc[k].z);
-                acc[k].w = fmaf(v.w, wr, acc[k].w);
-              }
-            }
-          }
-        }
-      }
-      // the next TMA load into the Q tile comes after these accesses to it
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      const float lse = finish(top, lsum, &inv);
-      if (p.lse && grp == 0 && mine) p.lse[(size_t)head * p.total_q + tok] = lse;
-      const long long at = mine ? ((long long)tok * p.Hq + head) * HEAD_DIM + 64 * grp : -1;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (2 * k < nr) {
-          const int row = 2 * k + (lane >> 4);
-          const float f = __shfl_sync(0xffffffffu, inv, row);
-          const long long to = __shfl_sync(0xffffffffu, at, row);
-          if (to >= 0) {
-            uint2 o;
-            o.x = pack2<BF16>(acc[k].x * f, acc[k].y * f);
-            o.y = pack2<BF16>(acc[k].z * f, acc[k].w * f);
-            *reinterpret_cast<uint2*>(p.out + to + (lane & 15) * 4) = o;
-          }
-        }
-      }
+      join_pieces<BF16>(p, un.c0, un.pieces, wq, nr, sink2,
+                        mine ? (long long)tok * p.Hq + head : -1,
+                        grp == 0 ? (size_t)head * p.total_q + tok : NO_LSE, 64 * grp,
+                        reinterpret_cast<float*>(stage));
     };
     bool ok = true;
-    int m = 0;    // step counter across units
     int cnt = 0, oth = 0;  // steps of this group and of the other one so far
-    Cyc<STAGES> rg;
     Cyc<NBUF> bc;
     Unit prev{};
     float prev_M = -INFINITY, prev_l = 0.f, prev_sink2 = -INFINITY;
@@ -843,21 +903,31 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       const Walk w(p, un.n, un.L, un.tok0);
       // the row's position; rows that are no token's see nothing
       const int x0 = un.L - un.n + un.tok0;
-      const int x = rloc < rows ? x0 + tl : -1;
+      const int x = x0 + tl;
+      const int key_end = rloc >= rows ? 0 : p.causal ? max(x + 1, 0) : un.L;
+      // sub-tiles that every row sees whole: [full_lo, full_hi] (before the
+      // first row's position and within the last one's window), and those up to
+      // full_first among the first keys
+      const int all_end = p.causal ? x0 + 1 : un.L;  // keys before this: no row lies before them
       const int x_last = x0 + (rows - 1) / p.group;
+      const int full_hi = all_end < Q_SUB ? -1 : all_end / Q_SUB - 1;
+      const int full_lo = !p.causal || x_last < p.window
+                              ? 0
+                              : (x_last - p.window + Q_SUB) / Q_SUB;
+      const int full_first = min(full_hi, p.first / Q_SUB - 1);
       int last_bf = 0;       // buffer of this group's previous step of the unit
       uint32_t last_ph = 0;  // and the parity of its use
-      for (int i = 0; ok && i < un.N; ++i, ++m, rg.next(), bc.next()) {
+      for (int i = 0; ok && i < un.N; ++i, bc.next()) {
         if ((i & 1) != grp) {
           ++oth;
           continue;
         }
-        const int st = rg.i, bf = bc.i;
-        // s_full implies the stage's loads landed; waiting on kv_full as well
-        // makes the step's tile index (written by the loader) visible
+        const int bf = bc.i;
+        const int t = w.tile(un.s0 + i);
+        // warp-uniform: every row of the tile sees every key of the sub-tile
+        const bool full = (t >= full_lo && t <= full_hi) || t <= full_first;
         ok = mbar_wait_warp(smem_u32(&s.bar_s_full[grp][cnt & 1]), (cnt >> 1) & 1, wc,
-                            TAG_S_FULL) &&
-             mbar_wait_warp(smem_u32(&s.bar_kv_full[st]), rg.ph, wc, TAG_KV_FULL);
+                            TAG_S_FULL);
         if (!ok) break;
         ++cnt;
         if (!busy) {
@@ -870,23 +940,6 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         float sv[64];
         tmem_ld32(lane_base + col, *reinterpret_cast<float(*)[32]>(&sv[0]));
         tmem_ld32(lane_base + col + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
-        const int k0 = s.step_t[st] * Q_SUB;
-        // warp-uniform: every row of the tile sees every key of the sub-tile
-        const bool full =
-            k0 + Q_SUB <= un.L &&
-            (!p.causal || (k0 + Q_SUB - 1 <= x0 &&
-                           (x_last - k0 < p.window || k0 + Q_SUB <= p.first)));
-        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
-        if (!full) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int j0 = k0 + 32 * q;
-            vis[q] = rloc < rows ? bit_range(0, un.L - 1 - j0) : 0u;
-            if (p.causal)
-              vis[q] &= bit_range(0, x - j0) & (bit_range(x - p.window + 1 - j0, 31) |
-                                                bit_range(0, p.first - 1 - j0));
-          }
-        }
         tmem_wait_ld_regs(sv);
         // row maximum of the visible raw logits (the scale is positive, so
         // it is applied once afterwards); eight partial maxima and sums keep
@@ -897,9 +950,14 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         if (!full) {
           // invisible logits drop out of the maximum
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            sv[c] = ((vis[0] >> c) & 1u) ? sv[c] : -INFINITY;
-            sv[32 + c] = ((vis[1] >> c) & 1u) ? sv[32 + c] : -INFINITY;
+          for (int q = 0; q < 2; ++q) {
+            const int j0 = t * Q_SUB + 32 * q;
+            uint32_t vis = bit_range(0, key_end - 1 - j0);
+            if (p.causal)
+              vis &= bit_range(x - p.window + 1 - j0, 31) | bit_range(0, p.first - 1 - j0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              sv[32 * q + c] = ((vis >> c) & 1u) ? sv[32 * q + c] : -INFINITY;
           }
         }
 #pragma unroll
