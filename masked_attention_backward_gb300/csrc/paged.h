@@ -11,10 +11,11 @@ constexpr int PAGED_MAX_CTAS = 152;  // CTAs of the attention grid at most (one 
 constexpr int PAGED_TICKETS = 8;     // softmax warps, each its own ticket of a unit
 // A warp's share of a piece in the workspace: O [32 rows, 64 columns], then
 // (M, l) [32 rows].
-constexpr int PAGED_WARP_FLOATS = 32 * 64 + 32 * 2;
+constexpr int PAGED_ML = 32 * 64;
+constexpr int PAGED_WARP_FLOATS = PAGED_ML + 32 * 2;
 // On the line that the schedule cuts, in steps of 64 keys: what a unit costs
 // beside its steps, and the least part that a CTA gets.
-constexpr int PAGED_UNIT_COST = 2;
+constexpr int PAGED_UNIT_COST = 7;
 constexpr int PAGED_MIN_COST = 8;
 
 // Where a CTA's part of the line begins, and what the loader needs there: the

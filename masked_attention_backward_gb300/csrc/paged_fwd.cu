@@ -28,7 +28,7 @@
 // pieces per CTA whatever the lengths, which stay on the device.
 //
 // The inner loop is that of the BHSD forward kernel (attn_fwd.cu): warp 0
-// loads Q and K, warp 11 V (each a box per run of keys in a page, the page
+// loads Q and K, warp 3 V (each a box per run of keys in a page, the page
 // numbers looked up 32 at a time, a batch ahead), warp 1 issues S = Q K^T, warp 2 O += P V, two groups
 // of four softmax warps take alternate steps.  Rows of V that no row of the unit sees (past
 // the last key, before the window, between the first keys and it) may hold
@@ -36,6 +36,8 @@
 // without a seen key are not loaded (zeros stand in), and warp 2 clears the
 // other unseen rows in shared memory before it multiplies.
 #include <math.h>
+
+#include <type_traits>
 
 #include "paged.h"
 #include "tiles.cuh"
@@ -49,11 +51,13 @@ constexpr int NBUF = 3;          // S / P buffers
 constexpr int COL_O = 0;         // O accumulator of group g at COL_O + 128 g
 constexpr int COL_QA = 256;      // Q as the A operand, 64 columns of 16-bit pairs
 constexpr int COL_S = 320;       // S buffer b at COL_S + 64 b
-constexpr int SM_WARP0 = 3;      // first softmax warp
+constexpr int V_WARP = 3;        // loader of V
+constexpr int SM_WARP0 = 4;      // first softmax warp (a warpgroup's first)
 constexpr int SM_WARPS = 8;      // softmax warps, two groups of four
-constexpr int V_WARP = SM_WARP0 + SM_WARPS;  // loader of V
-constexpr int NUM_THREADS = 32 * (V_WARP + 1);
+constexpr int NUM_THREADS = 32 * (SM_WARP0 + SM_WARPS);
 constexpr float RESCALE_LOG2 = 8.f;  // M moves when a row maximum exceeds it by this
+constexpr unsigned LOAD_SLEEP_NS = 100;  // polling period of the loaders' waits
+constexpr int AHEAD = STAGES + 3;  // steps of a unit issued before the next one's Q
 constexpr int SCHED_THREADS = 1024;
 constexpr unsigned long long DRAIN_NS = 10000000ull;  // a copy in flight lands well within 10 ms
 constexpr int NO_PAGE = (int)0x80000000;
@@ -73,7 +77,7 @@ struct __align__(1024) Smem {
   uint8_t V[STAGES][2 * Q_SUB * 128];
   float xml[2][2][Q_TILE][2];   // [unit parity][group][row]: (M, l) at the piece's end
   Unit unit;                    // piece of the latest Q load, N < 0: none left
-  uint64_t bar_unit;            // unit published (the loader of V does not wait for Q)
+  uint64_t bar_unit;            // unit published (for warps that do not wait for Q)
   uint64_t bar_q_full;
   uint64_t bar_qa_full;         // Q copied into TMEM (all softmax warps)
   uint64_t bar_kv_full[STAGES];
@@ -85,7 +89,7 @@ struct __align__(1024) Smem {
   uint64_t bar_acc_full;        // every O MMA of the piece complete
   uint64_t bar_acc_empty;       // its accumulators read (all softmax warps)
   uint64_t bar_unit_free;       // every other warp took the unit (and, softmax warps,
-                                // stored the previous unit's epilogue)
+                                // left the previous unit's rows)
   uint64_t bar_x_done[2];       // every MMA of the S / O warp complete
   uint32_t tmem_base;
   int abort_flag;
@@ -164,58 +168,55 @@ __device__ __forceinline__ float finish_row(float m_row, float l_row, float sink
   return (top + log2f(lt)) * 0.6931471805599453f;
 }
 
-constexpr size_t NO_LSE = ~(size_t)0;
-
 // Adds up a split unit's pieces, in their order, for one softmax warp's rows
-// and columns, and stores them.  Lane i knows row i: its sink, its place
-// row_at in the packed rows (-1: none) and lse_at in lse.
+// and columns, and stores them.  Lane i knows row i: its sink, its place row_at in the
+// packed rows (-1: none) and lse_at in lse.  wts: 32 x 32 floats of scratch.
 template <bool BF16>
-__device__ __forceinline__ void join_pieces(const PagedParams& p, int c0, int pieces, int wq, int nr,
-                                         float sink2, long long row_at, size_t lse_at, int col0,
-                                         float* stage) {
+__device__ __forceinline__ void join_pieces(const PagedParams& p, int c0, int pieces, int wq,
+                                            int nr, float sink2, long long row_at, size_t lse_at,
+                                            float* wts) {
   const int lane = threadIdx.x & 31;
-  const bool mine = lane < nr;
   // slots: 2 c0 + 1, then 2 c for the CTAs after c0
   auto piece = [&](int i) -> const float* {
     return p.part + (size_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * p.slot_floats +
            wq * PAGED_WARP_FLOATS;
   };
-  float top = -INFINITY, lsum = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < pieces; ++i)
-    if (mine) top = fmaxf(top, __ldcg(piece(i) + 2048 + 2 * lane));
-  // lane -> 4 columns of rows 2 k + lane / 16
-  float4 acc[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  // the weights of 32 pieces at a time, in this warp's staging space
-  float* wts = stage;
-  for (int i0 = 0; i0 < pieces; i0 += 32) {
-    const int cntp = min(32, pieces - i0);
-    __syncwarp();
-#pragma unroll 8
-    for (int i = 0; i < cntp; ++i) {
-      float wt = 0.f;
-      if (mine) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + i) + 2048) + lane);
-        wt = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
-        lsum += ml.y * wt;
-      }
-      wts[i * 32 + lane] = wt;
-    }
-    __syncwarp();
-    // 8 rows at a time, several pieces' loads in flight
-#pragma unroll
-    for (int kq = 0; kq < 4; ++kq) {
-      if (8 * kq < nr) {
+  const bool mine = lane < nr;
+  float top = -INFINITY, lsum = 0.f, inv = 0.f;
 #pragma unroll 4
-        for (int i = 0; i < cntp; ++i) {
-          const float4* src = reinterpret_cast<const float4*>(piece(i0 + i)) + lane;
+  for (int i = 0; i < pieces; ++i)
+    if (mine) top = fmaxf(top, __ldcg(piece(i) + PAGED_ML + 2 * lane));
+  const int c16 = lane & 15, h16 = lane >> 4;
+  for (int r0 = 0; r0 < nr; r0 += 8) {
+    // lane -> columns 4 c16 .. 4 c16 + 3 of rows r0 + h16, r0 + h16 + 2, ..
+    float4 acc[4];
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int k = 4 * kq + kk, row = 2 * k + (lane >> 4);
-            // (rows past nr were not written)
-            const float4 v = row < nr ? __ldcg(src + k * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+      const int cnt = min(32, pieces - i0);
+      if (r0 == 0 || pieces > 32) {  // the weights of 32 pieces at a time
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < cnt; ++i) {
+          float wt = 0.f;
+          if (mine) {
+            const float2 ml =
+                __ldcg(reinterpret_cast<const float2*>(piece(i0 + i) + PAGED_ML) + lane);
+            wt = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
+            if (r0 == 0) lsum += ml.y * wt;
+          }
+          wts[i * 32 + lane] = wt;
+        }
+        __syncwarp();
+      }
+#pragma unroll 4
+      for (int i = 0; i < cnt; ++i) {
+        const float4* src = reinterpret_cast<const float4*>(piece(i0 + i)) + r0 * 16 + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = r0 + 2 * k + h16;
+          if (row < nr) {  // (rows past nr were not written)
+            const float4 v = __ldcg(src + k * 32);
             const float wr = wts[i * 32 + row];
             acc[k].x = fmaf(v.x, wr, acc[k].x);
             acc[k].y = fmaf(v.y, wr, acc[k].y);
@@ -225,23 +226,20 @@ __device__ __forceinline__ void join_pieces(const PagedParams& p, int c0, int pi
         }
       }
     }
-  }
-  // the next TMA load into the Q tile comes after these accesses to it
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  float inv;
-  const float lse = finish_row(top, lsum, sink2, &inv);
-  if (p.lse && lse_at != NO_LSE && mine) p.lse[lse_at] = lse;
+    if (r0 == 0) {
+      const float lse = finish_row(top, lsum, sink2, &inv);
+      if (p.lse && mine && (wq & 1) == 0) p.lse[lse_at] = lse;
+    }
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    if (2 * k < nr) {
-      const int row = 2 * k + (lane >> 4);
+    for (int k = 0; k < 4; ++k) {
+      const int row = r0 + 2 * k + h16;
       const float f = __shfl_sync(0xffffffffu, inv, row);
       const long long to = __shfl_sync(0xffffffffu, row_at, row);
       if (to >= 0) {
         uint2 o;
         o.x = pack2<BF16>(acc[k].x * f, acc[k].y * f);
         o.y = pack2<BF16>(acc[k].z * f, acc[k].w * f);
-        *reinterpret_cast<uint2*>(p.out + to * HEAD_DIM + col0 + (lane & 15) * 4) = o;
+        *reinterpret_cast<uint2*>(p.out + to * HEAD_DIM + 64 * (wq & 1) + c16 * 4) = o;
       }
     }
   }
@@ -461,10 +459,11 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   grid_dependency_wait();
 
   // Steps [s0, s0 + N) of a unit, K (which = 0) or V: the boxes of each step
-  // into its stage, behind a full wait for the stage to be free.
+  // into its stage, once that is free; midway() before step AHEAD.
   int m_load = 0;  // steps issued, across units
   Cyc<STAGES> rg_load;
-  auto load_steps = [&](const Walk& w, int which, int b, int kvh, int s0, int N) -> bool {
+  auto load_steps = [&](const Walk& w, int which, int b, int kvh, int s0, int N,
+                        auto&& midway) -> bool {
     const CUtensorMap* tm = which ? &tV : &tK;
     const int runs = Q_SUB / p.box_rows;
     const int batch = 32 / runs;  // steps whose pages the lanes look up at once
@@ -485,6 +484,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     int page = NO_PAGE, prow = 0, next = pages_of(s0), next_row = row0, left = 0;
     for (int i = s0; i < s0 + N; ++i, ++m_load, rg_load.next(), --left) {
       const int st = rg_load.i;
+      if (i == s0 + AHEAD && !midway()) return false;
       if (left == 0) {
         page = next;
         prow = next_row;
@@ -498,7 +498,8 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         next_row = row0;
       }
       if (m_load >= STAGES &&
-          !mbar_wait_warp(smem_u32(&s.bar_kv_empty[st]), rg_load.ph ^ 1u, wc, TAG_KV_EMPTY))
+          !mbar_wait_sleep_warp(smem_u32(&s.bar_kv_empty[st]), rg_load.ph ^ 1u, wc, TAG_KV_EMPTY,
+                                LOAD_SLEEP_NS))
         return false;
       const uint32_t fb = smem_u32(&s.bar_kv_full[st]);
       if (lane == 0) mbar_arrive_expect_tx(fb, 2 * Q_SUB * 128);
@@ -542,59 +543,60 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     };
     load_lengths();
     const uint32_t qbar = smem_u32(&s.bar_q_full);
-    for (int j = 0; ok; ++j) {
+    // Publishes unit j and loads its Q once the slot and the Q tile are free;
+    // then stands at the unit after it.
+    Unit next;
+    auto publish = [&](int j) -> bool {
       if (j >= 1 &&
-          !mbar_wait_warp(smem_u32(&s.bar_unit_free), (j - 1) & 1, wc, TAG_UNIT_FREE)) {
-        ok = false;
-        break;
-      }
+          !mbar_wait_sleep_warp(smem_u32(&s.bar_unit_free), (j - 1) & 1, wc, TAG_UNIT_FREE,
+                                LOAD_SLEEP_NS))
+        return false;
       const bool in_end = b == end.b && kvh == end.kvh && tile == end.tile;
       if (b >= p.B || (in_end && end.step <= step)) {
+        next.N = -1;  // none is left
         if (lane == 0) {
           s.unit.N = -1;
           mbar_arrive(smem_u32(&s.bar_unit));
           mbar_arrive(qbar);
         }
-        break;
+        return true;
       }
-      const int tok0 = tile * p.tile_tokens;
-      const Walk w(p, n, L, tok0);
-      const int s0 = step, s1 = in_end ? end.step : w.cnt;
       // cuts inside this unit: the CTAs that go on with it
-      const int cuts = s0 > 0 ? at0.cuts : in_end ? end.cuts : 0;
-      const int first_cut = s0 > 0 ? at0.first_cut : end.first_cut;
+      const int cuts = step > 0 ? at0.cuts : in_end ? end.cuts : 0;
+      const int first_cut = step > 0 ? at0.first_cut : end.first_cut;
+      next.b = b;
+      next.kvh = kvh;
+      next.off = off;
+      next.n = n;
+      next.L = L;
+      next.tok0 = tile * p.tile_tokens;
+      next.s0 = step;
+      next.N = (in_end ? end.step : Walk(p, n, L, next.tok0).cnt) - step;
+      next.pieces = cuts + 1;
+      next.slot = 2 * cta + (step > 0 ? 0 : 1);
+      next.c0 = first_cut - 1;
       if (lane == 0) {
-        s.unit.b = b;
-        s.unit.kvh = kvh;
-        s.unit.off = off;
-        s.unit.n = n;
-        s.unit.L = L;
-        s.unit.tok0 = tok0;
-        s.unit.s0 = s0;
-        s.unit.N = s1 - s0;
-        s.unit.pieces = cuts + 1;
-        s.unit.slot = 2 * cta + (s0 > 0 ? 0 : 1);
-        s.unit.c0 = first_cut - 1;
+        s.unit = next;
         mbar_arrive(smem_u32(&s.bar_unit));
-        if (s1 == s0) {
+        if (next.N == 0) {
           mbar_arrive(qbar);  // no key to see: no Q either
         } else {
+          const int row = off + next.tok0;
           mbar_arrive_expect_tx(qbar, 2 * p.tile_rows * 128);
-          tma_load_3d(smem_u32(s.Q), &tQ, 0, kvh * p.group, off + tok0, qbar);
-          tma_load_3d(smem_u32(s.Q + Q_TILE * 128), &tQ, 64, kvh * p.group, off + tok0, qbar);
+          tma_load_3d(smem_u32(s.Q), &tQ, 0, kvh * p.group, row, qbar);
+          tma_load_3d(smem_u32(s.Q + Q_TILE * 128), &tQ, 64, kvh * p.group, row, qbar);
         }
       }
       __syncwarp();
-      if (s1 > s0) q_loaded = j;
-      ok = load_steps(w, 0, b, kvh, s0, s1 - s0);
+      if (next.N > 0) q_loaded = j;
       if (in_end) {  // nothing of this CTA is left
-        step = s1;
-        continue;
+        step = end.step;
+        return true;
       }
       step = 0;
-      if (++tile * p.tile_tokens < n) continue;
+      if (++tile * p.tile_tokens < n) return true;
       tile = 0;
-      if (++kvh < p.Hkv) continue;
+      if (++kvh < p.Hkv) return true;
       kvh = 0;
       // the next request with new tokens
       for (n = 0; n == 0 && ++b < p.B;) {
@@ -607,6 +609,20 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         L = __shfl_sync(0xffffffffu, l_L, b - b_base);
         if (b == end.b) break;
       }
+      return true;
+    };
+    bool ahead = false;  // the unit after the one being loaded is published
+    for (int j = 0; ok; ++j) {
+      if (!ahead) ok = publish(j);
+      if (!ok || next.N < 0) break;
+      const Walk w(p, next.n, next.L, next.tok0);
+      ahead = false;
+      // a long unit's successor is published, and its Q loaded, while this
+      // one is still being worked on: its consumers have then taken it
+      ok = load_steps(w, 0, next.b, next.kvh, next.s0, next.N, [&]() {
+        ahead = true;
+        return publish(j + 1);
+      });
     }
     if (!ok) {
       if (q_loaded >= 0) mbar_drain_warp(qbar, q_loaded & 1, DRAIN_NS);
@@ -616,7 +632,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     // ------------------------------------------------------------ loader of V
     bool ok = true;
     for (int j = 0; ok; ++j) {
-      if (!mbar_wait_warp(smem_u32(&s.bar_unit), j & 1, wc, TAG_UNIT)) {
+      if (!mbar_wait_sleep_warp(smem_u32(&s.bar_unit), j & 1, wc, TAG_UNIT, LOAD_SLEEP_NS)) {
         ok = false;
         break;
       }
@@ -625,7 +641,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
       if (un.N < 0) break;
       const Walk w(p, un.n, un.L, un.tok0);
-      ok = load_steps(w, 1, un.b, un.kvh, un.s0, un.N);
+      ok = load_steps(w, 1, un.b, un.kvh, un.s0, un.N, []() { return true; });
     }
     if (!ok) drain_loads();
   } else if (warp < SM_WARP0) {
@@ -732,89 +748,89 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     // Combines both groups' accumulators of unit j into columns [64 grp,
     // 64 grp + 64) of this warp's 32 rows, and stores them (a whole unit), or
     // leaves them in the workspace, where the last piece's warp joins them.
-    // (M, l) of the own group come in; the other group's are taken from
-    // shared memory.
-    auto epilogue = [&](int j, const Unit& un, float M, float l, float sink2, bool ok) {
+    // Arrives on acc_empty, and on unit_free of the unit after it (whose Q this
+    // warp has copied) once the staging space is not needed any more.  (M, l)
+    // of the own group come in, the other group's through shared memory.
+    auto epilogue = [&](int j, const Unit& un, float M, float l, bool ok) {
       s.xml[j & 1][grp][rloc][0] = M;
       s.xml[j & 1][grp][rloc][1] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.bar_xml[sp][j & 1]));
       const int N = un.N;
-      // rows of the tile that are a token of the request; this warp's share
-      const int rows = min(p.tile_tokens, un.n - un.tok0) * p.group;
-      const int nr = min(32, rows - sp * 32);
+      // rows of this warp that are a token of the request
+      const int nr = min(32, min(p.tile_tokens, un.n - un.tok0) * p.group - sp * 32);
+      const bool mine = lane < nr, whole = un.pieces == 1;
+      const int tok = un.off + un.tok0 + tl, head = un.kvh * p.group + hh;
+      const float sink2 = p.sink && mine ? p.sink[head] * LOG2E : -INFINITY;
+      const long long row_at = mine ? (long long)tok * p.Hq + head : -1;
+      const size_t lse_at = (size_t)head * p.total_q + tok;
+      const int wq = sp * 2 + grp;
       // (a piece without steps waits too, so that no wait meets these barriers
       // two phases late)
-      const bool done =
-          ok && mbar_wait_warp(smem_u32(&s.bar_xml[sp][j & 1]), (j >> 1) & 1, wc, TAG_XML) &&
-          mbar_wait_warp(smem_u32(&s.bar_acc_full), j & 1, wc, TAG_ACC);
-      const bool have = done && N > 0, gave_up = !done;
-      tc_fence_after();
-      float w[2] = {0.f, 0.f};  // weights of O_0 and O_1
-      float Mx = -INFINITY, lx = 0.f;
-      if (have) {
-        const float Mo = s.xml[j & 1][grp ^ 1][rloc][0], lo = s.xml[j & 1][grp ^ 1][rloc][1];
-        const float Mg[2] = {grp == 0 ? M : Mo, grp == 0 ? Mo : M};
-        const float lg[2] = {grp == 0 ? l : lo, grp == 0 ? lo : l};
-        Mx = fmaxf(Mg[0], Mg[1]);
-        // group 1 has steps only when the piece has two or more; a group's
-        // weight is zero when its row saw nothing (l = 0)
-        if (lg[0] > 0.f) w[0] = fast_exp2(Mg[0] - Mx);
-        if (N >= 2 && lg[1] > 0.f) w[1] = fast_exp2(Mg[1] - Mx);
-        lx = lg[0] * w[0] + lg[1] * w[1];
+      ok = ok && mbar_wait_warp(smem_u32(&s.bar_xml[sp][j & 1]), (j >> 1) & 1, wc, TAG_XML);
+      // weights of O_0 and O_1: group 1 has steps only when the piece has two
+      // or more, and a group that saw nothing of a row (l = 0) has none
+      float w0 = 0.f, w1 = 0.f, top = -INFINITY, lsum = 0.f;
+      if (ok && N > 0) {
+        const float mo = s.xml[j & 1][grp ^ 1][rloc][0], lo = s.xml[j & 1][grp ^ 1][rloc][1];
+        const float l0 = grp == 0 ? l : lo, l1 = grp == 0 ? lo : l;
+        top = fmaxf(M, mo);
+        if (l0 > 0.f) w0 = fast_exp2((grp == 0 ? M : mo) - top);
+        if (N >= 2 && l1 > 0.f) w1 = fast_exp2((grp == 0 ? mo : M) - top);
+        lsum = l0 * w0 + l1 * w1;
       }
-      const bool whole = un.pieces == 1;
-      const int tok = un.off + un.tok0 + tl, head = un.kvh * p.group + hh;
-      const bool mine = lane < nr;
-      float inv = 0.f;
+      float* part = p.part + (size_t)un.slot * p.slot_floats + wq * PAGED_WARP_FLOATS;
       if (whole) {
-        const float lse = finish_row(Mx, lx, sink2, &inv);
-        if (p.lse && grp == 0 && mine && !gave_up) p.lse[(size_t)head * p.total_q + tok] = lse;
-        w[0] *= inv;
-        w[1] *= inv;
+        float inv;
+        const float lse = finish_row(top, lsum, sink2, &inv);
+        if (p.lse && grp == 0 && mine && ok) p.lse[lse_at] = lse;
+        w0 *= inv;
+        w1 *= inv;
+      } else if (mine) {
+        part[PAGED_ML + 2 * lane] = top;
+        part[PAGED_ML + 2 * lane + 1] = lsum;
       }
-      if (nr > 0 && !gave_up) {
-        float* part = nullptr;
-        if (!whole) {
-          part = p.part + (size_t)un.slot * p.slot_floats + (sp * 2 + grp) * PAGED_WARP_FLOATS;
-          if (mine) {
-            part[2048 + 2 * lane] = Mx;
-            part[2048 + 2 * lane + 1] = lx;
+      ok = ok && mbar_wait_warp(smem_u32(&s.bar_acc_full), j & 1, wc, TAG_ACC);
+      tc_fence_after();
+      uint32_t pk[32];
+      if (ok && nr > 0) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float a0[32], a1[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) a0[c] = a1[c] = 0.f;
+          const uint32_t col = lane_base + COL_O + 64 * grp + 32 * q;
+          if (N > 0) {
+            tmem_ld32(col, a0);
+            if (N >= 2) tmem_ld32(col + 128, a1);
+            tmem_wait_ld_regs(a0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(a1[c]));
           }
-        }
-        uint32_t pk[32];
+          // (a row of weight zero may hold anything)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float acc[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) acc[c] = 0.f;
-          if (have) {
-#pragma unroll
-            for (int gg = 0; gg < 2; ++gg) {
-              if (__any_sync(0xffffffffu, w[gg] != 0.f)) {
-                float v[32];
-                tmem_ld32(lane_base + COL_O + 128 * gg + 64 * grp + 32 * half, v);
-                tmem_wait_ld_regs(v);
-                // (a row of weight zero may hold anything)
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  acc[c] = w[gg] != 0.f ? fmaf(v[c], w[gg], acc[c]) : acc[c];
-              }
-            }
+          for (int c = 0; c < 32; ++c) {
+            a0[c] = w0 != 0.f ? a0[c] * w0 : 0.f;
+            a0[c] = w1 != 0.f ? fmaf(a1[c], w1, a0[c]) : a0[c];
           }
           if (whole) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) pk[16 * half + c] = pack2<BF16>(acc[2 * c], acc[2 * c + 1]);
+            for (int c = 0; c < 16; ++c) pk[16 * q + c] = pack2<BF16>(a0[2 * c], a0[2 * c + 1]);
           } else if (mine) {
-            float4* dst = reinterpret_cast<float4*>(part + lane * 64 + 32 * half);
+            float4* dst = reinterpret_cast<float4*>(part + lane * 64 + 32 * q);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              dst[c] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+              dst[c] = make_float4(a0[4 * c], a0[4 * c + 1], a0[4 * c + 2], a0[4 * c + 3]);
           }
         }
-        // where this lane's row goes
-        const long long at = mine ? ((long long)tok * p.Hq + head) * HEAD_DIM + 64 * grp : -1;
+      }
+      // the accumulators are read: the next unit's O may begin
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.bar_acc_empty));
+      if (ok && nr > 0) {
         if (whole) {
+          // through shared memory, so that a row's 128 bytes leave together
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
@@ -823,57 +839,50 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int row = k * 4 + (lane >> 3), c = lane & 7;
-            const long long to = __shfl_sync(0xffffffffu, at, row);
+            const long long to = __shfl_sync(0xffffffffu, row_at, row);
             const uint4 v =
                 *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
-            if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + c * 8) = v;
+            if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * HEAD_DIM + 64 * grp + c * 8) = v;
           }
+        } else {
+          // the last piece to get here joins all of them, in their order
+          __threadfence();
           __syncwarp();
-          // the next TMA load into the Q tile comes after this warp's generic
-          // accesses to it
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          int before = 0;
+          if (lane == 0) before = atomicAdd(p.ticket + un.c0 * PAGED_TICKETS + wq, 1);
+          if (__shfl_sync(0xffffffffu, before, 0) == un.pieces - 1) {
+            __threadfence();
+            join_pieces<BF16>(p, un.c0, un.pieces, wq, nr, sink2, row_at, lse_at,
+                              reinterpret_cast<float*>(stage));
+          }
         }
       }
-      tc_fence_before();
+      // the next TMA load into the Q tile comes after this warp's generic
+      // accesses to it
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.bar_acc_empty));
-      if (whole || nr <= 0 || gave_up) return;
-
-      // ---- the last piece to get here joins all of them, in their order
-      const int wq = sp * 2 + grp;
-      __threadfence();
-      __syncwarp();
-      int before = 0;
-      if (lane == 0) before = atomicAdd(p.ticket + un.c0 * PAGED_TICKETS + wq, 1);
-      if (__shfl_sync(0xffffffffu, before, 0) != un.pieces - 1) return;
-      __threadfence();
-      join_pieces<BF16>(p, un.c0, un.pieces, wq, nr, sink2,
-                        mine ? (long long)tok * p.Hq + head : -1,
-                        grp == 0 ? (size_t)head * p.total_q + tok : NO_LSE, 64 * grp,
-                        reinterpret_cast<float*>(stage));
+      if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
     };
     bool ok = true;
     int cnt = 0, oth = 0;  // steps of this group and of the other one so far
     Cyc<NBUF> bc;
     Unit prev{};
-    float prev_M = -INFINITY, prev_l = 0.f, prev_sink2 = -INFINITY;
-    int j = 0;
-    for (; ok; ++j) {
-      ok = mbar_wait_warp(smem_u32(&s.bar_q_full), j & 1, wc, TAG_Q);
-      if (!ok) break;
+    float prev_M = -INFINITY, prev_l = 0.f;
+    for (int j = 0;; ++j) {
+      ok = ok && mbar_wait_warp(smem_u32(&s.bar_q_full), j & 1, wc, TAG_Q);
       const Unit un = s.unit;
-      if (un.N < 0) break;
+      const bool last = !ok || un.N < 0;  // no unit: only the previous one's epilogue
       const int rows = min(p.tile_tokens, un.n - un.tok0) * p.group;
       const bool busy = sp * 32 < rows;  // some row of this warp is a token's
       // Q rows into TMEM as 16-bit pairs (element 2c in the low half of
       // column c): this warp copies d columns 64 grp .. 64 grp + 63 of its
       // rows.  S of this group's last step is complete; the other group's last
       // one, which may be the later of the two, is waited for.
-      if (oth > 0)
+      if (!last && oth > 0)
         ok = mbar_wait_warp(smem_u32(&s.bar_s_full[grp ^ 1][(oth - 1) & 1]), ((oth - 1) >> 1) & 1,
                             wc, TAG_S_FULL);
       tc_fence_after();
-      if (ok && busy && un.N > 0) {
+      if (!last && ok && busy && un.N > 0) {
         const uint8_t* src = s.Q + grp * (Q_TILE * 128) + rloc * 128;
         uint32_t w[32];
 #pragma unroll
@@ -891,63 +900,42 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.bar_qa_full));
       // the previous unit's epilogue overlaps this unit's first MMAs
-      if (j >= 1) epilogue(j - 1, prev, prev_M, prev_l, prev_sink2, ok);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
+      if (j >= 1) {
+        epilogue(j - 1, prev, prev_M, prev_l, ok);
+      } else if (lane == 0) {
+        mbar_arrive(smem_u32(&s.bar_unit_free));
+      }
+      if (last) break;
 
-      // this group's running maximum M (log2 domain) and its row sum; the sink
-      // joins at the unit's end
-      const float sink2 =
-          p.sink && rloc < rows ? p.sink[un.kvh * p.group + hh] * LOG2E : -INFINITY;
+      // this group's running maximum M (log2 domain) and its row sum (the sink
+      // joins in the epilogue)
       float M = -INFINITY, l = 0.f;
       const Walk w(p, un.n, un.L, un.tok0);
-      // the row's position; rows that are no token's see nothing
-      const int x0 = un.L - un.n + un.tok0;
-      const int x = x0 + tl;
+      // the row's position and the end of the keys it may see; rows that are no
+      // token's see nothing
+      const int x0 = un.L - un.n + un.tok0, x = x0 + tl;
       const int key_end = rloc >= rows ? 0 : p.causal ? max(x + 1, 0) : un.L;
       // sub-tiles that every row sees whole: [full_lo, full_hi] (before the
       // first row's position and within the last one's window), and those up to
       // full_first among the first keys
-      const int all_end = p.causal ? x0 + 1 : un.L;  // keys before this: no row lies before them
-      const int x_last = x0 + (rows - 1) / p.group;
+      const int all_end = p.causal ? x0 + 1 : un.L;
+      const int x_last = x0 + min(p.tile_tokens, un.n - un.tok0) - 1;
       const int full_hi = all_end < Q_SUB ? -1 : all_end / Q_SUB - 1;
-      const int full_lo = !p.causal || x_last < p.window
-                              ? 0
-                              : (x_last - p.window + Q_SUB) / Q_SUB;
+      const int full_lo =
+          !p.causal || x_last < p.window ? 0 : (x_last - p.window + Q_SUB) / Q_SUB;
       const int full_first = min(full_hi, p.first / Q_SUB - 1);
       int last_bf = 0;       // buffer of this group's previous step of the unit
       uint32_t last_ph = 0;  // and the parity of its use
-      for (int i = 0; ok && i < un.N; ++i, bc.next()) {
-        if ((i & 1) != grp) {
-          ++oth;
-          continue;
-        }
-        const int bf = bc.i;
-        const int t = w.tile(un.s0 + i);
-        // warp-uniform: every row of the tile sees every key of the sub-tile
-        const bool full = (t >= full_lo && t <= full_hi) || t <= full_first;
-        ok = mbar_wait_warp(smem_u32(&s.bar_s_full[grp][cnt & 1]), (cnt >> 1) & 1, wc,
-                            TAG_S_FULL);
-        if (!ok) break;
-        ++cnt;
-        if (!busy) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s.bar_p_full[bf]));
-          continue;
-        }
-        tc_fence_after();
+      // Step i on buffer bf: S from TMEM, masked or seen whole, P back over it.
+      // One copy of the code for each: the masking code in the loop of the
+      // whole sub-tiles cost these 5 % (registers and scheduling).
+      auto softmax = [&](auto masked, int i, int t, int bf) -> bool {
         const uint32_t col = COL_S + 64 * bf;
         float sv[64];
         tmem_ld32(lane_base + col, *reinterpret_cast<float(*)[32]>(&sv[0]));
         tmem_ld32(lane_base + col + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
         tmem_wait_ld_regs(sv);
-        // row maximum of the visible raw logits (the scale is positive, so
-        // it is applied once afterwards); eight partial maxima and sums keep
-        // the dependency chains short
-        float mp[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) mp[c] = -INFINITY;
-        if (!full) {
+        if constexpr (decltype(masked)::value) {
           // invisible logits drop out of the maximum
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -960,6 +948,12 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
               sv[32 * q + c] = ((vis >> c) & 1u) ? sv[32 * q + c] : -INFINITY;
           }
         }
+        // row maximum of the visible raw logits (the scale is positive, so
+        // it is applied once afterwards); eight partial maxima and sums keep
+        // the dependency chains short
+        float mp[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mp[c] = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 32; ++c) mp[c & 7] = fmax3f(mp[c & 7], sv[2 * c], sv[2 * c + 1]);
         const float mx = fmax3f(fmax3f(mp[0], mp[1], mp[2]), fmax3f(mp[3], mp[4], mp[5]),
@@ -996,8 +990,8 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         // previous O += P V of the unit has completed (the unit's first
         // accumulation of the group overwrites instead)
         if (i >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          ok = mbar_wait_warp(smem_u32(&s.bar_p_free[last_bf]), last_ph, wc, TAG_P_FREE);
-          if (!ok) break;
+          if (!mbar_wait_warp(smem_u32(&s.bar_p_free[last_bf]), last_ph, wc, TAG_P_FREE))
+            return false;
           tc_fence_after();
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
@@ -1011,7 +1005,26 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         }
         tmem_st32(lane_base + col, pk);
         tmem_wait_st();
-        tc_fence_before();
+        return true;
+      };
+      for (int i = 0; ok && i < un.N; ++i, bc.next()) {
+        if ((i & 1) != grp) {
+          ++oth;
+          continue;
+        }
+        const int bf = bc.i;
+        const int t = w.tile(un.s0 + i);
+        // warp-uniform: every row of the tile sees every key of the sub-tile
+        const bool full = (t >= full_lo && t <= full_hi) || t <= full_first;
+        ok = mbar_wait_warp(smem_u32(&s.bar_s_full[grp][cnt & 1]), (cnt >> 1) & 1, wc, TAG_S_FULL);
+        if (!ok) break;
+        ++cnt;
+        if (busy) {
+          tc_fence_after();
+          ok = full ? softmax(std::false_type{}, i, t, bf) : softmax(std::true_type{}, i, t, bf);
+          if (!ok) break;
+          tc_fence_before();
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.bar_p_full[bf]));
         last_bf = bf;
@@ -1020,9 +1033,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       prev = un;
       prev_M = M;
       prev_l = l;
-      prev_sink2 = sink2;
     }
-    if (j >= 1) epilogue(j - 1, prev, prev_M, prev_l, prev_sink2, ok);
   }
   tc_fence_before();
   __syncthreads();

@@ -372,6 +372,14 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, co
   return __all_sync(0xffffffffu, ok);
 }
 
+// Warp-uniform form of mbar_wait_sleep.
+__device__ __forceinline__ bool mbar_wait_sleep_warp(uint32_t bar, uint32_t parity,
+                                                     const WaitCtx& w, unsigned int tag,
+                                                     unsigned int sleep_ns) {
+  const bool ok = mbar_wait_sleep(bar, parity, w, tag, sleep_ns);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Warp-uniform form of mbar_drain.
 __device__ __forceinline__ bool mbar_drain_warp(uint32_t bar, uint32_t parity,
                                                 unsigned long long timeout_ns) {
