@@ -6,6 +6,7 @@ library cannot be built or loaded, every call raises -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import threading
 from dataclasses import dataclass
@@ -198,16 +199,19 @@ class Mask:
         return self.cu_seqlens_q is not None
 
     def desc(self) -> attn_mask_desc_t:
-        def ptr(t):
-            return t.data_ptr() if t is not None else None
-        for t, n in ((self.seqlen_q, "seqlen_q"), (self.seqlen_k, "seqlen_k"),
-                     (self.cu_seqlens_q, "cu_seqlens_q"), (self.cu_seqlens_k, "cu_seqlens_k")):
-            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
-                raise ValueError(f"{n} must be a contiguous int32 tensor")
-        return attn_mask_desc_t(self.kind, self.window, self.bx, self.by, ptr(self.block_mask),
-                                ptr(self.seqlen_q), ptr(self.seqlen_k), ptr(self.cu_seqlens_q),
-                                ptr(self.cu_seqlens_k), self.total_q, self.total_k,
-                                self.first)
+        def ptr(t, name):
+            if t is None:
+                return None
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor")
+            return t.data_ptr()
+        bm = self.block_mask
+        return attn_mask_desc_t(self.kind, self.window, self.bx, self.by,
+                                None if bm is None else bm.data_ptr(),
+                                ptr(self.seqlen_q, "seqlen_q"), ptr(self.seqlen_k, "seqlen_k"),
+                                ptr(self.cu_seqlens_q, "cu_seqlens_q"),
+                                ptr(self.cu_seqlens_k, "cu_seqlens_k"), self.total_q,
+                                self.total_k, self.first)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -248,12 +252,19 @@ def packed_mask(kind: int, seqlens_q, seqlens_k, device, window: int = 0, bx: in
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+# the current stream's handle without a Stream object (4 us of a call's host time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def workspace(shape: attn_shape_t, mask: Mask, device) -> torch.Tensor:
@@ -341,6 +352,9 @@ def attn_paged_fwd(shape, pages, q, k_pages, v_pages, block_table, table_stride,
                                  ctypes.c_float(scale), o, lse, ws, ws_bytes, stream)
 
 
+_same_device = contextlib.nullcontext()
+
+
 def _one_device(*tensors):
     """All tensors on one CUDA device: a guard that makes it current."""
     dev = None
@@ -349,11 +363,12 @@ def _one_device(*tensors):
             continue
         if not t.is_cuda:
             raise ValueError("every tensor must be a CUDA tensor")
+        i = t.get_device()
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    return torch.cuda.device(dev)
+            dev = i
+        elif i != dev:
+            raise ValueError(f"tensors on cuda:{dev} and cuda:{i}")
+    return _same_device if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _int_tensor(t: torch.Tensor, name: str, numel: int, dtype=torch.int32):
@@ -397,8 +412,10 @@ class PagedPlan:
 
     @staticmethod
     def empty(B: int, max_tokens: int, device) -> "PagedPlan":
-        e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=device)
-        return PagedPlan(e(B + 1), e(B), e(1), e(max_tokens, torch.int64), e(max_tokens), e(1))
+        ints = torch.empty(2 * B + 3 + max_tokens, dtype=torch.int32, device=device)
+        cu, lens, free, refused, position = ints.split((B + 1, B, 1, 1, max_tokens))
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
+        return PagedPlan(cu, lens, free, slots, position, refused)
 
 
 def paged_plan(cached, fresh, free_pages, free_count, block_table, page_size: int,
@@ -473,8 +490,9 @@ def paged_shape(q: torch.Tensor, cache: PagedCache, mask: Mask) -> attn_shape_t:
                         mask.max_seqlen_k, q.shape[2], _dtype_code(q), 0)
 
 
-def paged_workspace(q: torch.Tensor, cache: PagedCache, mask: Mask) -> torch.Tensor:
-    r, n = attn_paged_workspace_size(paged_shape(q, cache, mask))
+def paged_workspace(q: torch.Tensor, cache: PagedCache, mask: Mask,
+                    shape: Optional[attn_shape_t] = None) -> torch.Tensor:
+    r, n = attn_paged_workspace_size(shape or paged_shape(q, cache, mask))
     if r != ATTN_OK:
         raise AttnError(r, "attn_paged_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=q.device)
@@ -510,7 +528,7 @@ def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
     with _one_device(q, cache.k_pages, block_table, sink, mask.cu_seqlens_q, mask.seqlen_k, o, lse,
                      ws):
         if ws is None:
-            ws = paged_workspace(q, cache, mask)
+            ws = paged_workspace(q, cache, mask, shape)
         r = attn_paged_fwd(shape, cache.desc, q.data_ptr(), cache.k_pages.data_ptr(),
                            cache.v_pages.data_ptr(), block_table.data_ptr(),
                            block_table.stride(0) if B > 1 else cols, cols, _ptr(sink), mask.desc(),

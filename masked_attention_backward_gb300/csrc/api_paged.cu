@@ -51,7 +51,7 @@ attn_status_t check_paged_shape(const attn_shape_t* sh) {
 }
 
 struct PagedLayout {
-  size_t status, start, ticket, part, total;
+  size_t status, start, part, total;
   int tile_tokens, tile_rows, slot_floats;
 };
 
@@ -66,8 +66,6 @@ PagedLayout paged_layout(const attn_shape_t* sh) {
   off = align256(off + sizeof(DevStatus));
   L.start = off;
   off = align256(off + (PAGED_MAX_CTAS + 1) * sizeof(PagedStart));
-  L.ticket = off;
-  off = align256(off + PAGED_MAX_CTAS * PAGED_TICKETS * sizeof(int));
   L.part = off;
   off = align256(off + (size_t)2 * PAGED_MAX_CTAS * L.slot_floats * sizeof(float));
   L.total = off;
@@ -199,7 +197,6 @@ attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* page
   p.timeout_ns = wait_timeout_ns();
   p.test_no_loads = test_no_loads();
   p.start = reinterpret_cast<PagedStart*>(w + L.start);
-  p.ticket = reinterpret_cast<int*>(w + L.ticket);
   p.part = reinterpret_cast<float*>(w + L.part);
   p.slot_floats = L.slot_floats;
   int dev = 0, sms = 0;

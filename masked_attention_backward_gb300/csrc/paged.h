@@ -8,7 +8,6 @@ namespace mab {
 
 constexpr int PAGED_MAX_B = 4096;    // requests of one call
 constexpr int PAGED_MAX_CTAS = 152;  // CTAs of the attention grid at most (one per SM)
-constexpr int PAGED_TICKETS = 8;     // softmax warps, each its own ticket of a unit
 // A warp's share of a piece in the workspace: O [32 rows, 64 columns], then
 // (M, l) [32 rows].
 constexpr int PAGED_ML = 32 * 64;
@@ -45,7 +44,6 @@ struct PagedParams {
   int test_no_loads;
   int grid;          // CTAs
   PagedStart* start; // [grid + 1]
-  int* ticket;       // [grid, PAGED_TICKETS] pieces done of the unit that the CTA's part ends in
   float* part;       // [2 grid, slot_floats] pieces
   int slot_floats;
 };

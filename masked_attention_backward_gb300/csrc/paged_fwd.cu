@@ -22,8 +22,8 @@
 // Balance: k_paged_schedule lays all units end to end, in steps, and cuts the
 // line into equal parts, one per CTA of a persistent grid: a unit that a cut
 // falls into is done in pieces, each leaving its fp32 O, M and l in the
-// workspace, and the last piece to finish (a ticket per warp) joins them in
-// order, whichever it is.  So a single request's keys spread over the whole
+// workspace, which k_paged_join adds up in order.  So a single request's keys
+// spread over the whole
 // GPU, ragged batches load every SM alike, and the workspace is bounded by two
 // pieces per CTA whatever the lengths, which stay on the device.
 //
@@ -67,7 +67,7 @@ struct Unit {
   int kvh, off, n, L, tok0;  // kv head; the request's first row, new tokens, keys; first token
   int s0, N;                 // first step and steps of the piece
   int b;                     // the request
-  int pieces, slot, c0;      // pieces of the unit; this one's slot; CTA of the first one
+  int whole, slot;           // not cut; else the piece's slot
 };
 
 struct __align__(1024) Smem {
@@ -113,9 +113,14 @@ struct Cyc {
   }
 };
 
-// The schedule's shared memory for B requests: costs, new tokens, keys.
-constexpr size_t sched_smem(int B) { return (size_t)(B + 1) * 8 + (size_t)B * 8; }
+// The schedule's shared memory for B requests: costs, new tokens, keys, rows.
+constexpr size_t sched_smem(int B) { return (size_t)(B + 1) * 8 + (size_t)B * 12; }
 static_assert(PAGED_MAX_CTAS < 32 * 32, "one lane of the schedule's block per cut");
+
+// a / b of non-negative numbers, in 32 bits where they fit.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 
 // New tokens and keys of request b.
 __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
@@ -168,83 +173,6 @@ __device__ __forceinline__ float finish_row(float m_row, float l_row, float sink
   return (top + log2f(lt)) * 0.6931471805599453f;
 }
 
-// Adds up a split unit's pieces, in their order, for one softmax warp's rows
-// and columns, and stores them.  Lane i knows row i: its sink, its place row_at in the
-// packed rows (-1: none) and lse_at in lse.  wts: 32 x 32 floats of scratch.
-template <bool BF16>
-__device__ __forceinline__ void join_pieces(const PagedParams& p, int c0, int pieces, int wq,
-                                            int nr, float sink2, long long row_at, size_t lse_at,
-                                            float* wts) {
-  const int lane = threadIdx.x & 31;
-  // slots: 2 c0 + 1, then 2 c for the CTAs after c0
-  auto piece = [&](int i) -> const float* {
-    return p.part + (size_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * p.slot_floats +
-           wq * PAGED_WARP_FLOATS;
-  };
-  const bool mine = lane < nr;
-  float top = -INFINITY, lsum = 0.f, inv = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i)
-    if (mine) top = fmaxf(top, __ldcg(piece(i) + PAGED_ML + 2 * lane));
-  const int c16 = lane & 15, h16 = lane >> 4;
-  for (int r0 = 0; r0 < nr; r0 += 8) {
-    // lane -> columns 4 c16 .. 4 c16 + 3 of rows r0 + h16, r0 + h16 + 2, ..
-    float4 acc[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < pieces; i0 += 32) {
-      const int cnt = min(32, pieces - i0);
-      if (r0 == 0 || pieces > 32) {  // the weights of 32 pieces at a time
-        __syncwarp();
-#pragma unroll 4
-        for (int i = 0; i < cnt; ++i) {
-          float wt = 0.f;
-          if (mine) {
-            const float2 ml =
-                __ldcg(reinterpret_cast<const float2*>(piece(i0 + i) + PAGED_ML) + lane);
-            wt = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
-            if (r0 == 0) lsum += ml.y * wt;
-          }
-          wts[i * 32 + lane] = wt;
-        }
-        __syncwarp();
-      }
-#pragma unroll 4
-      for (int i = 0; i < cnt; ++i) {
-        const float4* src = reinterpret_cast<const float4*>(piece(i0 + i)) + r0 * 16 + lane;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = r0 + 2 * k + h16;
-          if (row < nr) {  // (rows past nr were not written)
-            const float4 v = __ldcg(src + k * 32);
-            const float wr = wts[i * 32 + row];
-            acc[k].x = fmaf(v.x, wr, acc[k].x);
-            acc[k].y = fmaf(v.y, wr, acc[k].y);
-            acc[k].z = fmaf(v.z, wr, acc[k].z);
-            acc[k].w = fmaf(v.w, wr, acc[k].w);
-          }
-        }
-      }
-    }
-    if (r0 == 0) {
-      const float lse = finish_row(top, lsum, sink2, &inv);
-      if (p.lse && mine && (wq & 1) == 0) p.lse[lse_at] = lse;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int row = r0 + 2 * k + h16;
-      const float f = __shfl_sync(0xffffffffu, inv, row);
-      const long long to = __shfl_sync(0xffffffffu, row_at, row);
-      if (to >= 0) {
-        uint2 o;
-        o.x = pack2<BF16>(acc[k].x * f, acc[k].y * f);
-        o.y = pack2<BF16>(acc[k].z * f, acc[k].w * f);
-        *reinterpret_cast<uint2*>(p.out + to * HEAD_DIM + 64 * (wq & 1) + c16 * 4) = o;
-      }
-    }
-  }
-}
-
 }  // namespace paged_side
 
 // One block.  Lays the units (request, kv head, query tile) end to end and
@@ -256,6 +184,7 @@ k_paged_schedule(const PagedParams p, int grid) {
   extern __shared__ long long base[];  // [B + 1] cost of the requests before b
   int* s_n = reinterpret_cast<int*>(base + p.B + 1);  // [B] new tokens
   int* s_L = s_n + p.B;                               // [B] keys
+  int* s_off = s_L + p.B;                             // [B] first row
   __shared__ long long warp_tot[32];
   __shared__ int s_units;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -271,6 +200,7 @@ k_paged_schedule(const PagedParams p, int grid) {
       tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
       s_n[b] = n;
       s_L[b] = L;
+      s_off[b] = packed_off(p.cu_q, b, p.total_q);
     }
     long long w = tiles > 0 ? unit_cost(p, n, L, 0) : 0;
     // several tiles: the warp adds their costs, one request after another
@@ -313,7 +243,6 @@ k_paged_schedule(const PagedParams p, int grid) {
   }
   if (tid == 0) base[p.B] = carry;
   if (tid < (int)(sizeof(DevStatus) / 4)) reinterpret_cast<unsigned*>(p.status)[tid] = 0u;
-  for (int i = tid; i < grid * PAGED_TICKETS; i += SCHED_THREADS) p.ticket[i] = 0;
   __syncthreads();
   const long long total = carry;
   // a CTA for each unit while there are CTAs, and parts of at least
@@ -322,7 +251,7 @@ k_paged_schedule(const PagedParams p, int grid) {
   const int parts = (int)(most < 1 ? 1 : most < grid ? most : grid);
   // lane l of warp w places cut w + 32 l
   const int c = warp + 32 * lane;
-  const long long cut = c < parts ? total / parts * c + total % parts * c / parts : total;
+  const long long cut = c < parts ? quot(total * c, parts) : total;
   int b = p.B, kvh = 0, tile = 0, tiles = 0, cost = 0, n = 0, L = 0;  // past the last unit
   long long rem = 0;  // the cut's distance from the start of the head, then of the unit
   if (c <= grid && cut < total) {
@@ -333,8 +262,8 @@ k_paged_schedule(const PagedParams p, int grid) {
       else hi = mid - 1;
     }
     b = lo;
-    const long long head = (base[b + 1] - base[b]) / p.Hkv;
-    kvh = (int)((cut - base[b]) / head);
+    const long long head = quot(base[b + 1] - base[b], p.Hkv);
+    kvh = (int)quot(cut - base[b], head);
     rem = (cut - base[b]) - kvh * head;
     n = s_n[b];
     L = s_L[b];
@@ -392,8 +321,8 @@ k_paged_schedule(const PagedParams p, int grid) {
     int first = 0, cuts = 0;
     if (step > 0) {
       const long long u0 = cut - rem;
-      first = (int)(((u0 + PAGED_UNIT_COST + 1) * parts + total - 1) / total);
-      cuts = (int)(((u0 + cost - 1) * parts + total - 1) / total) - first;
+      first = (int)quot((u0 + PAGED_UNIT_COST + 1) * parts + total - 1, total);
+      cuts = (int)quot((u0 + cost - 1) * parts + total - 1, total) - first;
     }
     PagedStart r;
     r.b = b;
@@ -402,7 +331,7 @@ k_paged_schedule(const PagedParams p, int grid) {
     r.step = step;
     r.first_cut = first;
     r.cuts = cuts;
-    r.off = b < p.B ? packed_off(p.cu_q, b, p.total_q) : 0;
+    r.off = b < p.B ? s_off[b] : 0;
     r.n = b < p.B ? s_n[b] : 0;
     r.L = b < p.B ? s_L[b] : 0;
     p.start[c] = r;
@@ -455,8 +384,10 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = s.tmem_base;
-  // launched over the schedule kernel: its cuts are read from here on
+  // launched over the schedule kernel: its cuts are read from here on; the
+  // join's blocks may wait beside this grid
   grid_dependency_wait();
+  grid_launch_dependents();
 
   // Steps [s0, s0 + N) of a unit, K (which = 0) or V: the boxes of each step
   // into its stage, once that is free; midway() before step AHEAD.
@@ -531,8 +462,9 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     int off = at0.off, n = at0.n, L = at0.L;                         // of request b
     bool ok = !p.test_no_loads;
     int q_loaded = -1;  // last unit whose Q tile was loaded
-    // lane i holds the lengths of request b_base + i
-    int b_base = b, l_off = 0, l_n = 0, l_L = 0;
+    // lane i holds the lengths of request b_base + i (none yet: the first
+    // request's came with the start)
+    int b_base = b - 32, l_off = 0, l_n = 0, l_L = 0;
     auto load_lengths = [&]() {
       l_off = l_n = l_L = 0;
       if (b_base + lane < p.B) {
@@ -541,7 +473,6 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         l_L = keys_of(p, b_base + lane);
       }
     };
-    load_lengths();
     const uint32_t qbar = smem_u32(&s.bar_q_full);
     // Publishes unit j and loads its Q once the slot and the Q tile are free;
     // then stands at the unit after it.
@@ -561,9 +492,6 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         }
         return true;
       }
-      // cuts inside this unit: the CTAs that go on with it
-      const int cuts = step > 0 ? at0.cuts : in_end ? end.cuts : 0;
-      const int first_cut = step > 0 ? at0.first_cut : end.first_cut;
       next.b = b;
       next.kvh = kvh;
       next.off = off;
@@ -572,9 +500,9 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       next.tok0 = tile * p.tile_tokens;
       next.s0 = step;
       next.N = (in_end ? end.step : Walk(p, n, L, next.tok0).cnt) - step;
-      next.pieces = cuts + 1;
+      // slots: 2 c for a piece that goes on with a unit, 2 c + 1 for its first one
+      next.whole = step == 0 && !(in_end && end.step > 0);
       next.slot = 2 * cta + (step > 0 ? 0 : 1);
-      next.c0 = first_cut - 1;
       if (lane == 0) {
         s.unit = next;
         mbar_arrive(smem_u32(&s.bar_unit));
@@ -747,7 +675,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     uint8_t* stage = s.Q + grp * (Q_TILE * 128) + sp * 4096;
     // Combines both groups' accumulators of unit j into columns [64 grp,
     // 64 grp + 64) of this warp's 32 rows, and stores them (a whole unit), or
-    // leaves them in the workspace, where the last piece's warp joins them.
+    // leaves them in the workspace for the join (a piece).
     // Arrives on acc_empty, and on unit_free of the unit after it (whose Q this
     // warp has copied) once the staging space is not needed any more.  (M, l)
     // of the own group come in, the other group's through shared memory.
@@ -759,7 +687,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       const int N = un.N;
       // rows of this warp that are a token of the request
       const int nr = min(32, min(p.tile_tokens, un.n - un.tok0) * p.group - sp * 32);
-      const bool mine = lane < nr, whole = un.pieces == 1;
+      const bool mine = lane < nr, whole = un.whole;
       const int tok = un.off + un.tok0 + tl, head = un.kvh * p.group + hh;
       const float sink2 = p.sink && mine ? p.sink[head] * LOG2E : -INFINITY;
       const long long row_at = mine ? (long long)tok * p.Hq + head : -1;
@@ -828,33 +756,20 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.bar_acc_empty));
-      if (ok && nr > 0) {
-        if (whole) {
-          // through shared memory, so that a row's 128 bytes leave together
+      if (ok && nr > 0 && whole) {
+        // through shared memory, so that a row's 128 bytes leave together
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-          __syncwarp();
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int row = k * 4 + (lane >> 3), c = lane & 7;
-            const long long to = __shfl_sync(0xffffffffu, row_at, row);
-            const uint4 v =
-                *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
-            if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * HEAD_DIM + 64 * grp + c * 8) = v;
-          }
-        } else {
-          // the last piece to get here joins all of them, in their order
-          __threadfence();
-          __syncwarp();
-          int before = 0;
-          if (lane == 0) before = atomicAdd(p.ticket + un.c0 * PAGED_TICKETS + wq, 1);
-          if (__shfl_sync(0xffffffffu, before, 0) == un.pieces - 1) {
-            __threadfence();
-            join_pieces<BF16>(p, un.c0, un.pieces, wq, nr, sink2, row_at, lse_at,
-                              reinterpret_cast<float*>(stage));
-          }
+        for (int k = 0; k < 8; ++k) {
+          const int row = k * 4 + (lane >> 3), c = lane & 7;
+          const long long to = __shfl_sync(0xffffffffu, row_at, row);
+          const uint4 v =
+              *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * HEAD_DIM + 64 * grp + c * 8) = v;
         }
       }
       // the next TMA load into the Q tile comes after this warp's generic
@@ -1043,6 +958,80 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   }
 }
 
+// Adds up the pieces of the units that a cut fell into, in their order, and
+// stores them: block (c, sp) the 32 rows from 32 sp on of the unit whose first
+// piece is CTA c's last one, a warp per row, 4 columns a lane.  Weights with
+// one lane per piece, and the pieces' rows without a branch between their
+// loads, so that all of a row's loads are in flight together (joined by the
+// last warp to finish inside the kernel above, 19 pieces took 5 to 15 us and
+// the code slowed its loop by 5 %).
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_paged_join(const PagedParams p) {
+  using namespace paged_side;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = (int)blockIdx.x, sp = (int)blockIdx.y;
+  grid_dependency_wait();
+  const PagedStart u = p.start[c + 1];
+  if (u.step == 0 || u.first_cut != c + 1) return;
+  const int pieces = u.cuts + 1, tok0 = u.tile * p.tile_tokens;
+  const int rows = min(32, min(p.tile_tokens, u.n - tok0) * p.group - 32 * sp);
+  // slots: 2 c + 1, then those of the CTAs that go on
+  auto piece = [&](int i, int half) -> const float* {
+    return p.part + (size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * p.slot_floats +
+           (2 * sp + half) * PAGED_WARP_FLOATS;
+  };
+  constexpr int MOST = (PAGED_MAX_CTAS + 31) / 32;  // pieces a lane may know
+  for (int r = warp; r < rows; r += 8) {
+    float m[MOST], l[MOST], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      m[k] = -INFINITY;
+      l[k] = 0.f;
+      if (32 * k + lane < pieces) {
+        const float2 x =
+            *reinterpret_cast<const float2*>(piece(32 * k + lane, 0) + PAGED_ML + 2 * r);
+        m[k] = x.x;
+        l[k] = x.y;
+      }
+      top = fmaxf(top, m[k]);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      m[k] = l[k] > 0.f ? fast_exp2(m[k] - top) : 0.f;  // the piece's weight from here on
+      sum += l[k] * m[k];
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      const int cnt = min(32, pieces - 32 * k);
+#pragma unroll 8
+      for (int i = 0; i < cnt; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(piece(32 * k + i, lane >> 4) + r * 64 +
+                                                          4 * (lane & 15));
+        const float w = __shfl_sync(0xffffffffu, m[k], i);
+        acc.x = fmaf(v.x, w, acc.x);
+        acc.y = fmaf(v.y, w, acc.y);
+        acc.z = fmaf(v.z, w, acc.z);
+        acc.w = fmaf(v.w, w, acc.w);
+      }
+    }
+    const int row = 32 * sp + r, tl = row / p.group;
+    const int tok = u.off + tok0 + tl, head = u.kvh * p.group + row - tl * p.group;
+    float inv;
+    const float lse =
+        finish_row(top, sum, p.sink ? p.sink[head] * LOG2E : -INFINITY, &inv);
+    if (p.lse && lane == 0) p.lse[(size_t)head * p.total_q + tok] = lse;
+    uint2 o;
+    o.x = pack2<BF16>(acc.x * inv, acc.y * inv);
+    o.y = pack2<BF16>(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(p.out + ((size_t)tok * p.Hq + head) * HEAD_DIM + 4 * lane) = o;
+  }
+}
+
 cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap& tQ,
                              const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st) {
   using namespace paged_side;
@@ -1066,7 +1055,12 @@ cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tQ, tK, tV, p);
+  e = cudaLaunchKernelEx(&cfg, kern, tQ, tK, tV, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((p.tile_rows + 31) / 32));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, bf16 ? k_paged_join<true> : k_paged_join<false>, p);
 }
 
 }  // namespace mab
