@@ -172,14 +172,11 @@ WsLayout layout_of(const attn_shape_t* sh, const attn_mask_desc_t* mk) {
     L.cnt_q = off;
     off = align256(off + BH * d.nQT_q * sizeof(int));
   }
-  L.first_ticket = L.first_part = off;
+  L.first_part = off;
   if (mk->kind == ATTN_MASK_SLIDING_FIRST && mask_kind_of(sh, mk) == MK_FIRST) {
     const size_t pieces = kv_first_pieces(sh->B, sh->Hq, sh->Hkv, sh->Sq, mk->first);
     if (pieces > 1) {
       const size_t units = (size_t)kv_first_tiles(mk->first) * sh->B * sh->Hkv;
-      L.first_ticket = off;
-      off = align256(off + units * KV_FIRST_WARPS * sizeof(int));
-      L.first_part = off;
       off = align256(off + units * pieces * KV_FIRST_PIECE_FLOATS * sizeof(float));
     }
   }
@@ -255,10 +252,9 @@ AttnParams params_of(const attn_shape_t* sh, const attn_mask_desc_t* mk, const W
     p.dq_flag = ws + L.dq_flag;
     p.dq_steps_head = single_pass_steps_head(sh, mk);
   }
-  if (L.first_part != L.first_ticket) {
+  if (p.mask_kind == MK_FIRST) {
     p.first_parts = kv_first_pieces(sh->B, sh->Hq, sh->Hkv, sh->Sq, mk->first);
     p.first_part = reinterpret_cast<float*>(ws + L.first_part);
-    p.first_ticket = reinterpret_cast<int*>(ws + L.first_ticket);
   }
   p.seqlen_q = mk->seqlen_q;
   p.seqlen_k = mk->seqlen_k;
@@ -464,7 +460,6 @@ attn_status_t attn_bwd(const attn_shape_t* shape, const void* q, const void* k, 
                           reinterpret_cast<float*>(w + L.dsink_part), shape->B, shape->Hq,
                           shape->Sq, d.Sq_pad, mask->seqlen_q, mask->cu_seqlens_q,
                           mask->total_q, reinterpret_cast<DevStatus*>(w + L.status),
-                          p.first_ticket, p.first_ticket ? (int)((L.first_part - L.first_ticket) / 4) : 0,
                           blk && !prof, st);
   }
   if (e == cudaSuccess && single) {

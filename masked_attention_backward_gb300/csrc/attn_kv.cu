@@ -94,6 +94,11 @@ static_assert(2 * (2 * KV_SUB * 128) >= SM_WARPS * 2048, "epilogue staging fits 
 enum { TAG_KV = 0x201, TAG_Q_EMPTY = 0x203, TAG_Q_FULL, TAG_S_FREE, TAG_P_FULL, TAG_S_FULL,
        TAG_DP_FULL, TAG_DS_FULL, TAG_ACC, TAG_X_DONE, TAG_DP_FREE };
 
+// Pieces of a first-key tile's walk of N steps that are not empty.
+__device__ __forceinline__ int first_pieces_used(int parts, int N) {
+  return min(parts, max(N / KV_FIRST_STEPS, 1));
+}
+
 }  // namespace kv_side
 
 // HILO: P^T and dS^T enter dV and dK as a 16-bit high part plus a 16-bit
@@ -133,7 +138,7 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
   int n0 = 0, used = 1;
   const int piece = FIRST ? (int)blockIdx.x % parts : 0;
   if constexpr (FIRST) {
-    used = min(parts, max(N / KV_FIRST_STEPS, 1));
+    used = first_pieces_used(parts, N);
     n0 = piece < used ? (int)((long long)N * piece / used) : 0;
     N = piece < used ? (int)((long long)N * (piece + 1) / used) - n0 : 0;
   }
@@ -447,19 +452,14 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
                               : RowAddr{r0, bc, ((size_t)bc * p.Skv + r0) * HEAD_DIM, HEAD_DIM};
     uint8_t* stage = s.Q[0] + (warp - SM_WARP0) * 2048;
     const bool staged = __all_sync(0xffffffffu, have || (ok && N == 0));
-    // A piece of a split walk leaves its fp32 sums in the workspace, and the
-    // last piece to finish adds them up, in the pieces' order whichever it is
-    // (each warp for its own 32 rows and 32 columns: no barrier between
-    // warps).  It stores the sum below; the other pieces store nothing.
+    // A piece of a split walk leaves its fp32 sums in the workspace for the
+    // join and stores no row.
     bool store = true;
-    const float* parts0 = nullptr;  // piece 0's sums of this warp's rows and columns
     if constexpr (FIRST) {
-      if (piece >= used) {
-        store = false;
-      } else if (used > 1) {
-        const int w = warp - SM_WARP0;
+      store = piece == 0 && used == 1;
+      if (piece < used && used > 1) {
         float* mine = p.first_part + ((size_t)unit * parts + piece) * KV_FIRST_PIECE_FLOATS +
-                      w * (KV_FIRST_PIECE_FLOATS / KV_FIRST_WARPS) + lane;
+                      (warp - SM_WARP0) * (KV_FIRST_PIECE_FLOATS / SM_WARPS) + lane;
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
           float v[32];
@@ -472,13 +472,6 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
 #pragma unroll
           for (int cc = 0; cc < 32; ++cc) mine[which * 1024 + cc * 32] = v[cc];
         }
-        __threadfence();
-        __syncwarp();
-        int before = 0;
-        if (lane == 0) before = atomicAdd(p.first_ticket + unit * KV_FIRST_WARPS + w, 1);
-        store = __shfl_sync(0xffffffffu, before, 0) == used - 1;
-        __threadfence();
-        parts0 = mine - (size_t)piece * KV_FIRST_PIECE_FLOATS;
       }
     }
 #pragma unroll 1
@@ -493,18 +486,8 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
       if (have) {
         const float sc = which ? p.scale : 1.f;
         float v[32];
-        if (FIRST && parts0) {
-#pragma unroll
-          for (int cc = 0; cc < 32; ++cc) v[cc] = 0.f;
-          for (int i = 0; i < used; ++i) {
-            const float* src = parts0 + (size_t)i * KV_FIRST_PIECE_FLOATS + which * 1024;
-#pragma unroll
-            for (int cc = 0; cc < 32; ++cc) v[cc] += __ldcg(src + cc * 32);
-          }
-        } else {
-          tmem_ld32(lane_base + (which ? COL_DK : COL_DV) + 32 * g, v);
-          tmem_wait_ld_regs(v);
-        }
+        tmem_ld32(lane_base + (which ? COL_DK : COL_DV) + 32 * g, v);
+        tmem_wait_ld_regs(v);
 #pragma unroll
         for (int cc = 0; cc < 16; ++cc) pk[cc] = pack2<BF16>(v[2 * cc] * sc, v[2 * cc + 1] * sc);
       } else {
@@ -535,6 +518,51 @@ k_dkdv(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorM
   // launched over the first-key tiles' grid: this one does not complete
   // before that one has
   if (p.after_first && blockIdx.x == 0 && threadIdx.x == 0) grid_dependency_wait();
+}
+
+// Adds up the pieces of the split first-key tiles, in their order, and stores
+// the rows: 16 blocks a tile, each warp 32 rows and 8 columns of dV or dK.  (The
+// last piece to finish doing so alone read 128 KB a piece on one SM: 20 us.)
+template <bool BF16, bool PACKED>
+__global__ void __launch_bounds__(256)
+k_dkdv_first_join(uint16_t* __restrict__ dk, uint16_t* __restrict__ dv, const AttnParams p) {
+  using namespace kv_side;
+  // the other tiles' grid needs nothing of this one; the grid before this one
+  // waited for the preprocess kernel before it let this one start
+  grid_launch_dependents();
+  const int unit = (int)blockIdx.x / 16, lane = threadIdx.x & 31;
+  const int e = ((int)blockIdx.x % 16) * 8 + (threadIdx.x >> 5);  // 0 .. 127
+  const int w = e >> 3, which = (e >> 2) & 1, c0 = (e & 3) * 8;  // softmax warp, dV or dK, columns
+  const int BHkv = p.B * p.Hkv;
+  const int t = unit / BHkv, bc = unit % BHkv, b = bc / p.Hkv, c = bc % p.Hkv;
+  KVWalk walk;
+  walk.init(p, b, c, t, len_q(p, b), len_k(p, b));
+  const int used = first_pieces_used(p.first_parts, walk.total(p));
+  // that grid's sums, and its rows where a walk was not split
+  grid_dependency_wait();
+  if (used == 1) return;
+  const float* src = p.first_part + (size_t)unit * p.first_parts * KV_FIRST_PIECE_FLOATS +
+                     w * (KV_FIRST_PIECE_FLOATS / SM_WARPS) + which * 1024 + c0 * 32 + lane;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < used; ++s)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += __ldcg(src + (size_t)s * KV_FIRST_PIECE_FLOATS + i * 32);
+  const int r0 = t * KV_TILE + ((w + SM_WARP0) & 3) * 32;
+  const int nvalid = PACKED ? rows_to_store_k(p, b, r0) : min(32, p.Skv - r0);
+  if (lane >= nvalid) return;
+  const RowAddr oa = PACKED ? row_k(p, b, c, r0)
+                            : RowAddr{r0, bc, ((size_t)bc * p.Skv + r0) * HEAD_DIM, HEAD_DIM};
+  const float sc = which ? p.scale : 1.f;
+  uint4 o;
+  o.x = pack2<BF16>(v[0] * sc, v[1] * sc);
+  o.y = pack2<BF16>(v[2] * sc, v[3] * sc);
+  o.z = pack2<BF16>(v[4] * sc, v[5] * sc);
+  o.w = pack2<BF16>(v[6] * sc, v[7] * sc);
+  uint16_t* row = (which ? dk : dv) + oa.elem + (size_t)lane * oa.stride;
+  *reinterpret_cast<uint4*>(row + 32 * (w >> 2) + c0) = o;
 }
 
 // Whether the persistent form (attn_kv_units.cu) runs the dK/dV walk: for the
@@ -598,9 +626,22 @@ cudaError_t launch_dkdv(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
 cudaError_t launch_dkdv_first(bool bf16, const AttnParams& p, const CUtensorMap& tQ,
                               const CUtensorMap& tdO, const CUtensorMap& tK,
                               const CUtensorMap& tV, void* dk, void* dv, cudaStream_t st) {
-  return launch_tiles(bf16, p, tQ, tdO, tK, tV, dk, dv,
-                      kv_first_tiles(p.first) * p.B * p.Hkv * (p.first_parts > 1 ? p.first_parts : 1),
-                      st);
+  const int units = kv_first_tiles(p.first) * p.B * p.Hkv;
+  const int parts = p.first_parts > 1 ? p.first_parts : 1;
+  cudaError_t e = launch_tiles(bf16, p, tQ, tdO, tK, tV, dk, dv, units * parts, st);
+  if (e != cudaSuccess || parts == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * 16));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const auto kern = bf16 ? (p.cu_q ? k_dkdv_first_join<true, true> : k_dkdv_first_join<true, false>)
+                         : (p.cu_q ? k_dkdv_first_join<false, true> : k_dkdv_first_join<false, false>);
+  return cudaLaunchKernelEx(&cfg, kern, (uint16_t*)dk, (uint16_t*)dv, p);
 }
 
 }  // namespace mab

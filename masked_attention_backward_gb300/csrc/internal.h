@@ -19,7 +19,6 @@ constexpr int Q_TILE = 128;
 constexpr int Q_SUB = 64;
 constexpr int PREP_ROWS = 128;  // padding unit of the per-row statistics
 constexpr int PREP_BLOCK_ROWS = 64;  // rows per preprocess block (divides PREP_ROWS)
-constexpr int KV_FIRST_WARPS = 16;    // softmax warps of the dK/dV kernel, each its own ticket
 constexpr int KV_FIRST_STEPS = 16;    // steps a piece of a first-key tile's walk has at least
 constexpr int KV_FIRST_PIECES = 152;  // pieces over all tiles at most (one per SM)
 constexpr int KV_FIRST_PIECE_FLOATS = 2 * KV_TILE * HEAD_DIM;
@@ -42,8 +41,7 @@ struct WsLayout {
   size_t cnt_k;      // int32 [B*Hq, nKT_k]
   size_t sel_q;      // int32 [B*Hq, nQT_q, nKT_q]  (query tiles of Q_TILE, key tiles of Q_SUB)
   size_t cnt_q;      // int32 [B*Hq, nQT_q]
-  size_t first_ticket;  // MK_FIRST, split walks: int [units, KV_FIRST_WARPS] pieces done
-  size_t first_part;    // float [units, pieces, KV_FIRST_PIECE_FLOATS]: their dV and dK sums
+  size_t first_part; // MK_FIRST, split walks: float [units, pieces, KV_FIRST_PIECE_FLOATS]
   size_t dq_flag;    // single pass: uint8 [B*Hq, steps per head], 1 = partial written
   size_t dq_part;    // single pass: float [B*Hq, steps per head, KV_SUB, HEAD_DIM]
   size_t total;
@@ -98,12 +96,11 @@ struct AttnParams {
   long long dq_steps_head;  // slots per query head
   int first;  // MK_FIRST: keys j < first stay visible to every later query
   // MK_FIRST, dK/dV: the key tiles below kv_tile0 hold first keys and are
-  // walked by a grid of their own, each in up to first_parts pieces whose
-  // sums the last one to finish adds up; the other tiles' grid (a plain
-  // sliding window from kv_tile0 on) runs over its tail (after_first).
+  // walked by a grid of their own, each in up to first_parts pieces whose sums
+  // a join adds up; the other tiles' grid (a plain sliding window from kv_tile0
+  // on) runs over the tail of both (after_first).
   int kv_tile0, after_first, first_parts;
   float* first_part;
-  int* first_ticket;
 };
 
 #ifdef __CUDACC__
@@ -195,8 +192,7 @@ int test_no_loads();
 cudaError_t launch_preprocess(bool bf16, const void* O, const void* dO, const float* lse,
                               const float* sink, float* nlse2, float* delta, float* part, int B,
                               int Hq, int Sq, int Sq_pad, const int* seqlen_q, const int* cu_q,
-                              int total_q, DevStatus* status, int* zero, int n_zero,
-                              bool overlap_prev, cudaStream_t st);
+                              int total_q, DevStatus* status, bool overlap_prev, cudaStream_t st);
 cudaError_t launch_dsink_finalize(const float* part, int Hq, int nparts, float* dsink,
                                   cudaStream_t st);
 cudaError_t launch_mask_tables(const AttnParams& p, uint8_t* maskT, int* sel_k, int* cnt_k,

@@ -1039,9 +1039,11 @@ cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap&
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_paged_schedule, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sched_smem(PAGED_MAX_B));
-  if (e != cudaSuccess) return e;
+  if (sched_smem(p.B) > (47u << 10)) {  // past what a launch may use unasked
+    e = cudaFuncSetAttribute(k_paged_schedule, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sched_smem(p.B));
+    if (e != cudaSuccess) return e;
+  }
   k_paged_schedule<<<1, SCHED_THREADS, sched_smem(p.B), st>>>(p, p.grid);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
