@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_
   constexpr int REFUSED = -1, ENDED = -2;
   __shared__ Sums warp_tot[PLAN_THREADS / 32];
   __shared__ int s_refused, s_granted;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int rank = (int)cluster_rank(), nranks = (int)gridDim.x;
   const int gtid = rank * PLAN_THREADS + tid, gthreads = nranks * PLAN_THREADS;
   const unsigned ps = (unsigned)p.page_size;
@@ -103,11 +103,16 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_
     const Sums upto =
         block_scan(Sums{ended ? 0 : fresh, ended ? held : 0}, warp_tot) + carry;
     carry = carry + warp_tot[PLAN_THREADS / 32 - 1];
-    // one thread of the cluster moves an ended request's pages
-    if (ended && b % nranks == rank) {
-      const long long at = count + upto.b - held;
-      for (int i = 0; i < held && at + i < p.num_pages; ++i)
-        p.free_pages[at + i] = p.block_table[(size_t)b * p.table_stride + i];
+    // one warp of the cluster moves an ended request's pages
+    for (unsigned todo = __ballot_sync(0xffffffffu, ended && b % nranks == rank); todo;
+         todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const long long at = __shfl_sync(0xffffffffu, count + upto.b - held, src);
+      const int moved =
+          (int)min((long long)__shfl_sync(0xffffffffu, held, src), p.num_pages - at);
+      const int* row = p.block_table + (size_t)(b - lane + src) * p.table_stride;
+#pragma unroll 4
+      for (int i = lane; i < moved; i += 32) p.free_pages[at + i] = row[i];
     }
     // what can never be placed needs no page
     const bool bad = !ended && ((long long)cached + fresh > cap || upto.a > p.max_tokens);
@@ -141,16 +146,31 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_
     *p.free_count_out = avail - s_granted;
     *p.refused = s_refused;
   }
-  for (int b = gtid; b < p.B; b += gthreads) {
-    const int g = s_grant[b], cached = s_cached[b];
-    p.cu_seqlens_q[b + 1] = s_end[b];
-    p.seqlen_k[b] = g == ENDED     ? 0
-                    : g == REFUSED ? cached
-                                   : cached + s_end[b] - (b > 0 ? s_end[b - 1] : 0);
-    const int held = (int)(((unsigned)cached + ps - 1) / ps);
-    for (int i = 0; i < g; ++i)
-      p.block_table[(size_t)b * p.table_stride + held + i] =
-          p.free_pages[avail - 1 - s_need0[b] - i];
+  // requests in whole warps: one that gets many pages has all lanes append them
+  for (int b0 = gtid - lane; b0 < p.B; b0 += gthreads) {
+    const int b = b0 + lane;
+    int g = 0, held = 0, need0 = 0;
+    if (b < p.B) {
+      const int cached = s_cached[b];
+      g = s_grant[b];
+      need0 = s_need0[b];
+      p.cu_seqlens_q[b + 1] = s_end[b];
+      p.seqlen_k[b] = g == ENDED     ? 0
+                      : g == REFUSED ? cached
+                                     : cached + s_end[b] - (b > 0 ? s_end[b - 1] : 0);
+      held = (int)(((unsigned)cached + ps - 1) / ps);
+    }
+    auto append = [&](int to, int have, int first, int i) {
+      p.block_table[(size_t)to * p.table_stride + have + i] = p.free_pages[avail - 1 - first - i];
+    };
+    if (g <= 4)
+      for (int i = 0; i < g; ++i) append(b, held, need0, i);
+    for (unsigned todo = __ballot_sync(0xffffffffu, g > 4); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int n = __shfl_sync(0xffffffffu, g, src), h = __shfl_sync(0xffffffffu, held, src);
+      const int first = __shfl_sync(0xffffffffu, need0, src);
+      for (int i = lane; i < n; i += 32) append(b0 + src, h, first, i);
+    }
   }
   for (int t = gtid; t < p.max_tokens; t += gthreads) {
     long long slot = -1;
