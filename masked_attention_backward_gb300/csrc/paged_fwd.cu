@@ -959,77 +959,87 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
 }
 
 // Adds up the pieces of the units that a cut fell into, in their order, and
-// stores them: block (c, sp) the 32 rows from 32 sp on of the unit whose first
-// piece is CTA c's last one, a warp per row, 4 columns a lane.  Weights with
-// one lane per piece, and the pieces' rows without a branch between their
-// loads, so that all of a row's loads are in flight together (joined by the
-// last warp to finish inside the kernel above, 19 pieces took 5 to 15 us and
-// the code slowed its loop by 5 %).
+// stores them: block (c, y) the rows 8 y .. 8 y + 7 of the unit whose first
+// piece is CTA c's last one, a warp per row, 4 columns a lane.  Latency bound:
+// one lane per piece for the weights, and the first 16 pieces' rows on their
+// way before those are known.  (Joined by the last warp to finish inside the
+// kernel above, 19 pieces took 5 to 15 us and the code slowed its loop by 5 %;
+// with four rows a warp one after another they took 15 us more than now.)
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_paged_join(const PagedParams p) {
   using namespace paged_side;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = (int)blockIdx.x, sp = (int)blockIdx.y;
+  const int lane = threadIdx.x & 31, c = (int)blockIdx.x;
+  const int row = (int)blockIdx.y * 8 + (threadIdx.x >> 5);
   grid_dependency_wait();
   const PagedStart u = p.start[c + 1];
-  if (u.step == 0 || u.first_cut != c + 1) return;
-  const int pieces = u.cuts + 1, tok0 = u.tile * p.tile_tokens;
-  const int rows = min(32, min(p.tile_tokens, u.n - tok0) * p.group - 32 * sp);
-  // slots: 2 c + 1, then those of the CTAs that go on
+  const int tok0 = u.tile * p.tile_tokens;
+  if (u.step == 0 || u.first_cut != c + 1 ||
+      row >= min(p.tile_tokens, u.n - tok0) * p.group)
+    return;
+  const int pieces = u.cuts + 1;
+  // this row in piece i (slots: 2 c + 1, then those of the CTAs that go on),
+  // from column 64 half on
+  const int sp = row >> 5, r = row & 31;
   auto piece = [&](int i, int half) -> const float* {
     return p.part + (size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * p.slot_floats +
            (2 * sp + half) * PAGED_WARP_FLOATS;
   };
+  auto values = [&](int i) -> float4 {
+    return __ldcg(reinterpret_cast<const float4*>(piece(i, lane >> 4) + r * 64) + (lane & 15));
+  };
+  constexpr int EARLY = 16;
+  float4 v[EARLY];
+#pragma unroll
+  for (int i = 0; i < EARLY; ++i) v[i] = values(min(i, pieces - 1));
   constexpr int MOST = (PAGED_MAX_CTAS + 31) / 32;  // pieces a lane may know
-  for (int r = warp; r < rows; r += 8) {
-    float m[MOST], l[MOST], top = -INFINITY, sum = 0.f;
+  float m[MOST], l[MOST], top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < MOST; ++k) {
-      m[k] = -INFINITY;
-      l[k] = 0.f;
-      if (32 * k + lane < pieces) {
-        const float2 x =
-            *reinterpret_cast<const float2*>(piece(32 * k + lane, 0) + PAGED_ML + 2 * r);
-        m[k] = x.x;
-        l[k] = x.y;
-      }
-      top = fmaxf(top, m[k]);
+  for (int k = 0; k < MOST; ++k) {
+    m[k] = -INFINITY;
+    l[k] = 0.f;
+    if (32 * k + lane < pieces) {
+      const float2 x =
+          __ldcg(reinterpret_cast<const float2*>(piece(32 * k + lane, 0) + PAGED_ML) + r);
+      m[k] = x.x;
+      l[k] = x.y;
     }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-#pragma unroll
-    for (int k = 0; k < MOST; ++k) {
-      m[k] = l[k] > 0.f ? fast_exp2(m[k] - top) : 0.f;  // the piece's weight from here on
-      sum += l[k] * m[k];
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < MOST; ++k) {
-      const int cnt = min(32, pieces - 32 * k);
-#pragma unroll 8
-      for (int i = 0; i < cnt; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(piece(32 * k + i, lane >> 4) + r * 64 +
-                                                          4 * (lane & 15));
-        const float w = __shfl_sync(0xffffffffu, m[k], i);
-        acc.x = fmaf(v.x, w, acc.x);
-        acc.y = fmaf(v.y, w, acc.y);
-        acc.z = fmaf(v.z, w, acc.z);
-        acc.w = fmaf(v.w, w, acc.w);
-      }
-    }
-    const int row = 32 * sp + r, tl = row / p.group;
-    const int tok = u.off + tok0 + tl, head = u.kvh * p.group + row - tl * p.group;
-    float inv;
-    const float lse =
-        finish_row(top, sum, p.sink ? p.sink[head] * LOG2E : -INFINITY, &inv);
-    if (p.lse && lane == 0) p.lse[(size_t)head * p.total_q + tok] = lse;
-    uint2 o;
-    o.x = pack2<BF16>(acc.x * inv, acc.y * inv);
-    o.y = pack2<BF16>(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(p.out + ((size_t)tok * p.Hq + head) * HEAD_DIM + 4 * lane) = o;
+    top = fmaxf(top, m[k]);
   }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    m[k] = l[k] > 0.f ? fast_exp2(m[k] - top) : 0.f;  // the piece's weight from here on
+    sum += l[k] * m[k];
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& x, float w) {
+    acc.x = fmaf(x.x, w, acc.x);
+    acc.y = fmaf(x.y, w, acc.y);
+    acc.z = fmaf(x.z, w, acc.z);
+    acc.w = fmaf(x.w, w, acc.w);
+  };
+#pragma unroll
+  for (int i = 0; i < EARLY; ++i)
+    add(v[i], i < pieces ? __shfl_sync(0xffffffffu, m[0], i) : 0.f);
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    const int end = min(32, pieces - 32 * k);
+#pragma unroll 8
+    for (int i = k == 0 ? EARLY : 0; i < end; ++i)
+      add(values(32 * k + i), __shfl_sync(0xffffffffu, m[k], i));
+  }
+  const int tl = row / p.group;
+  const int tok = u.off + tok0 + tl, head = u.kvh * p.group + row - tl * p.group;
+  float inv;
+  const float lse = finish_row(top, sum, p.sink ? p.sink[head] * LOG2E : -INFINITY, &inv);
+  if (p.lse && lane == 0) p.lse[(size_t)head * p.total_q + tok] = lse;
+  uint2 o;
+  o.x = pack2<BF16>(acc.x * inv, acc.y * inv);
+  o.y = pack2<BF16>(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.out + ((size_t)tok * p.Hq + head) * HEAD_DIM + 4 * lane) = o;
 }
 
 cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap& tQ,
@@ -1059,7 +1069,7 @@ cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap&
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, tQ, tK, tV, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((p.tile_rows + 31) / 32));
+  cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((p.tile_rows + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, bf16 ? k_paged_join<true> : k_paged_join<false>, p);
