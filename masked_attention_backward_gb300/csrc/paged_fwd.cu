@@ -37,8 +37,6 @@
 // other unseen rows in shared memory before it multiplies.
 #include <math.h>
 
-#include <type_traits>
-
 #include "paged.h"
 #include "tiles.cuh"
 
@@ -720,34 +718,41 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       }
       ok = ok && mbar_wait_warp(smem_u32(&s.bar_acc_full), j & 1, wc, TAG_ACC);
       tc_fence_after();
-      uint32_t pk[32];
+      // 16 columns at a time, in a loop: this code runs once a unit, and as one
+      // straight piece most of its time went into fetching it
       if (ok && nr > 0) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float a0[16], a1[16];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float a0[32], a1[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) a0[c] = a1[c] = 0.f;
-          const uint32_t col = lane_base + COL_O + 64 * grp + 32 * q;
+          for (int c = 0; c < 16; ++c) a0[c] = a1[c] = 0.f;
+          const uint32_t col = lane_base + COL_O + 64 * grp + 16 * q;
           if (N > 0) {
-            tmem_ld32(col, a0);
-            if (N >= 2) tmem_ld32(col + 128, a1);
+            tmem_ld16(col, a0);
+            if (N >= 2) tmem_ld16(col + 128, a1);
             tmem_wait_ld_regs(a0);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(a1[c]));
+            for (int c = 0; c < 16; ++c) asm volatile("" : "+f"(a1[c]));
           }
           // (a row of weight zero may hold anything)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
+          for (int c = 0; c < 16; ++c) {
             a0[c] = w0 != 0.f ? a0[c] * w0 : 0.f;
             a0[c] = w1 != 0.f ? fmaf(a1[c], w1, a0[c]) : a0[c];
           }
           if (whole) {
+            // through shared memory, so that a row's 128 bytes leave together
 #pragma unroll
-            for (int c = 0; c < 16; ++c) pk[16 * q + c] = pack2<BF16>(a0[2 * c], a0[2 * c + 1]);
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * q + h) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack2<BF16>(a0[8 * h], a0[8 * h + 1]),
+                             pack2<BF16>(a0[8 * h + 2], a0[8 * h + 3]),
+                             pack2<BF16>(a0[8 * h + 4], a0[8 * h + 5]),
+                             pack2<BF16>(a0[8 * h + 6], a0[8 * h + 7]));
           } else if (mine) {
-            float4* dst = reinterpret_cast<float4*>(part + lane * 64 + 32 * q);
+            float4* dst = reinterpret_cast<float4*>(part + lane * 64 + 16 * q);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
+            for (int c = 0; c < 4; ++c)
               dst[c] = make_float4(a0[4 * c], a0[4 * c + 1], a0[4 * c + 2], a0[4 * c + 3]);
           }
         }
@@ -757,13 +762,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.bar_acc_empty));
       if (ok && nr > 0 && whole) {
-        // through shared memory, so that a row's 128 bytes leave together
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        __syncwarp();
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 8; ++k) {
           const int row = k * 4 + (lane >> 3), c = lane & 7;
           const long long to = __shfl_sync(0xffffffffu, row_at, row);
@@ -841,69 +840,20 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       const int full_first = min(full_hi, p.first / Q_SUB - 1);
       int last_bf = 0;       // buffer of this group's previous step of the unit
       uint32_t last_ph = 0;  // and the parity of its use
-      // Step i on buffer bf: S from TMEM, masked or seen whole, P back over it.
-      // One copy of the code for each: the masking code in the loop of the
-      // whole sub-tiles cost these 5 % (registers and scheduling).
-      auto softmax = [&](auto masked, int i, int t, int bf) -> bool {
-        const uint32_t col = COL_S + 64 * bf;
-        float sv[64];
-        tmem_ld32(lane_base + col, *reinterpret_cast<float(*)[32]>(&sv[0]));
-        tmem_ld32(lane_base + col + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
-        tmem_wait_ld_regs(sv);
-        if constexpr (decltype(masked)::value) {
-          // invisible logits drop out of the maximum
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int j0 = t * Q_SUB + 32 * q;
-            uint32_t vis = bit_range(0, key_end - 1 - j0);
-            if (p.causal)
-              vis &= bit_range(x - p.window + 1 - j0, 31) | bit_range(0, p.first - 1 - j0);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              sv[32 * q + c] = ((vis >> c) & 1u) ? sv[32 * q + c] : -INFINITY;
-          }
-        }
-        // row maximum of the visible raw logits (the scale is positive, so
-        // it is applied once afterwards); eight partial maxima and sums keep
-        // the dependency chains short
-        float mp[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) mp[c] = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) mp[c & 7] = fmax3f(mp[c & 7], sv[2 * c], sv[2 * c + 1]);
-        const float mx = fmax3f(fmax3f(mp[0], mp[1], mp[2]), fmax3f(mp[3], mp[4], mp[5]),
-                                fmaxf(mp[6], mp[7]));
+      // Takes a step's row maximum mx (raw logits; the scale is positive, so it
+      // is applied once here).  M moves when mx exceeds it by more than 8; a row
+      // that has seen nothing yet (M = -inf, so O and l are still zero) just
+      // takes the new value.  The group's O rows whose M moved are rescaled once
+      // its previous O += P V of the unit has completed (the unit's first
+      // accumulation of the group overwrites instead).
+      auto move_max = [&](int i, float mx) -> bool {
         const float mx2 = mx == -INFINITY ? -INFINITY : mx * p.scale_log2;
-        // move M when the row maximum exceeds it by more than 8; a row that
-        // has seen nothing yet (M = -inf, so O and l are still zero) just
-        // takes the new value
         float alpha = 1.f;
         if (mx2 > M + RESCALE_LOG2) {
           if (M != -INFINITY) alpha = fast_exp2(M - mx2);
           M = mx2;
           l *= alpha;
         }
-        // P = exp2(S scale log2e - M): an invisible logit (-inf here) gives 0;
-        // a row with nothing visible keeps M = -inf and all its logits at
-        // -inf, and the finite stand-in keeps -inf - (-inf) out
-        const float Ms = M == -INFINITY ? 0.f : M;
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-Ms, -Ms);
-        uint32_t pk[32];
-        float2 lp[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) lp[c] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 xx = ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nm2);
-          const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
-          lp[c & 3] = fadd2(lp[c & 3], pp);
-          pk[c] = pack2<BF16>(pp.x, pp.y);
-        }
-        const float2 ls = fadd2(fadd2(lp[0], lp[1]), fadd2(lp[2], lp[3]));
-        l += ls.x + ls.y;
-        // rescale this group's O rows whose M moved, once the group's
-        // previous O += P V of the unit has completed (the unit's first
-        // accumulation of the group overwrites instead)
         if (i >= 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
           if (!mbar_wait_warp(smem_u32(&s.bar_p_free[last_bf]), last_ph, wc, TAG_P_FREE))
             return false;
@@ -918,7 +868,91 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
             tmem_st32(lane_base + COL_O + 128 * grp + 32 * q, v);
           }
         }
-        tmem_st32(lane_base + col, pk);
+        return true;
+      };
+      // P = exp2(S scale log2e - M): an invisible logit (-inf) gives 0; a row
+      // with nothing visible keeps M = -inf and all its logits at -inf, and the
+      // finite stand-in keeps -inf - (-inf) out
+      auto minus_max = [&]() { return M == -INFINITY ? 0.f : -M; };
+      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+      // A sub-tile that every row sees whole, from TMEM buffer column `col`: P
+      // packed over it.
+      auto whole_step = [&](int i, uint32_t col) -> bool {
+        float sv[64];
+        tmem_ld32(col, *reinterpret_cast<float(*)[32]>(&sv[0]));
+        tmem_ld32(col + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
+        tmem_wait_ld_regs(sv);
+        // eight partial maxima and four sums keep the dependency chains short
+        float mp[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mp[c] = fmaxf(sv[2 * c], sv[2 * c + 1]);
+#pragma unroll
+        for (int c = 8; c < 32; ++c) mp[c & 7] = fmax3f(mp[c & 7], sv[2 * c], sv[2 * c + 1]);
+        if (!move_max(i, fmax3f(fmax3f(mp[0], mp[1], mp[2]), fmax3f(mp[3], mp[4], mp[5]),
+                                fmaxf(mp[6], mp[7]))))
+          return false;
+        const float nm = minus_max();
+        const float2 nm2 = make_float2(nm, nm);
+        uint32_t pk[32];
+        float2 lp[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) lp[c] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float2 xx = ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nm2);
+          const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+          lp[c & 3] = fadd2(lp[c & 3], pp);
+          pk[c] = pack2<BF16>(pp.x, pp.y);
+        }
+        const float2 ls = fadd2(fadd2(lp[0], lp[1]), fadd2(lp[2], lp[3]));
+        l += ls.x + ls.y;
+        tmem_st32(col, pk);
+        tmem_wait_st();
+        return true;
+      };
+      // A sub-tile from key j0 on that some row does not see whole: two passes
+      // of 32 columns at a time, in loops.  It runs once or twice a unit; the
+      // masking among the code above cost whole sub-tiles 5 %, and a masked copy
+      // of that code the time to fetch it.
+      auto masked_step = [&](int i, uint32_t col, int j0) -> bool {
+        auto load32 = [&](int q, float (&v)[32]) {
+          tmem_ld32(col + 32 * q, v);
+          const int k0 = j0 + 32 * q;
+          uint32_t vis = bit_range(0, key_end - 1 - k0);
+          if (p.causal)
+            vis &= bit_range(x - p.window + 1 - k0, 31) | bit_range(0, p.first - 1 - k0);
+          tmem_wait_ld_regs(v);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = ((vis >> c) & 1u) ? v[c] : -INFINITY;
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float v[32];
+          load32(q, v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) mx = fmax3f(mx, v[2 * c], v[2 * c + 1]);
+        }
+        if (!move_max(i, mx)) return false;
+        const float nm = minus_max();
+        const float2 nm2 = make_float2(nm, nm);
+        float2 ls = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float v[32];
+          load32(q, v);
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 xx = ffma2(make_float2(v[2 * c], v[2 * c + 1]), sc2, nm2);
+            const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+            ls = fadd2(ls, pp);
+            pk[c] = pack2<BF16>(pp.x, pp.y);
+          }
+          // over columns that have been read: 16 q + 15 < 32 q + 32
+          tmem_st16(col + 16 * q, pk);
+        }
+        l += ls.x + ls.y;
         tmem_wait_st();
         return true;
       };
@@ -936,7 +970,8 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         ++cnt;
         if (busy) {
           tc_fence_after();
-          ok = full ? softmax(std::false_type{}, i, t, bf) : softmax(std::true_type{}, i, t, bf);
+          const uint32_t col = lane_base + COL_S + 64 * bf;
+          ok = full ? whole_step(i, col) : masked_step(i, col, t * Q_SUB);
           if (!ok) break;
           tc_fence_before();
         }
