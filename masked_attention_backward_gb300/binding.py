@@ -357,17 +357,10 @@ _same_device = contextlib.nullcontext()
 
 def _one_device(*tensors):
     """All tensors on one CUDA device: a guard that makes it current."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        i = t.get_device()
-        if dev is None:
-            dev = i
-        elif i != dev:
-            raise ValueError(f"tensors on cuda:{dev} and cuda:{i}")
+    devs = {t.get_device() for t in tensors if t is not None}
+    dev = devs.pop()
+    if devs or dev < 0:   # -1: a tensor of the host
+        raise ValueError("every tensor must be a CUDA tensor, all on one device")
     return _same_device if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
@@ -384,20 +377,21 @@ class PagedCache:
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, layout: str = "HND"):
         if layout not in ("HND", "NHD"):
             raise ValueError(f"unknown layout {layout!r}")
-        if k_pages.dim() != 4 or k_pages.shape[3] != 128 or v_pages.shape != k_pages.shape:
+        shape = k_pages.shape
+        if len(shape) != 4 or shape[3] != 128 or v_pages.shape != shape:
             raise ValueError("k_pages and v_pages must be [pages, ., ., 128] of one shape")
         if v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device:
             raise ValueError("k_pages and v_pages must have one type and one device")
         hd, td = (1, 2) if layout == "HND" else (2, 1)
-
-        def strides(t):   # a dimension of one element may have any stride
-            return [128 if t.shape[i] == 1 else t.stride(i) for i in (0, hd, td)]
-        if k_pages.stride(3) != 1 or v_pages.stride(3) != 1 or strides(k_pages) != strides(v_pages):
+        # a dimension of one element may have any stride
+        ks, vs = ([128 if n == 1 else m for n, m in zip(shape, t.stride())]
+                  for t in (k_pages, v_pages))
+        if ks != vs or ks[3] != 1:
             raise ValueError("k_pages and v_pages must have the same strides, 1 for the last")
         self.k_pages, self.v_pages, self.layout = k_pages, v_pages, layout
-        self.num_pages, self.Hkv, self.page_size = (k_pages.shape[i] for i in (0, hd, td))
+        self.num_pages, self.Hkv, self.page_size = shape[0], shape[hd], shape[td]
         self.desc = attn_pages_t(self.num_pages, self.page_size, self.Hkv, _dtype_code(k_pages),
-                                 *strides(k_pages))
+                                 ks[0], ks[hd], ks[td])
 
 
 @dataclass
@@ -502,38 +496,40 @@ def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
               ws: Optional[torch.Tensor] = None, out=None, stream=None):
     """Attention of the packed new tokens q [total_q, Hq, 128] over the cache;
     returns (o, lse).  out: (o, lse) to write, of which lse may be None."""
-    if mask.cu_seqlens_q is None or mask.seqlen_k is None or \
-            mask.cu_seqlens_q.numel() != mask.seqlen_k.numel() + 1:
+    cu, lens = mask.cu_seqlens_q, mask.seqlen_k
+    if cu is None or lens is None or cu.numel() != lens.numel() + 1:
         raise ValueError("the mask needs cu_seqlens_q [B + 1] and seqlen_k [B]")
     if q.dim() != 3 or q.shape[0] != mask.total_q or not q.is_contiguous():
         raise ValueError("q must be a contiguous [total_q, Hq, 128] tensor")
-    if q.dtype != cache.k_pages.dtype:
+    T, Hq, _ = q.shape
+    dtype, B = q.dtype, lens.numel()
+    if dtype != cache.k_pages.dtype:
         raise ValueError("q and the cache must have one type")
-    B = mask.seqlen_k.numel()
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B \
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, max_pages]")
+    rows, cols = block_table.shape
+    row_stride, col_stride = block_table.stride()
+    if rows != B or (cols > 1 and col_stride != 1):
         raise ValueError("block_table must be int32 [B, max_pages] with rows of stride 1")
     if sink is not None:
-        _int_tensor(sink, "sink", q.shape[1], torch.float32)
+        _int_tensor(sink, "sink", Hq, torch.float32)
     if out is None:
-        out = (torch.empty_like(q),
-               torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device))
-    o, lse = out
-    if o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
-        raise ValueError("o must be a contiguous tensor like q")
-    if lse is not None:
-        _int_tensor(lse, "lse", q.shape[0] * q.shape[1], torch.float32)
+        o = torch.empty_like(q)
+        lse = torch.empty(Hq, T, dtype=torch.float32, device=q.device)
+    else:
+        o, lse = out
+        if o.shape != q.shape or o.dtype != dtype or not o.is_contiguous():
+            raise ValueError("o must be a contiguous tensor like q")
+        if lse is not None:
+            _int_tensor(lse, "lse", T * Hq, torch.float32)
     shape = paged_shape(q, cache, mask)
-    cols = block_table.shape[1]
-    with _one_device(q, cache.k_pages, block_table, sink, mask.cu_seqlens_q, mask.seqlen_k, o, lse,
-                     ws):
+    with _one_device(q, cache.k_pages, block_table, sink, cu, lens, o, lse, ws):
         if ws is None:
             ws = paged_workspace(q, cache, mask, shape)
         r = attn_paged_fwd(shape, cache.desc, q.data_ptr(), cache.k_pages.data_ptr(),
                            cache.v_pages.data_ptr(), block_table.data_ptr(),
-                           block_table.stride(0) if B > 1 else cols, cols, _ptr(sink), mask.desc(),
-                           scale, o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-                           _stream(stream))
+                           row_stride if B > 1 else cols, cols, _ptr(sink), mask.desc(), scale,
+                           o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
     if r != ATTN_OK:
         raise AttnError(r, "attn_paged_fwd")
     return o, lse
