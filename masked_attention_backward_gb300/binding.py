@@ -592,9 +592,15 @@ class HostBackward:
         flags = ATTN_FLAG_COMPENSATED if compensated else 0
         self.cshapes = [attn_shape_t(B, self.g * kv, kv, Sq, Skv, D, code, flags) for kv in sizes]
         nws = min(3, self.chunks)
-        # each workspace is sized for the largest run, so any run may use it
-        big = attn_shape_t(B, self.g * max(sizes), max(sizes), Sq, Skv, D, code, flags)
-        self.ws = [workspace(big, mask, self.device) for _ in range(nws)]
+        # each workspace is sized for whichever run needs most, so any run may use
+        # it (with first keys a short run may need more than a long one)
+        need = 256
+        for shape in self.cshapes:
+            r, n = attn_workspace_size(shape, mask.desc())
+            if r != ATTN_OK:
+                raise AttnError(r, "attn_workspace_size")
+            need = max(need, n)
+        self.ws = [torch.empty(need, dtype=torch.uint8, device=self.device) for _ in range(nws)]
         self.s_comp = [torch.cuda.Stream(self.device) for _ in range(nws)]
         self.s_in = torch.cuda.Stream(self.device)
         self.s_out = torch.cuda.Stream(self.device)

@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_
          todo &= todo - 1) {
       const int src = __ffs(todo) - 1;
       const long long at = __shfl_sync(0xffffffffu, count + upto.b - held, src);
-      const int moved =
-          (int)min((long long)__shfl_sync(0xffffffffu, held, src), p.num_pages - at);
+      const long long room = max(p.num_pages - at, 0ll);
+      const int moved = (int)min((long long)__shfl_sync(0xffffffffu, held, src), room);
       const int* row = p.block_table + (size_t)(b - lane + src) * p.table_stride;
 #pragma unroll 4
       for (int i = lane; i < moved; i += 32) p.free_pages[at + i] = row[i];

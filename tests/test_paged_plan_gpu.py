@@ -223,3 +223,20 @@ def test_store_past_32_bit_offsets(cuda_lib):
     assert torch.equal(kp[-1, :, -1], k[0]) and torch.equal(vp[-1, :, -1], 2 * k[0])
     assert torch.equal(kp[0, :, 0], k[1]) and torch.equal(vp[0, :, 0], 2 * k[1])
     assert int(torch.count_nonzero(base)) == 2 * int(torch.count_nonzero(k))
+
+
+def test_more_returned_pages_than_an_int(cuda_lib):
+    # lengths that claim 2^27 pages each: nothing past the stack or the rows is touched
+    B, cols = 4096, 2 ** 20
+    table = torch.zeros(1, cols, dtype=torch.int32, device="cuda").expand(B, cols)
+    stack = torch.full((64,), 5, dtype=torch.int32, device="cuda")
+    with pytest.raises(mab.AttnError):   # rows may not overlap
+        mab.paged_plan(_i32([2 ** 31 - 1] * B), _i32([-1] * B), stack[:10].contiguous(), _i32([0]),
+                       table, 16, 0)
+    table = torch.zeros(B, 64, dtype=torch.int32, device="cuda")
+    guarded = torch.full((10 + 4096,), 9, dtype=torch.int32, device="cuda")
+    plan = mab.paged_plan(_i32([2 ** 31 - 1] * B), _i32([-1] * B), guarded[:10], _i32([3]), table,
+                          16, 0)
+    torch.cuda.synchronize()
+    assert int(plan.free_count) == 10 and plan.seqlen_k.sum() == 0
+    assert guarded.tolist() == [9] * 3 + [0] * 7 + [9] * 4096

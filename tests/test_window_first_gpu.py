@@ -251,3 +251,42 @@ def test_wait_that_runs_out_is_reported(cuda_lib, monkeypatch):
     got = mab.bwd(q, k, v, o, dO, lse, sk, mask, SCALE, ws=ws)
     assert mab.device_status(ws) == mab.ATTN_OK
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_without_a_workspace(cuda_lib):
+    S = 1100
+    q, k, v, dO, sk = _inputs(1, 8, 2, S, F16, True, 19)
+    mask = mab.Mask(kind=mab.ATTN_MASK_SLIDING_FIRST, window=100, first=7)
+    o, lse, want = _step(q, k, v, dO, sk, mask)
+    got = [torch.full_like(x, float("nan")) for x in want]
+    stream = torch.cuda.current_stream().cuda_stream
+    r = mab.attn_bwd_noalloc(mab.shape_of(q, k), *(x.data_ptr() for x in (q, k, v, o, dO, lse, sk)),
+                             mask.desc(), SCALE, *(x.data_ptr() for x in got), stream)
+    assert r == mab.ATTN_OK
+    torch.cuda.synchronize()
+    assert mab.attn_noalloc_get_device_status(stream) == mab.ATTN_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_host_pipeline_with_uneven_runs(cuda_lib):
+    # the long run's first-key tiles are not split, the short one's are: its workspace is larger
+    S, H = 2048, 160
+    q, k, v, dO, sk = _inputs(1, H, H, S, BF16, True, 20)
+    mask = mab.Mask(kind=mab.ATTN_MASK_SLIDING_FIRST, window=64, first=3)
+    o, lse, want = _step(q, k, v, dO, sk, mask)
+    host = mab.HostBackward(1, H, H, S, S, BF16, mask, SCALE, True, "cuda", chunks=[100, 60])
+    pin = lambda x: x.cpu().pin_memory()
+    out = tuple(torch.empty_like(x, device="cpu").pin_memory() for x in want)
+    host(dict(q=pin(q), k=pin(k), v=pin(v), o=pin(o), dO=pin(dO), lse=pin(lse), sink=pin(sk)), out)
+    torch.cuda.synchronize()
+    # a run's pieces differ from the whole call's: fp32 sums in another order
+    for n, a, b in zip(("dq", "dk", "dv", "dsink"), out, want):
+        if n in ("dq", "dsink"):
+            assert torch.equal(a, b.cpu()), n
+    ref = attn64.backward(q[:, :2], k[:, :2], v[:, :2], o[:, :2], dO[:, :2], lse[:, :2],
+                          _vis(S, 64, 3), sk[:2], SCALE)
+    last = attn64.backward(q[:, -2:], k[:, -2:], v[:, -2:], o[:, -2:], dO[:, -2:], lse[:, -2:],
+                           _vis(S, 64, 3), sk[-2:], SCALE)
+    for n, a in zip(("dq", "dk", "dv"), out):
+        attn64.check(n, a[:, :2].cuda(), *ref[n])
+        attn64.check(n, a[:, -2:].cuda(), *last[n])
