@@ -639,8 +639,11 @@ cudaError_t launch_dkdv_first(bool bf16, const AttnParams& p, const CUtensorMap&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kern = bf16 ? (p.cu_q ? k_dkdv_first_join<true, true> : k_dkdv_first_join<true, false>)
-                         : (p.cu_q ? k_dkdv_first_join<false, true> : k_dkdv_first_join<false, false>);
+  using Kern = decltype(&k_dkdv_first_join<true, false>);
+  static const Kern table[2][2] = {
+      {k_dkdv_first_join<false, false>, k_dkdv_first_join<false, true>},
+      {k_dkdv_first_join<true, false>, k_dkdv_first_join<true, true>}};
+  const Kern kern = table[bf16 ? 1 : 0][p.cu_q ? 1 : 0];
   return cudaLaunchKernelEx(&cfg, kern, (uint16_t*)dk, (uint16_t*)dv, p);
 }
 

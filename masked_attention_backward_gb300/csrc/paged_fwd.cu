@@ -23,18 +23,32 @@
 // line into equal parts, one per CTA of a persistent grid: a unit that a cut
 // falls into is done in pieces, each leaving its fp32 O, M and l in the
 // workspace, which k_paged_join adds up in order.  So a single request's keys
-// spread over the whole
-// GPU, ragged batches load every SM alike, and the workspace is bounded by two
-// pieces per CTA whatever the lengths, which stay on the device.
+// spread over the whole GPU, ragged batches load every SM alike, and the
+// workspace is bounded by two pieces per CTA whatever the lengths, which stay
+// on the device.  The three kernels overlap by programmatic launches: the
+// attention's set-up runs beside the schedule, and the join's blocks wait
+// beside the attention's last CTAs.
 //
-// The inner loop is that of the BHSD forward kernel (attn_fwd.cu): warp 0
-// loads Q and K, warp 3 V (each a box per run of keys in a page, the page
-// numbers looked up 32 at a time, a batch ahead), warp 1 issues S = Q K^T, warp 2 O += P V, two groups
-// of four softmax warps take alternate steps.  Rows of V that no row of the unit sees (past
-// the last key, before the window, between the first keys and it) may hold
-// anything, NaN included, and 0 * NaN is NaN in the matrix unit: the page runs
-// without a seen key are not loaded (zeros stand in), and warp 2 clears the
-// other unseen rows in shared memory before it multiplies.
+// The inner loop is that of the BHSD forward kernel (attn_fwd.cu): warp 0 loads
+// (a box per run of keys in a page, the page numbers looked up 32 at a time, a
+// batch ahead), warp 1 issues S = Q K^T, warp 2 O += P V, two groups of four
+// softmax warps take alternate steps.  Rows of V that no row of the unit sees
+// (past the last key, before the window, between the first keys and it) may
+// hold anything, NaN included, and 0 * NaN is NaN in the matrix unit: the page
+// runs without a seen key are not loaded (zeros stand in), and warp 2 clears
+// the other unseen rows in shared memory before it multiplies.
+//
+// Measured (one GB300, bf16 unless stated): 64 single tokens at 9000 keys, 64/8
+// heads, 0.350 ms, 6.75 TB/s (16-token pages, [page, row, head], 6.6); 2 at
+// 100000 keys, 32/4 heads, 76 us, 5.4 TB/s; 200 at 300 keys, 32/8 heads, 82 us,
+// latency bound (a unit's start and end, about 5000 cycles, beside 5 steps);
+// chunks of 2048 over 9000 keys, 32/8 heads, 0.45 ms, 1180 TFLOP/s, bound by
+// the latency of S, softmax and P V over three buffers (tensor pipe 56 %
+// active); one token at 1000 keys (fp16) 19 us, of which the schedule takes 4
+// and the join 3.  Kept out, measured: one lane per box in place of an elected
+// lane per load (a chunk's loader 940 cycles a step of 1140), a second loader
+// warp for V, four epilogue warps of their own (every polling warp slows the
+// softmax: a chunk 10 %), the join at the end of the last piece.
 #include <math.h>
 
 #include "paged.h"
@@ -49,15 +63,13 @@ constexpr int NBUF = 3;          // S / P buffers
 constexpr int COL_O = 0;         // O accumulator of group g at COL_O + 128 g
 constexpr int COL_QA = 256;      // Q as the A operand, 64 columns of 16-bit pairs
 constexpr int COL_S = 320;       // S buffer b at COL_S + 64 b
-constexpr int V_WARP = 3;        // loader of V
-constexpr int SM_WARP0 = 4;      // first softmax warp (a warpgroup's first)
+constexpr int SM_WARP0 = 3;      // first softmax warp
 constexpr int SM_WARPS = 8;      // softmax warps, two groups of four
 constexpr int NUM_THREADS = 32 * (SM_WARP0 + SM_WARPS);
 constexpr float RESCALE_LOG2 = 8.f;  // M moves when a row maximum exceeds it by this
-constexpr unsigned LOAD_SLEEP_NS = 100;  // polling period of the loaders' waits
+constexpr unsigned LOAD_SLEEP_NS = 100;  // polling period of the loader's waits
 constexpr int AHEAD = STAGES + 3;  // steps of a unit issued before the next one's Q
 constexpr int SCHED_THREADS = 1024;
-constexpr unsigned long long DRAIN_NS = 10000000ull;  // a copy in flight lands well within 10 ms
 constexpr int NO_PAGE = (int)0x80000000;
 
 // A unit's piece, as the loader publishes it.
@@ -75,7 +87,6 @@ struct __align__(1024) Smem {
   uint8_t V[STAGES][2 * Q_SUB * 128];
   float xml[2][2][Q_TILE][2];   // [unit parity][group][row]: (M, l) at the piece's end
   Unit unit;                    // piece of the latest Q load, N < 0: none left
-  uint64_t bar_unit;            // unit published (for warps that do not wait for Q)
   uint64_t bar_q_full;
   uint64_t bar_qa_full;         // Q copied into TMEM (all softmax warps)
   uint64_t bar_kv_full[STAGES];
@@ -97,7 +108,7 @@ constexpr size_t SMEM_BYTES = sizeof(Smem) + 1024;
 static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may use");
 
 enum { TAG_Q = 0x501, TAG_QA, TAG_KV_EMPTY, TAG_KV_FULL, TAG_S_FULL, TAG_P_FULL, TAG_P_FREE,
-       TAG_ACC, TAG_ACC_EMPTY, TAG_UNIT_FREE, TAG_XML, TAG_UNIT };
+       TAG_ACC, TAG_ACC_EMPTY, TAG_UNIT_FREE, TAG_XML };
 
 template <int NS>
 struct Cyc {
@@ -349,11 +360,10 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
 
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    mbar_init(smem_u32(&s.bar_unit), 1);
     mbar_init(smem_u32(&s.bar_q_full), 1);
     mbar_init(smem_u32(&s.bar_qa_full), SM_WARPS);
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&s.bar_kv_full[i]), 2);
+      mbar_init(smem_u32(&s.bar_kv_full[i]), 1);
       mbar_init(smem_u32(&s.bar_kv_empty[i]), 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -367,7 +377,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     }
     mbar_init(smem_u32(&s.bar_acc_full), 1);
     mbar_init(smem_u32(&s.bar_acc_empty), SM_WARPS);
-    mbar_init(smem_u32(&s.bar_unit_free), SM_WARPS + 3);
+    mbar_init(smem_u32(&s.bar_unit_free), SM_WARPS + 2);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.bar_x_done[i]), 1);
     fence_mbar_init();
     tma_prefetch_desc(&tQ);
@@ -387,13 +397,11 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // Steps [s0, s0 + N) of a unit, K (which = 0) or V: the boxes of each step
-  // into its stage, once that is free; midway() before step AHEAD.
+  // Steps [s0, s0 + N) of a unit: the boxes of each step into its stage, once
+  // that is free; midway() before step AHEAD.
   int m_load = 0;  // steps issued, across units
   Cyc<STAGES> rg_load;
-  auto load_steps = [&](const Walk& w, int which, int b, int kvh, int s0, int N,
-                        auto&& midway) -> bool {
-    const CUtensorMap* tm = which ? &tV : &tK;
+  auto load_steps = [&](const Walk& w, int b, int kvh, int s0, int N, auto&& midway) -> bool {
     const int runs = Q_SUB / p.box_rows;
     const int batch = 32 / runs;  // steps whose pages the lanes look up at once
     const int* row = p.table + (size_t)b * p.table_stride;
@@ -431,25 +439,26 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
                                 LOAD_SLEEP_NS))
         return false;
       const uint32_t fb = smem_u32(&s.bar_kv_full[st]);
-      if (lane == 0) mbar_arrive_expect_tx(fb, 2 * Q_SUB * 128);
+      if (lane == 0) mbar_arrive_expect_tx(fb, 4 * Q_SUB * 128);
       __syncwarp();
-      const uint32_t dst = smem_u32(which ? s.V[st] : s.K[st]);
+      const uint32_t dst_k = smem_u32(s.K[st]), dst_v = smem_u32(s.V[st]);
       for (int r = 0; r < runs; ++r) {
         const int src = (batch - left) * runs + r;
         const int pg = __shfl_sync(0xffffffffu, page, src);
         const int pr = __shfl_sync(0xffffffffu, prow, src);
-        const uint32_t to = dst + r * p.box_rows * 128;
-        tma_load_4d_w(to, tm, 0, pr, kvh, pg, fb);
-        tma_load_4d_w(to + Q_SUB * 128, tm, 64, pr, kvh, pg, fb);
+        const uint32_t k = dst_k + r * p.box_rows * 128, v = dst_v + r * p.box_rows * 128;
+        tma_load_4d_w(k, &tK, 0, pr, kvh, pg, fb);
+        tma_load_4d_w(k + Q_SUB * 128, &tK, 64, pr, kvh, pg, fb);
+        tma_load_4d_w(v, &tV, 0, pr, kvh, pg, fb);
+        tma_load_4d_w(v + Q_SUB * 128, &tV, 64, pr, kvh, pg, fb);
       }
     }
     return true;
   };
-  // A CTA that gives up lets this warp's copies still in flight land first
-  // (the phase may lack the other loader's part, hence the short limit).
+  // a CTA that gives up lets the copies still in flight land first
   auto drain_loads = [&]() {
     for (int k = m_load > STAGES ? m_load - STAGES : 0; k < m_load; ++k)
-      mbar_drain_warp(smem_u32(&s.bar_kv_full[k % STAGES]), (k / STAGES) & 1, DRAIN_NS);
+      mbar_drain_warp(smem_u32(&s.bar_kv_full[k % STAGES]), (k / STAGES) & 1, wc.timeout_ns);
   };
 
   if (warp == 0) {
@@ -485,7 +494,6 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         next.N = -1;  // none is left
         if (lane == 0) {
           s.unit.N = -1;
-          mbar_arrive(smem_u32(&s.bar_unit));
           mbar_arrive(qbar);
         }
         return true;
@@ -503,7 +511,6 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       next.slot = 2 * cta + (step > 0 ? 0 : 1);
       if (lane == 0) {
         s.unit = next;
-        mbar_arrive(smem_u32(&s.bar_unit));
         if (next.N == 0) {
           mbar_arrive(qbar);  // no key to see: no Q either
         } else {
@@ -545,31 +552,15 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       ahead = false;
       // a long unit's successor is published, and its Q loaded, while this
       // one is still being worked on: its consumers have then taken it
-      ok = load_steps(w, 0, next.b, next.kvh, next.s0, next.N, [&]() {
+      ok = load_steps(w, next.b, next.kvh, next.s0, next.N, [&]() {
         ahead = true;
         return publish(j + 1);
       });
     }
     if (!ok) {
-      if (q_loaded >= 0) mbar_drain_warp(qbar, q_loaded & 1, DRAIN_NS);
+      if (q_loaded >= 0) mbar_drain_warp(qbar, q_loaded & 1, wc.timeout_ns);
       drain_loads();
     }
-  } else if (warp == V_WARP) {
-    // ------------------------------------------------------------ loader of V
-    bool ok = true;
-    for (int j = 0; ok; ++j) {
-      if (!mbar_wait_sleep_warp(smem_u32(&s.bar_unit), j & 1, wc, TAG_UNIT, LOAD_SLEEP_NS)) {
-        ok = false;
-        break;
-      }
-      const Unit un = s.unit;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
-      if (un.N < 0) break;
-      const Walk w(p, un.n, un.L, un.tok0);
-      ok = load_steps(w, 1, un.b, un.kvh, un.s0, un.N, []() { return true; });
-    }
-    if (!ok) drain_loads();
   } else if (warp < SM_WARP0) {
     // ------------------------------------------------------------ MMA issuers (whole warps)
     bool ok = true;
