@@ -267,8 +267,9 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def workspace(shape: attn_shape_t, mask: Mask, device) -> torch.Tensor:
-    r, n = attn_workspace_size(shape, mask.desc())
+def workspace(shape: attn_shape_t, mask, device) -> torch.Tensor:
+    """mask: a Mask, or its desc()."""
+    r, n = attn_workspace_size(shape, mask.desc() if isinstance(mask, Mask) else mask)
     if r != ATTN_OK:
         raise AttnError(r, "attn_workspace_size")
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
@@ -288,9 +289,10 @@ def fwd(q, k, v, sink, mask: Mask, scale: float, ws: Optional[torch.Tensor] = No
     o = torch.empty_like(q)
     lse_shape = (q.shape[1], q.shape[0]) if mask.packed else q.shape[:3]   # [Hq, T] when packed
     lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+    desc = mask.desc()
     if ws is None:
-        ws = workspace(shape, mask, q.device)
-    r = attn_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(sink), mask.desc(), scale, _ptr(o),
+        ws = workspace(shape, desc, q.device)
+    r = attn_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(sink), desc, scale, _ptr(o),
                  _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
     if r != ATTN_OK:
         raise AttnError(r, "attn_fwd")
@@ -313,10 +315,11 @@ def bwd(q, k, v, o, dO, lse, sink, mask: Mask, scale: float, ws: Optional[torch.
         dsink = torch.empty_like(sink) if sink is not None else None
     else:
         dq, dk, dv, dsink = out
+    desc = mask.desc()
     if ws is None:
-        ws = workspace(shape, mask, q.device)
+        ws = workspace(shape, desc, q.device)
     r = attn_bwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(sink),
-                 mask.desc(), scale, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dsink), _ptr(ws),
+                 desc, scale, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dsink), _ptr(ws),
                  ws.numel(), _stream(stream))
     if r != ATTN_OK:
         raise AttnError(r, "attn_bwd")

@@ -310,10 +310,14 @@ k_paged_schedule(const PagedParams p, int grid) {
   }
   if (c <= grid) {
     // the unit's own cost stands before its steps; a cut beside its first or
-    // last step moves to the unit's edge
+    // last step moves to the unit's edge, and a cut in a unit of less than
+    // PAGED_MIN_STEPS to the nearer edge
     int step = (int)rem - PAGED_UNIT_COST;
     if (step <= 0) step = 0;
-    if (step > 0 && cost - (int)rem <= 1) {
+    const int steps = cost - PAGED_UNIT_COST;
+    const bool small = steps < PAGED_MIN_STEPS;
+    if (small && 2 * step <= steps) step = 0;
+    if (step > 0 && (small || steps - step <= 1)) {
       step = 0;
       if (++tile == tiles) {
         tile = 0;
