@@ -409,10 +409,8 @@ class PagedPlan:
 
     @staticmethod
     def empty(B: int, max_tokens: int, device) -> "PagedPlan":
-        ints = torch.empty(2 * B + 3 + max_tokens, dtype=torch.int32, device=device)
-        cu, lens, free, refused, position = ints.split((B + 1, B, 1, 1, max_tokens))
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
-        return PagedPlan(cu, lens, free, slots, position, refused)
+        e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=device)
+        return PagedPlan(e(B + 1), e(B), e(1), e(max_tokens, torch.int64), e(max_tokens), e(1))
 
 
 def paged_plan(cached, fresh, free_pages, free_count, block_table, page_size: int,
