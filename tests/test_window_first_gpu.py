@@ -290,3 +290,36 @@ def test_host_pipeline_with_uneven_runs(cuda_lib):
     for n, a in zip(("dq", "dk", "dv"), out):
         attn64.check(n, a[:, :2].cuda(), *ref[n])
         attn64.check(n, a[:, -2:].cuda(), *last[n])
+
+
+@pytest.mark.parametrize("first", [4, 200])
+def test_both_forms_of_the_dkdv_kernel(cuda_lib, monkeypatch, first):
+    # the tiles behind the first keys, per tile and persistent: the same bits
+    S = 900
+    q, k, v, dO, sk = _inputs(2, 8, 4, S, BF16, True, 21)
+    mask = mab.Mask(kind=mab.ATTN_MASK_SLIDING_FIRST, window=70, first=first)
+    runs = []
+    for form in ("tile", "units"):
+        monkeypatch.setenv("MASKATTN_DKDV_SCHEDULE", form)
+        runs.append(_step(q, k, v, dO, sk, mask))
+    monkeypatch.delenv("MASKATTN_DKDV_SCHEDULE")
+    assert all(torch.equal(a, b) for a, b in zip(runs[0][2], runs[1][2]))
+    _check(*runs[1], q, k, v, dO, sk, _vis(S, 70, first))
+
+
+def test_two_streams_at_once(cuda_lib):
+    S = 1200
+    mask = mab.Mask(kind=mab.ATTN_MASK_SLIDING_FIRST, window=100, first=9)
+    data = [_inputs(1, 8, 2, S, F16, True, 30 + i) for i in range(3)]
+    fwd = [mab.fwd(q, k, v, sk, mask, SCALE) for q, k, v, _, sk in data]
+    bwd = lambda i, **kw: mab.bwd(*data[i][:3], *fwd[i][:1], data[i][3], fwd[i][1], data[i][4], mask,
+                                  SCALE, **kw)
+    want = [bwd(i) for i in range(3)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    ws = [mab.workspace(mab.shape_of(d[0], d[1]), mask, "cuda") for d in data]
+    for _ in range(5):
+        got = [bwd(i, ws=ws[i], stream=streams[i]) for i in range(3)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
