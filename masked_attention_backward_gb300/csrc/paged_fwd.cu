@@ -1079,9 +1079,11 @@ cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap&
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  if (sched_smem(p.B) > (47u << 10)) {  // past what a launch may use unasked
+  if (sched_smem(p.B) > (47u << 10)) {
+    // past what a launch may use unasked; the most that any call needs, so that
+    // calls of several host threads do not lower one another's limit
     e = cudaFuncSetAttribute(k_paged_schedule, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sched_smem(p.B));
+                             (int)sched_smem(PAGED_MAX_B));
     if (e != cudaSuccess) return e;
   }
   k_paged_schedule<<<1, SCHED_THREADS, sched_smem(p.B), st>>>(p, p.grid);

@@ -207,9 +207,12 @@ cudaError_t launch_paged_plan(const attn_plan_t& p, cudaStream_t st) {
   int ranks = 1;
   while (ranks < n && ranks < 8) ranks *= 2;
   const size_t smem = (size_t)p.B * 4 * sizeof(int);
-  if (smem + sizeof(Sums) * 64 > (48u << 10)) {  // past what a launch may use unasked
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem + sizeof(Sums) * 64 > (48u << 10)) {
+    // past what a launch may use unasked; the most that any call needs, so that
+    // calls of several host threads do not lower one another's limit
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(PAGED_MAX_B * 4 * sizeof(int)));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

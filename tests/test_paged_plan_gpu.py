@@ -240,3 +240,33 @@ def test_more_returned_pages_than_an_int(cuda_lib):
     torch.cuda.synchronize()
     assert int(plan.free_count) == 10 and plan.seqlen_k.sum() == 0
     assert guarded.tolist() == [9] * 3 + [0] * 7 + [9] * 4096
+
+
+def test_host_threads_with_different_numbers_of_requests(cuda_lib):
+    # both need more shared memory than a launch may use unasked, and the
+    # smaller one must not lower the larger one's limit
+    import threading
+    sizes = (4096, 3500)
+    errors = []
+
+    def work(B):
+        try:
+            fresh, cached = _i32([1] * B), _i32([0] * B)
+            stack, n = _i32(list(range(B))), _i32([B])
+            table = torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+            stream = torch.cuda.Stream()
+            plan = mab.PagedPlan.empty(B, B, "cuda")
+            torch.cuda.synchronize()
+            for _ in range(1000):
+                mab.paged_plan(cached, fresh, stack, n, table, 16, B, out=plan, stream=stream)
+            stream.synchronize()
+            assert plan.refused.item() == 0 and plan.free_count.item() == 0
+        except Exception as e:  # noqa: BLE001 (reported below, from the main thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(B,)) for B in sizes for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[0]
