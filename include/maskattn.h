@@ -304,7 +304,8 @@ attn_status_t attn_paged_workspace_size(const attn_shape_t* shape, size_t* bytes
  * Pages may hold anything, NaN included, in rows past a request's keys, and in
  * those that none of its new tokens sees any more (before the window, past the
  * first keys): pages that left the window may be given back.  Keys and values
- * that some new token sees must be finite.  A page number outside [0,
+ * that some new token sees must be finite.  A row of q that is not finite gets
+ * NaN in its own o and lse alone.  A page number outside [0,
  * num_pages) that holds seen keys is not read: it stands for zeros, and
  * attn_get_device_status then returns ATTN_ERR_INVALID_ARG.
  *

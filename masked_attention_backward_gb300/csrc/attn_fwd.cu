@@ -367,7 +367,10 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUten
         const float Mg[2] = {grp == 0 ? M : Mo, grp == 0 ? Mo : M};
         const float lg[2] = {grp == 0 ? l : lo, grp == 0 ? lo : l};
         const float Mx = fmaxf(Mg[0], Mg[1]);
-        if (Mx > -INFINITY) {
+        if (l + lo != l + lo) {
+          // a query or a logit that is not finite
+          w[0] = w[1] = lse = l + lo;
+        } else if (Mx > -INFINITY) {
           // group 1 has steps only when the unit has two or more; a group's
           // weight is zero when its row saw nothing (l = 0)
           const float e0 = lg[0] > 0.f ? fast_exp2(Mg[0] - Mx) : 0.f;

@@ -169,8 +169,10 @@ __device__ __forceinline__ int unit_cost(const PagedParams& p, int n, int L, int
 }
 
 // Row sum and LSE of a row with maximum m_row and sum l_row, the sink (log2
-// domain) joined; *inv is what the row's O is multiplied by.
+// domain) joined; *inv is what the row's O is multiplied by.  A row whose sum is
+// NaN (a query or a logit that is not finite) gives NaN.
 __device__ __forceinline__ float finish_row(float m_row, float l_row, float sink2, float* inv) {
+  if (l_row != l_row) return *inv = l_row;
   const float top = fmaxf(m_row, sink2);
   *inv = 0.f;
   if (top == -INFINITY) return INFINITY;  // no key and no sink
@@ -690,14 +692,15 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       // two phases late)
       ok = ok && mbar_wait_warp(smem_u32(&s.bar_xml[sp][j & 1]), (j >> 1) & 1, wc, TAG_XML);
       // weights of O_0 and O_1: group 1 has steps only when the piece has two
-      // or more, and a group that saw nothing of a row (l = 0) has none
+      // or more, and a group that saw nothing of a row (l = 0) has none (l is
+      // never negative, and a NaN stays)
       float w0 = 0.f, w1 = 0.f, top = -INFINITY, lsum = 0.f;
       if (ok && N > 0) {
         const float mo = s.xml[j & 1][grp ^ 1][rloc][0], lo = s.xml[j & 1][grp ^ 1][rloc][1];
         const float l0 = grp == 0 ? l : lo, l1 = grp == 0 ? lo : l;
         top = fmaxf(M, mo);
-        if (l0 > 0.f) w0 = fast_exp2((grp == 0 ? M : mo) - top);
-        if (N >= 2 && l1 > 0.f) w1 = fast_exp2((grp == 0 ? mo : M) - top);
+        if (l0 != 0.f) w0 = fast_exp2((grp == 0 ? M : mo) - top);
+        if (N >= 2 && l1 != 0.f) w1 = fast_exp2((grp == 0 ? mo : M) - top);
         lsum = l0 * w0 + l1 * w1;
       }
       float* part = p.part + (size_t)un.slot * p.slot_floats + wq * PAGED_WARP_FLOATS;
@@ -1039,7 +1042,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedParams p) {
   for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
 #pragma unroll
   for (int k = 0; k < MOST; ++k) {
-    m[k] = l[k] > 0.f ? fast_exp2(m[k] - top) : 0.f;  // the piece's weight from here on
+    m[k] = l[k] != 0.f ? fast_exp2(m[k] - top) : 0.f;  // the piece's weight from here on
     sum += l[k] * m[k];
   }
 #pragma unroll

@@ -404,3 +404,20 @@ def test_one_workspace_for_different_calls(cuda_lib):
             o, lse = mab.paged_fwd(c.q, c.cache, c.table, c.sink, c.mask, SCALE, ws=ws)
             torch.cuda.synchronize()
             assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("reqs", [[(1, 40), (3, 90), (70, 300)], [(1, 6000), (1, 9)]])
+def test_a_query_that_is_not_finite_gives_nan(cuda_lib, reqs, bad):
+    # in its own row, whole or in pieces, and in no other
+    c = Case(reqs, seed=50)
+    (o, lse), _ = c.run()
+    for t, h in ((0, 1), (c.T - 1, 2)):
+        c.q[t, h, 5] = bad
+        (o2, lse2), status = c.run()
+        assert status == mab.ATTN_OK
+        assert bool(o2[t, h].isnan().all()) and bool(lse2[h, t].isnan())
+        o2[t, h], lse2[h, t] = o[t, h], lse[h, t]
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
+        c.q[t, h, 5] = 0.5
+        (o, lse), _ = c.run()

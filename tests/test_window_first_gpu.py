@@ -323,3 +323,23 @@ def test_two_streams_at_once(cuda_lib):
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("kind", [mab.ATTN_MASK_CAUSAL, mab.ATTN_MASK_SLIDING,
+                                  mab.ATTN_MASK_SLIDING_FIRST])
+@pytest.mark.parametrize("sink", [True, False])
+def test_a_query_that_is_not_finite_gives_nan(cuda_lib, kind, sink):
+    # in its own row and in no other
+    S = 300
+    q, k, v, _, sk = _inputs(1, 4, 2, S, F16, sink, 60)
+    mask = mab.Mask(kind=kind, window=90, first=5)
+    o, lse = mab.fwd(q, k, v, sk, mask, SCALE)
+    for i in (0, 63, 64, 211, 299):
+        bad = q.clone()
+        bad[0, 2, i, 7] = float("nan")
+        o2, lse2 = mab.fwd(bad, k, v, sk, mask, SCALE)
+        torch.cuda.synchronize()
+        assert bool(o2[0, 2, i].isnan().all()) and bool(lse2.view(4, S)[2, i].isnan())
+        o2[0, 2, i] = o[0, 2, i]
+        lse2.view(4, S)[2, i] = lse.view(4, S)[2, i]
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
