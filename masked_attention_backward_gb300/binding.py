@@ -267,6 +267,15 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+_nothing = contextlib.nullcontext()
+
+
+def _alloc_on(stream):
+    """Tensors that a call makes belong to the stream that it runs on: the
+    allocator reuses a tensor's memory in the order of its own stream."""
+    return _nothing if stream is None else torch.cuda.stream(stream)
+
+
 def workspace(shape: attn_shape_t, mask, device) -> torch.Tensor:
     """mask: a Mask, or its desc()."""
     r, n = attn_workspace_size(shape, mask.desc() if isinstance(mask, Mask) else mask)
@@ -286,12 +295,13 @@ def fwd(q, k, v, sink, mask: Mask, scale: float, ws: Optional[torch.Tensor] = No
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _check(t, n)
     shape = shape_of(q, k, mask=mask)
-    o = torch.empty_like(q)
     lse_shape = (q.shape[1], q.shape[0]) if mask.packed else q.shape[:3]   # [Hq, T] when packed
-    lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
     desc = mask.desc()
-    if ws is None:
-        ws = workspace(shape, desc, q.device)
+    with _alloc_on(stream):
+        o = torch.empty_like(q)
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = workspace(shape, desc, q.device)
     r = attn_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(sink), desc, scale, _ptr(o),
                  _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
     if r != ATTN_OK:
@@ -310,14 +320,15 @@ def bwd(q, k, v, o, dO, lse, sink, mask: Mask, scale: float, ws: Optional[torch.
     flags = (ATTN_FLAG_COMPENSATED if compensated else 0) | \
         (ATTN_FLAG_SINGLE_PASS if single_pass else 0)
     shape = shape_of(q, k, flags, mask=mask)
-    if out is None:
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        dsink = torch.empty_like(sink) if sink is not None else None
-    else:
-        dq, dk, dv, dsink = out
     desc = mask.desc()
-    if ws is None:
-        ws = workspace(shape, desc, q.device)
+    with _alloc_on(stream):
+        if out is None:
+            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+            dsink = torch.empty_like(sink) if sink is not None else None
+        else:
+            dq, dk, dv, dsink = out
+        if ws is None:
+            ws = workspace(shape, desc, q.device)
     r = attn_bwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(sink),
                  desc, scale, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dsink), _ptr(ws),
                  ws.numel(), _stream(stream))
@@ -355,16 +366,13 @@ def attn_paged_fwd(shape, pages, q, k_pages, v_pages, block_table, table_stride,
                                  ctypes.c_float(scale), o, lse, ws, ws_bytes, stream)
 
 
-_same_device = contextlib.nullcontext()
-
-
 def _one_device(*tensors):
     """All tensors on one CUDA device: a guard that makes it current."""
     devs = {t.get_device() for t in tensors if t is not None}
     dev = devs.pop()
     if devs or dev < 0:   # -1: a tensor of the host
         raise ValueError("every tensor must be a CUDA tensor, all on one device")
-    return _same_device if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _nothing if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _int_tensor(t: torch.Tensor, name: str, numel: int, dtype=torch.int32):
@@ -429,7 +437,8 @@ def paged_plan(cached, fresh, free_pages, free_count, block_table, page_size: in
             or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be int32 [B, max_pages] with rows of stride 1")
     if out is None:
-        out = PagedPlan.empty(B, max_tokens, cached.device)
+        with _alloc_on(stream):
+            out = PagedPlan.empty(B, max_tokens, cached.device)
     else:
         for t, n, m in ((out.cu_seqlens_q, "cu_seqlens_q", B + 1), (out.seqlen_k, "seqlen_k", B),
                         (out.free_count, "out.free_count", 1), (out.refused, "refused", 1),
@@ -515,8 +524,9 @@ def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
     if sink is not None:
         _int_tensor(sink, "sink", Hq, torch.float32)
     if out is None:
-        o = torch.empty_like(q)
-        lse = torch.empty(Hq, T, dtype=torch.float32, device=q.device)
+        with _alloc_on(stream):
+            o = torch.empty_like(q)
+            lse = torch.empty(Hq, T, dtype=torch.float32, device=q.device)
     else:
         o, lse = out
         if o.shape != q.shape or o.dtype != dtype or not o.is_contiguous():
@@ -526,7 +536,8 @@ def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
     shape = paged_shape(q, cache, mask)
     with _one_device(q, cache.k_pages, block_table, sink, cu, lens, o, lse, ws):
         if ws is None:
-            ws = paged_workspace(q, cache, mask, shape)
+            with _alloc_on(stream):
+                ws = paged_workspace(q, cache, mask, shape)
         r = attn_paged_fwd(shape, cache.desc, q.data_ptr(), cache.k_pages.data_ptr(),
                            cache.v_pages.data_ptr(), block_table.data_ptr(),
                            row_stride if B > 1 else cols, cols, _ptr(sink), mask.desc(), scale,
