@@ -12,6 +12,13 @@
 // The group reduction happens in the TMEM accumulators; the epilogue scales
 // dK, rounds both to the input dtype and writes each row once, contiguously.
 //
+// A sliding window with first keys runs this kernel twice: over the tiles that
+// hold first keys, which every later query sees, each walk in pieces (unsplit,
+// one such tile takes as long as half the grid), and over the others, which
+// have the plain window's walks.  The first grid's pieces leave fp32 sums for
+// k_dkdv_first_join, which runs beside the second.  S 8192, 32/8 heads, window
+// 1024, 4 first keys, bf16: the backward 415 us, 365 for the window alone.
+//
 // Sources: tilelang-ascend PR #1 "Add GQA Sink Backward BHSD", commit notes
 // (five contractions + softmax + dS per step; GQA group of query heads per
 // key/value head); cannbot-knowledge PR #174, BlockSparseAttentionGrad
