@@ -40,7 +40,7 @@
 //
 // Measured (one GB300, bf16 unless stated): 64 single tokens at 9000 keys, 64/8
 // heads, 0.350 ms, 6.75 TB/s (16-token pages, [page, row, head], 6.6); 2 at
-// 100000 keys, 32/4 heads, 76 us, 5.4 TB/s; 200 at 300 keys, 32/8 heads, 78 us,
+// 100000 keys, 32/4 heads, 76 us, 5.4 TB/s; 200 at 300 keys, 32/8 heads, 72 us,
 // latency bound (a unit's start and end, about 5000 cycles, beside 5 steps);
 // chunks of 2048 over 9000 keys, 32/8 heads, 0.45 ms, 1180 TFLOP/s, bound by
 // the latency of S, softmax and P V over three buffers (tensor pipe 56 %
@@ -717,26 +717,32 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       ok = ok && mbar_wait_warp(smem_u32(&s.bar_acc_full), j & 1, wc, TAG_ACC);
       tc_fence_after();
       // 16 columns at a time, in a loop: this code runs once a unit, and as one
-      // straight piece most of its time went into fetching it
+      // straight piece most of its time went into fetching it.  (O of a group
+      // that saw nothing of a row is zero there; group 1 without a step has the
+      // weight zero, and O_0 stands in.)
       if (ok && nr > 0) {
+        const uint32_t o1 = N >= 2 ? 128u : 0u;
+        const float2 w02 = make_float2(w0, w0), w12 = make_float2(w1, w1);
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           float a0[16], a1[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) a0[c] = a1[c] = 0.f;
           const uint32_t col = lane_base + COL_O + 64 * grp + 16 * q;
           if (N > 0) {
             tmem_ld16(col, a0);
-            if (N >= 2) tmem_ld16(col + 128, a1);
+            tmem_ld16(col + o1, a1);
             tmem_wait_ld_regs(a0);
 #pragma unroll
             for (int c = 0; c < 16; ++c) asm volatile("" : "+f"(a1[c]));
-          }
-          // (a row of weight zero may hold anything)
+          } else {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            a0[c] = w0 != 0.f ? a0[c] * w0 : 0.f;
-            a0[c] = w1 != 0.f ? fmaf(a1[c], w1, a0[c]) : a0[c];
+            for (int c = 0; c < 16; ++c) a0[c] = a1[c] = 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2 x = ffma2(make_float2(a1[2 * c], a1[2 * c + 1]), w12,
+                                   fmul2(make_float2(a0[2 * c], a0[2 * c + 1]), w02));
+            a0[2 * c] = x.x;
+            a0[2 * c + 1] = x.y;
           }
           if (whole) {
             // through shared memory, so that a row's 128 bytes leave together
@@ -760,7 +766,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.bar_acc_empty));
       if (ok && nr > 0 && whole) {
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int row = k * 4 + (lane >> 3), c = lane & 7;
           const long long to = __shfl_sync(0xffffffffu, row_at, row);
