@@ -51,7 +51,7 @@ attn_status_t check_paged_shape(const attn_shape_t* sh) {
 }
 
 struct PagedLayout {
-  size_t status, start, part, total;
+  size_t status, cta_status, start, part, total;
   int tile_tokens, tile_rows, slot_floats;
 };
 
@@ -64,6 +64,8 @@ PagedLayout paged_layout(const attn_shape_t* sh) {
   size_t off = 0;
   L.status = off;
   off = align256(off + sizeof(DevStatus));
+  L.cta_status = off;
+  off = align256(off + PAGED_MAX_CTAS * sizeof(DevStatus));
   L.start = off;
   off = align256(off + (PAGED_MAX_CTAS + 1) * sizeof(PagedStart));
   L.part = off;
@@ -194,6 +196,7 @@ attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* page
   p.lse = lse;
   p.scale_log2 = scale * LOG2E;
   p.status = reinterpret_cast<DevStatus*>(w + L.status);
+  p.cta_status = reinterpret_cast<DevStatus*>(w + L.cta_status);
   p.timeout_ns = wait_timeout_ns();
   p.test_no_loads = test_no_loads();
   p.start = reinterpret_cast<PagedStart*>(w + L.start);

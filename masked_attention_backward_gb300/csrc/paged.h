@@ -12,7 +12,7 @@ constexpr int PAGED_MAX_CTAS = 152;  // CTAs of the attention grid at most (one 
 // (M, l) [32 rows].
 constexpr int PAGED_ML = 32 * 64;
 constexpr int PAGED_WARP_FLOATS = PAGED_ML + 32 * 2;
-// On the line that the schedule cuts, in steps of 64 keys: what a unit costs
+// On the line of all units, in steps of 64 keys: what a unit costs
 // beside its steps (measured: a causal chunk of 8192 took 535 us at 3, 475 at 6,
 // 478 at 9), the least part that a CTA gets (one token at 8000 keys took 20.6 us
 // at 8, 22.7 at 11, 26.8 at 20), and the steps below which a unit is not cut (a
@@ -43,7 +43,8 @@ struct PagedParams {
   uint16_t* out;
   float* lse;  // or nullptr
   float scale_log2;
-  DevStatus* status;
+  DevStatus* status;      // of the call
+  DevStatus* cta_status;  // [grid] of each CTA
   unsigned long long timeout_ns;
   int test_no_loads;
   int grid;          // CTAs

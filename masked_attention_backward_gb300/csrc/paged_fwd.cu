@@ -19,15 +19,17 @@
 // token moves 32 KB and costs the tensor pipe 540 cycles, an SM's share of the
 // HBM rate 1400, so the idle rows cost nothing there.
 //
-// Balance: k_paged_schedule lays all units end to end, in steps, and cuts the
-// line into equal parts, one per CTA of a persistent grid: a unit that a cut
-// falls into is done in pieces, each leaving its fp32 O, M and l in the
-// workspace, which k_paged_join adds up in order.  So a single request's keys
-// spread over the whole GPU, ragged batches load every SM alike, and the
+// Balance: every CTA of a persistent grid lays all units end to end, in steps,
+// for itself, cuts the line into equal parts, one per CTA, and takes its own: a
+// unit that a cut falls into is done in pieces, each leaving its fp32 O, M and l
+// in the workspace, which k_paged_join adds up in order.  So a single request's
+// keys spread over the whole GPU, ragged batches load every SM alike, and the
 // workspace is bounded by two pieces per CTA whatever the lengths, which stay
-// on the device.  The three kernels overlap by programmatic launches: the
-// attention's set-up runs beside the schedule, and the join's blocks wait
-// beside the attention's last CTAs.
+// on the device.  (The line laid once, by a kernel before this one: 4 to 9 us
+// until the first CTA had its part, 2.5 to 4 now; a window of 1024 over 8192
+// keys 197 -> 189 us, 15 single tokens and a chunk of 500 51 -> 49, 4096
+// requests of 64 keys 99 -> 102.)  The join's blocks wait beside the
+// attention's last CTAs (programmatic launch).
 //
 // The inner loop is that of the BHSD forward kernel (attn_fwd.cu): warp 0 loads
 // (a box per run of keys in a page, the page numbers looked up 32 at a time, a
@@ -44,7 +46,7 @@
 // latency bound (a unit's start and end, about 5000 cycles, beside 5 steps);
 // chunks of 2048 over 9000 keys, 32/8 heads, 0.45 ms, 1180 TFLOP/s, bound by
 // the latency of S, softmax and P V over three buffers (tensor pipe 56 %
-// active); one token at 1000 keys (fp16) 19 us, of which the schedule takes 4
+// active); one token at 1000 keys (fp16) 18.6 us, of which the line takes 2.5
 // and the join 3.  Kept out, measured: one lane per box in place of an elected
 // lane per load (a chunk's loader 940 cycles a step of 1140), a second loader
 // warp for V, four epilogue warps of their own (every polling warp slows the
@@ -69,8 +71,13 @@ constexpr int NUM_THREADS = 32 * (SM_WARP0 + SM_WARPS);
 constexpr float RESCALE_LOG2 = 8.f;  // M moves when a row maximum exceeds it by this
 constexpr unsigned LOAD_SLEEP_NS = 100;  // polling period of the loader's waits
 constexpr int AHEAD = STAGES + 3;  // steps of a unit issued before the next one's Q
-constexpr int SCHED_THREADS = 1024;
 constexpr int NO_PAGE = (int)0x80000000;
+
+// The warps' shares of the line: cost and units.
+struct LineSums {
+  long long cost[NUM_THREADS / 32];
+  int units[NUM_THREADS / 32];
+};
 
 // A unit's piece, as the loader publishes it.
 struct Unit {
@@ -86,6 +93,8 @@ struct __align__(1024) Smem {
   uint8_t K[STAGES][2 * Q_SUB * 128];
   uint8_t V[STAGES][2 * Q_SUB * 128];
   float xml[2][2][Q_TILE][2];   // [unit parity][group][row]: (M, l) at the piece's end
+  LineSums sums;
+  PagedStart cut[2];            // where this CTA's part begins and ends
   Unit unit;                    // piece of the latest Q load, N < 0: none left
   uint64_t bar_q_full;
   uint64_t bar_qa_full;         // Q copied into TMEM (all softmax warps)
@@ -121,10 +130,6 @@ struct Cyc {
     }
   }
 };
-
-// The schedule's shared memory for B requests: costs, new tokens, keys, rows.
-constexpr size_t sched_smem(int B) { return (size_t)(B + 1) * 8 + (size_t)B * 12; }
-static_assert(PAGED_MAX_CTAS < 32 * 32, "one lane of the schedule's block per cut");
 
 // a / b of non-negative numbers, in 32 bits where they fit.
 __device__ __forceinline__ long long quot(long long a, long long b) {
@@ -168,6 +173,170 @@ __device__ __forceinline__ int unit_cost(const PagedParams& p, int n, int L, int
   return Walk(p, n, L, tile * p.tile_tokens).cnt + PAGED_UNIT_COST;
 }
 
+// The line of all units as every CTA lays it out for itself, in the memory of
+// the K / V ring: cost of the requests before each, and their new tokens, keys
+// and first rows.
+struct Line {
+  long long* base;  // [B + 1]
+  int *n, *L, *off; // [B]
+};
+__device__ __forceinline__ Line line_at(void* mem, int B) {
+  Line l;
+  l.base = static_cast<long long*>(mem);
+  l.n = reinterpret_cast<int*>(l.base + B + 1);
+  l.L = l.n + B;
+  l.off = l.L + B;
+  return l;
+}
+static_assert((PAGED_MAX_B + 1) * 8 + PAGED_MAX_B * 12 <= sizeof(Smem::K) + sizeof(Smem::V),
+              "the line of the most requests fits the ring");
+
+// Lays the line out (all threads of the block); returns the number of parts it
+// is cut into: one per unit while there are CTAs, and parts of at least
+// PAGED_MIN_COST, since further cuts would cost more to join.
+__device__ int lay_line(const PagedParams& p, const Line& line, LineSums& sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + NUM_THREADS - 1) / NUM_THREADS;  // requests of a thread
+  long long mine = 0;
+  int units = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    int n = 0, L = 0, tiles = 0;
+    if (b < p.B) {
+      n = new_tokens(p, b);
+      L = keys_of(p, b);
+      tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
+      line.n[b] = n;
+      line.L[b] = L;
+      line.off[b] = packed_off(p.cu_q, b, p.total_q);
+    }
+    long long w = tiles > 0 ? unit_cost(p, n, L, 0) : 0;
+    // several tiles: the warp adds their costs, one request after another
+    for (unsigned todo = __ballot_sync(0xffffffffu, tiles > 1); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int sn = __shfl_sync(0xffffffffu, n, src), sL = __shfl_sync(0xffffffffu, L, src);
+      const int st = __shfl_sync(0xffffffffu, tiles, src);
+      long long sum = 0;
+      for (int t = lane; t < st; t += 32) sum += unit_cost(p, sn, sL, t);
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == src) w = sum;
+    }
+    if (b < p.B) line.base[b] = mine;  // of this thread's requests so far
+    mine += w * p.Hkv;
+    units = min(units + min(tiles, PAGED_MAX_CTAS) * p.Hkv, 1 << 24);
+  }
+  // exclusive sums over the block
+  long long v = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  units = __reduce_add_sync(0xffffffffu, units);
+  if (lane == 31) {
+    sums.cost[warp] = v;
+    sums.units[warp] = units;
+  }
+  __syncthreads();
+  long long total = 0, before = v - mine;
+  units = 0;
+#pragma unroll
+  for (int w = 0; w < NUM_THREADS / 32; ++w) {
+    if (w < warp) before += sums.cost[w];
+    total += sums.cost[w];
+    units = min(units + sums.units[w], 1 << 24);
+  }
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < p.B) line.base[tid * per + i] += before;
+  if (tid == 0) line.base[p.B] = total;
+  __syncthreads();
+  const long long most = max(total / PAGED_MIN_COST, (long long)units);
+  return (int)(most < 1 ? 1 : most < p.grid ? most : p.grid);
+}
+
+// Where cut c of `parts` falls (one warp, all lanes alike).
+__device__ PagedStart cut_of(const PagedParams& p, const Line& line, int parts, int c) {
+  const int lane = threadIdx.x & 31;
+  PagedStart r;
+  r.b = p.B;  // past the last unit
+  r.kvh = r.tile = r.step = r.first_cut = r.cuts = r.off = r.n = r.L = 0;
+  const long long total = line.base[p.B];
+  const long long cut = c < parts ? quot(total * c, parts) : total;
+  if (cut >= total) return r;
+  int lo = 0, hi = p.B - 1;  // the request that holds the cut: the last with base <= cut
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (line.base[mid] <= cut) lo = mid;
+    else hi = mid - 1;
+  }
+  int b = lo;
+  const int n = line.n[b], L = line.L[b];
+  const int tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
+  const long long head = quot(line.base[b + 1] - line.base[b], p.Hkv);
+  int kvh = (int)quot(cut - line.base[b], head);
+  // the cut's distance from the start of the head, then of the unit
+  long long rem = (cut - line.base[b]) - kvh * head;
+  int tile = 0, cost = (int)head;  // of the only tile
+  if (tiles > 1) {
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+      const int mine = t0 + lane < tiles ? unit_cost(p, n, L, t0 + lane) : 0;
+      int v = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += u;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, v > rem);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        tile = t0 + at;
+        cost = __shfl_sync(0xffffffffu, mine, at);
+        rem -= __shfl_sync(0xffffffffu, v, at) - cost;
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  // the unit's own cost stands before its steps; a cut beside its first or
+  // last step moves to the unit's edge, and a cut in a unit of less than
+  // PAGED_MIN_STEPS to the nearer edge
+  int step = (int)rem - PAGED_UNIT_COST;
+  if (step <= 0) step = 0;
+  const int steps = cost - PAGED_UNIT_COST;
+  const bool small = steps < PAGED_MIN_STEPS;
+  if (small && 2 * step <= steps) step = 0;
+  if (step > 0 && (small || steps - step <= 1)) {
+    step = 0;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++kvh == p.Hkv) {
+        kvh = 0;
+        ++b;
+        while (b < p.B && line.base[b + 1] == line.base[b]) ++b;
+      }
+    }
+  }
+  // cuts inside the unit: those that lie more than its own cost past its
+  // start and more than one step before its end (cut c is at
+  // floor(c total / parts))
+  if (step > 0) {
+    const long long u0 = cut - rem;
+    r.first_cut = (int)quot((u0 + PAGED_UNIT_COST + 1) * parts + total - 1, total);
+    r.cuts = (int)quot((u0 + cost - 1) * parts + total - 1, total) - r.first_cut;
+  }
+  r.b = b;
+  r.kvh = kvh;
+  r.tile = tile;
+  r.step = step;
+  if (b < p.B) {
+    r.off = line.off[b];
+    r.n = line.n[b];
+    r.L = line.L[b];
+  }
+  return r;
+}
+
 // Row sum and LSE of a row with maximum m_row and sum l_row, the sink (log2
 // domain) joined; *inv is what the row's O is multiplied by.  A row whose sum is
 // NaN (a query or a logit that is not finite) gives NaN.
@@ -186,173 +355,6 @@ __device__ __forceinline__ float finish_row(float m_row, float l_row, float sink
 
 }  // namespace paged_side
 
-// One block.  Lays the units (request, kv head, query tile) end to end and
-// writes where each CTA's part begins.
-__global__ void __launch_bounds__(paged_side::SCHED_THREADS)
-k_paged_schedule(const PagedParams p, int grid) {
-  using namespace paged_side;
-  grid_launch_dependents();
-  extern __shared__ long long base[];  // [B + 1] cost of the requests before b
-  int* s_n = reinterpret_cast<int*>(base + p.B + 1);  // [B] new tokens
-  int* s_L = s_n + p.B;                               // [B] keys
-  int* s_off = s_L + p.B;                             // [B] first row
-  __shared__ long long warp_tot[32];
-  __shared__ int s_units;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_units = 0;
-  __syncthreads();
-  long long carry = 0;
-  for (int b0 = 0; b0 < p.B; b0 += SCHED_THREADS) {
-    const int b = b0 + tid;
-    int n = 0, L = 0, tiles = 0;
-    if (b < p.B) {
-      n = new_tokens(p, b);
-      L = keys_of(p, b);
-      tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
-      s_n[b] = n;
-      s_L[b] = L;
-      s_off[b] = packed_off(p.cu_q, b, p.total_q);
-    }
-    long long w = tiles > 0 ? unit_cost(p, n, L, 0) : 0;
-    // several tiles: the warp adds their costs, one request after another
-    for (unsigned todo = __ballot_sync(0xffffffffu, tiles > 1); todo; todo &= todo - 1) {
-      const int src = __ffs(todo) - 1;
-      const int sn = __shfl_sync(0xffffffffu, n, src), sL = __shfl_sync(0xffffffffu, L, src);
-      const int st = __shfl_sync(0xffffffffu, tiles, src);
-      long long sum = 0;
-      for (int t = lane; t < st; t += 32) sum += unit_cost(p, sn, sL, t);
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == src) w = sum;
-    }
-    w *= p.Hkv;
-    const int units = __reduce_add_sync(0xffffffffu, min(tiles, PAGED_MAX_CTAS) * p.Hkv);
-    if (lane == 0 && units) atomicAdd(&s_units, min(units, 1 << 16));
-    // inclusive scan over the block
-    long long v = w;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v += u;
-    }
-    __syncthreads();
-    if (lane == 31) warp_tot[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      long long u = warp_tot[lane];
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, u, d);
-        if (lane >= d) u += x;
-      }
-      warp_tot[lane] = u;
-    }
-    __syncthreads();
-    if (warp > 0) v += warp_tot[warp - 1];
-    if (b < p.B) base[b] = carry + v - w;
-    carry += warp_tot[31];
-  }
-  if (tid == 0) base[p.B] = carry;
-  if (tid < (int)(sizeof(DevStatus) / 4)) reinterpret_cast<unsigned*>(p.status)[tid] = 0u;
-  __syncthreads();
-  const long long total = carry;
-  // a CTA for each unit while there are CTAs, and parts of at least
-  // PAGED_MIN_COST: further cuts would cost more to join
-  const long long most = max(total / PAGED_MIN_COST, (long long)s_units);
-  const int parts = (int)(most < 1 ? 1 : most < grid ? most : grid);
-  // lane l of warp w places cut w + 32 l
-  const int c = warp + 32 * lane;
-  const long long cut = c < parts ? quot(total * c, parts) : total;
-  int b = p.B, kvh = 0, tile = 0, tiles = 0, cost = 0, n = 0, L = 0;  // past the last unit
-  long long rem = 0;  // the cut's distance from the start of the head, then of the unit
-  if (c <= grid && cut < total) {
-    int lo = 0, hi = p.B - 1;  // the request that holds the cut: the last with base <= cut
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (base[mid] <= cut) lo = mid;
-      else hi = mid - 1;
-    }
-    b = lo;
-    const long long head = quot(base[b + 1] - base[b], p.Hkv);
-    kvh = (int)quot(cut - base[b], head);
-    rem = (cut - base[b]) - kvh * head;
-    n = s_n[b];
-    L = s_L[b];
-    tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
-    cost = (int)head;  // of the only tile
-  }
-  // several tiles: the warp looks for the cut's, one cut after another
-  for (unsigned todo = __ballot_sync(0xffffffffu, tiles > 1); todo; todo &= todo - 1) {
-    const int src = __ffs(todo) - 1;
-    const int sn = __shfl_sync(0xffffffffu, n, src), sL = __shfl_sync(0xffffffffu, L, src);
-    const int st = __shfl_sync(0xffffffffu, tiles, src);
-    long long srem = __shfl_sync(0xffffffffu, rem, src);
-    for (int t0 = 0; t0 < st; t0 += 32) {
-      const int mine = t0 + lane < st ? unit_cost(p, sn, sL, t0 + lane) : 0;
-      long long v = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += u;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, v > srem);
-      if (past) {
-        const int at = __ffs(past) - 1;
-        const int found = __shfl_sync(0xffffffffu, mine, at);
-        const long long upto = __shfl_sync(0xffffffffu, v, at);
-        if (lane == src) {
-          tile = t0 + at;
-          cost = found;
-          rem = srem - (upto - found);
-        }
-        break;
-      }
-      srem -= __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
-  if (c <= grid) {
-    // the unit's own cost stands before its steps; a cut beside its first or
-    // last step moves to the unit's edge, and a cut in a unit of less than
-    // PAGED_MIN_STEPS to the nearer edge
-    int step = (int)rem - PAGED_UNIT_COST;
-    if (step <= 0) step = 0;
-    const int steps = cost - PAGED_UNIT_COST;
-    const bool small = steps < PAGED_MIN_STEPS;
-    if (small && 2 * step <= steps) step = 0;
-    if (step > 0 && (small || steps - step <= 1)) {
-      step = 0;
-      if (++tile == tiles) {
-        tile = 0;
-        if (++kvh == p.Hkv) {
-          kvh = 0;
-          ++b;
-          while (b < p.B && base[b + 1] == base[b]) ++b;
-        }
-      }
-    }
-    // cuts inside the unit: those that lie more than its own cost past its
-    // start and more than one step before its end (cut c is at
-    // floor(c total / parts))
-    int first = 0, cuts = 0;
-    if (step > 0) {
-      const long long u0 = cut - rem;
-      first = (int)quot((u0 + PAGED_UNIT_COST + 1) * parts + total - 1, total);
-      cuts = (int)quot((u0 + cost - 1) * parts + total - 1, total) - first;
-    }
-    PagedStart r;
-    r.b = b;
-    r.kvh = kvh;
-    r.tile = tile;
-    r.step = step;
-    r.first_cut = first;
-    r.cuts = cuts;
-    r.off = b < p.B ? s_off[b] : 0;
-    r.n = b < p.B ? s_n[b] : 0;
-    r.L = b < p.B ? s_L[b] : 0;
-    p.start[c] = r;
-  }
-}
-
 template <bool BF16>
 __global__ void __launch_bounds__(paged_side::NUM_THREADS, 1)
 k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
@@ -362,10 +364,12 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                      ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  WaitCtx wc{p.status, &s.abort_flag, p.timeout_ns};
+  // this CTA's own status word, which the join passes on
+  WaitCtx wc{p.cta_status + blockIdx.x, &s.abort_flag, p.timeout_ns};
 
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
+    *wc.status = DevStatus{};
     mbar_init(smem_u32(&s.bar_q_full), 1);
     mbar_init(smem_u32(&s.bar_qa_full), SM_WARPS);
     for (int i = 0; i < STAGES; ++i) {
@@ -398,10 +402,22 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = s.tmem_base;
-  // launched over the schedule kernel: its cuts are read from here on; the
-  // join's blocks may wait beside this grid
-  grid_dependency_wait();
-  grid_launch_dependents();
+  grid_launch_dependents();  // the join's blocks may wait beside this grid
+
+  {
+    const Line line = line_at(s.K, p.B);
+    const int parts = lay_line(p, line, s.sums);
+    if (warp < 2) {
+      const PagedStart at = cut_of(p, line, parts, (int)blockIdx.x + warp);
+      if (lane == 0) {
+        s.cut[warp] = at;
+        if (warp == 1) p.start[blockIdx.x + 1] = at;  // for the join
+      }
+    }
+    // the loads into the ring come after these generic accesses to it
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+  }
 
   // Steps [s0, s0 + N) of a unit: the boxes of each step into its stage, once
   // that is free; midway() before step AHEAD.
@@ -434,7 +450,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         left = batch;
         if ((unsigned)page >= (unsigned)p.num_pages) {
           // past the tensor's end, where a load reads zeros
-          if (page != NO_PAGE) atomicCAS(&p.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);
+          if (page != NO_PAGE) atomicCAS(&wc.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);
           page = p.num_pages;
         }
         next = pages_of(i + batch);  // a batch ahead
@@ -470,7 +486,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   if (warp == 0) {
     // ------------------------------------------------------------ loader of Q and K
     const int cta = (int)blockIdx.x;
-    const PagedStart at0 = p.start[cta], end = p.start[cta + 1];
+    const PagedStart at0 = s.cut[0], end = s.cut[1];
     int b = at0.b, kvh = at0.kvh, tile = at0.tile, step = at0.step;  // where this CTA stands
     int off = at0.off, n = at0.n, L = at0.L;                         // of request b
     bool ok = !p.test_no_loads;
@@ -1010,6 +1026,27 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedParams p) {
   const int lane = threadIdx.x & 31, c = (int)blockIdx.x;
   const int row = (int)blockIdx.y * 8 + (threadIdx.x >> 5);
   grid_dependency_wait();
+  if (c == p.grid - 1) {
+    // the last CTA's part ends with the line: here the CTAs' statuses are
+    // passed on, the first one that is not 0
+    if (blockIdx.y == 0 && threadIdx.x < 32) {
+      unsigned code = 0, v[(PAGED_MAX_CTAS + 31) / 32];
+#pragma unroll
+      for (int k = 0; k < (PAGED_MAX_CTAS + 31) / 32; ++k)
+        v[k] = 32 * k + lane < p.grid ? __ldcg(&p.cta_status[32 * k + lane].code) : 0u;
+#pragma unroll
+      for (int k = (PAGED_MAX_CTAS + 31) / 32 - 1; k >= 0; --k) {
+        const unsigned set = __ballot_sync(0xffffffffu, v[k] != 0u);
+        if (set) code = __shfl_sync(0xffffffffu, v[k], __ffs(set) - 1);
+      }
+      if (lane == 0) {
+        DevStatus st{};
+        st.code = code;
+        *p.status = st;
+      }
+    }
+    return;
+  }
   const PagedStart u = p.start[c + 1];
   const int tok0 = u.tile * p.tile_tokens;
   if (u.step == 0 || u.first_cut != c + 1 ||
@@ -1088,28 +1125,18 @@ cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap&
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  if (sched_smem(p.B) > (47u << 10)) {
-    // past what a launch may use unasked; the most that any call needs, so that
-    // calls of several host threads do not lower one another's limit
-    e = cudaFuncSetAttribute(k_paged_schedule, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sched_smem(PAGED_MAX_B));
-    if (e != cudaSuccess) return e;
-  }
-  k_paged_schedule<<<1, SCHED_THREADS, sched_smem(p.B), st>>>(p, p.grid);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = st;
+  e = cudaLaunchKernelEx(&cfg, kern, tQ, tK, tV, p);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tQ, tK, tV, p);
-  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((p.tile_rows + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
