@@ -18,10 +18,14 @@
 // that an output may alias; then all threads of the cluster write the tokens'
 // entries, a binary search in shared memory finding each token's request.  A
 // new page's number is taken from the stack, not from the table entry another
-// CTA may be writing.  Measured (one GB300, replayed): 8 decodes 6.2 us, 512
-// requests with 16384 tokens 16.4 us (41 with a thread, not a warp, moving each
-// request's pages).
+// CTA may be writing.  Page numbers are moved by all threads too, whichever
+// request they belong to, by the same search: a warp per request took 35 us for
+// one of 100000 tokens that ended among 64 decodes, now 7.5.  Measured (one GB300, replayed):
+// 8 decodes 6.2 us, 512 requests with 16384 tokens 12.3 (16.4 with a warp per
+// request and one token at a time).
 #include <limits.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "paged.h"
@@ -31,6 +35,13 @@ namespace mab {
 namespace {
 
 constexpr int PLAN_THREADS = 1024;
+// Pages or tokens that a thread handles at a time: four when it has several,
+// whose searches and loads then overlap (512 requests and 16384 tokens: 13.8 us
+// one after another, 11.8 so), else one, the shorter code (8 single tokens: 4.8
+// us, 4.9 with the longer).
+template <int K>
+using Width = std::integral_constant<int, K>;
+constexpr int PLAN_INTS = 6;  // shared ints per request
 
 struct Sums {
   long long a, b;
@@ -66,6 +77,19 @@ __device__ Sums block_scan(Sums v, Sums* warp_tot) {
   return warp > 0 ? warp_tot[warp - 1] + v : v;
 }
 
+// For K x at a time: how many of n non-decreasing ends are <= x, which is the
+// first entry whose range holds x.
+template <int K>
+__device__ __forceinline__ void find(const int* end, int n, const int (&x)[K], int (&at)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) at[k] = 0;
+  for (int s = 1 << (31 - __clz(n)); s > 0; s >>= 1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (at[k] + s <= n && end[at[k] + s - 1] <= x[k]) at[k] += s;
+  }
+}
+
 __device__ __forceinline__ int clamp_int(long long x) {
   return x > INT_MAX ? INT_MAX : (int)x;
 }
@@ -73,13 +97,17 @@ __device__ __forceinline__ int clamp_int(long long x) {
 }  // namespace
 
 __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_t p) {
-  // per request: the end of its tokens, its cached tokens, the needed pages of
-  // the requests before it, and its own (REFUSED, ENDED: none)
+  // per request: the ends of its tokens, of the pages that it returns and of
+  // those that it needs, where its pages begin among the needed ones less the
+  // held ones, its cached tokens, and the pages that it needs (REFUSED, ENDED:
+  // none)
   extern __shared__ int smem[];
   int* s_end = smem;
-  int* s_cached = s_end + p.B;
-  int* s_need0 = s_cached + p.B;
-  int* s_grant = s_need0 + p.B;
+  int* s_ret = s_end + p.B;
+  int* s_need = s_ret + p.B;
+  int* s_from = s_need + p.B;
+  int* s_cached = s_from + p.B;
+  int* s_grant = s_cached + p.B;
   constexpr int REFUSED = -1, ENDED = -2;
   __shared__ Sums warp_tot[PLAN_THREADS / 32];
   __shared__ int s_refused, s_granted;
@@ -89,6 +117,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_
   const unsigned ps = (unsigned)p.page_size;
   const long long cap = (long long)p.max_pages * p.page_size;
   const int count = min(max(*p.free_count, 0), p.num_pages);
+  auto pages_of = [&](int n) -> int { return (int)(((unsigned)n + ps - 1) / ps); };
   if (tid == 0) s_refused = s_granted = 0;
 
   Sums carry{0, 0};          // tokens and returned pages of the chunks before
@@ -99,36 +128,60 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_
     if (b < p.B) {
       cached = max(p.cached[b], 0);
       fresh = p.fresh[b];
-      held = min((int)(((unsigned)cached + ps - 1) / ps), p.max_pages);
+      held = min(pages_of(cached), p.max_pages);
     }
     const bool ended = fresh < 0;
     const Sums upto =
         block_scan(Sums{ended ? 0 : fresh, ended ? held : 0}, warp_tot) + carry;
     carry = carry + warp_tot[PLAN_THREADS / 32 - 1];
-    // one warp of the cluster moves an ended request's pages
-    for (unsigned todo = __ballot_sync(0xffffffffu, ended && b % nranks == rank); todo;
-         todo &= todo - 1) {
-      const int src = __ffs(todo) - 1;
-      const long long at = __shfl_sync(0xffffffffu, count + upto.b - held, src);
-      const long long room = max(p.num_pages - at, 0ll);
-      const int moved = (int)min((long long)__shfl_sync(0xffffffffu, held, src), room);
-      const int* row = p.block_table + (size_t)(b - lane + src) * p.table_stride;
-#pragma unroll 4
-      for (int i = lane; i < moved; i += 32) p.free_pages[at + i] = row[i];
-    }
     // what can never be placed needs no page
     const bool bad = !ended && ((long long)cached + fresh > cap || upto.a > p.max_tokens);
-    const int need = ended || bad ? 0 : (int)(((unsigned)(cached + fresh) + ps - 1) / ps) - held;
+    const int need = ended || bad ? 0 : pages_of(cached + fresh) - held;
     const long long need_upto = block_scan(Sums{need, 0}, warp_tot).a + need_carry;
     need_carry += warp_tot[PLAN_THREADS / 32 - 1].a;
     if (b < p.B) {
       s_end[b] = clamp_int(upto.a);
+      s_ret[b] = clamp_int(upto.b);
       s_cached[b] = cached;
-      s_need0[b] = clamp_int(need_upto - need);
+      s_need[b] = clamp_int(need_upto);
+      s_from[b] = clamp_int(need_upto - need) - held;
       s_grant[b] = ended ? ENDED : bad ? REFUSED : need;
     }
   }
   const int avail = (int)min(count + carry.b, (long long)p.num_pages);
+  // Copies n page numbers, those of request b up to ends[b], spread over all
+  // threads of the cluster: at(b, i, x, from, to) says where number i of request
+  // b, x of all, comes from and goes to.
+  auto spread = [&](const int* ends, int n, auto at) {
+    auto go = [&](auto width) {
+      constexpr int K = decltype(width)::value;
+      for (unsigned x0 = gtid; x0 < (unsigned)n; x0 += K * gthreads) {
+        int x[K], b[K], page[K];
+        int* to[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[k] = (int)min(x0 + k * gthreads, (unsigned)n - 1);
+        find(ends, p.B, x, b);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int* from;
+          at(b[k], x[k] - (b[k] > 0 ? ends[b[k] - 1] : 0), x[k], from, to[k]);
+          page[k] = *from;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (x0 + k * gthreads < (unsigned)n) *to[k] = page[k];
+      }
+    };
+    if (n > gthreads) go(Width<4>());
+    else go(Width<1>());
+  };
+  // the returned pages onto the stack
+  __syncthreads();
+  const int moved = avail - count;
+  spread(s_ret, moved, [&](int b, int i, int x, const int*& from, int*& to) {
+    from = &p.block_table[(size_t)b * p.table_stride + i];
+    to = &p.free_pages[count + x];
+  });
   // every input that an output may alias has been read, and the returned
   // pages are on the stack
   cluster_sync();
@@ -137,9 +190,12 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_
   // no later one does
   for (int b = tid; b < p.B; b += PLAN_THREADS) {
     const int g = s_grant[b];
-    if (g > 0 && (long long)s_need0[b] + g > avail) s_grant[b] = REFUSED;
+    if (g > 0) {
+      const long long end = (long long)s_from[b] + pages_of(s_cached[b]) + g;
+      if (end > avail) s_grant[b] = REFUSED;
+      else atomicMax(&s_granted, (int)end);
+    }
     if (s_grant[b] == REFUSED) atomicAdd(&s_refused, 1);
-    if (s_grant[b] > 0) atomicMax(&s_granted, s_need0[b] + g);
   }
   __syncthreads();
   const int total = min(s_end[p.B - 1], p.max_tokens);
@@ -148,57 +204,58 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) k_paged_plan(const attn_plan_
     *p.free_count_out = avail - s_granted;
     *p.refused = s_refused;
   }
-  // requests in whole warps: one that gets many pages has all lanes append them
-  for (int b0 = gtid - lane; b0 < p.B; b0 += gthreads) {
-    const int b = b0 + lane;
-    int g = 0, held = 0, need0 = 0;
-    if (b < p.B) {
-      const int cached = s_cached[b];
-      g = s_grant[b];
-      need0 = s_need0[b];
-      p.cu_seqlens_q[b + 1] = s_end[b];
-      p.seqlen_k[b] = g == ENDED     ? 0
-                      : g == REFUSED ? cached
-                                     : cached + s_end[b] - (b > 0 ? s_end[b - 1] : 0);
-      held = (int)(((unsigned)cached + ps - 1) / ps);
-    }
-    auto append = [&](int to, int have, int first, int i) {
-      p.block_table[(size_t)to * p.table_stride + have + i] = p.free_pages[avail - 1 - first - i];
-    };
-    if (g <= 4)
-      for (int i = 0; i < g; ++i) append(b, held, need0, i);
-    for (unsigned todo = __ballot_sync(0xffffffffu, g > 4); todo; todo &= todo - 1) {
-      const int src = __ffs(todo) - 1;
-      const int n = __shfl_sync(0xffffffffu, g, src), h = __shfl_sync(0xffffffffu, held, src);
-      const int first = __shfl_sync(0xffffffffu, need0, src);
-      for (int i = lane; i < n; i += 32) append(b0 + src, h, first, i);
-    }
+  for (int b = gtid; b < p.B; b += gthreads) {
+    const int g = s_grant[b];
+    p.cu_seqlens_q[b + 1] = s_end[b];
+    p.seqlen_k[b] = g == ENDED     ? 0
+                    : g == REFUSED ? s_cached[b]
+                                   : s_cached[b] + s_end[b] - (b > 0 ? s_end[b - 1] : 0);
   }
-  for (int t = gtid; t < p.max_tokens; t += gthreads) {
-    long long slot = -1;
-    int pos = -1;
-    if (t < total) {
-      // the first request whose tokens end past t
-      int lo = 0, hi = p.B - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s_end[mid] > t) hi = mid;
-        else lo = mid + 1;
+  spread(s_need, s_granted, [&](int b, int i, int x, const int*& from, int*& to) {
+    from = &p.free_pages[avail - 1 - x];
+    to = &p.block_table[(size_t)b * p.table_stride + pages_of(s_cached[b]) + i];
+  });
+  auto place = [&](auto width) {
+    constexpr int K = decltype(width)::value;
+    const unsigned tokens = (unsigned)p.max_tokens;
+    for (unsigned t0 = gtid; t0 < tokens; t0 += K * gthreads) {
+      int x[K], at[K], pos[K], off[K];
+      const int* src[K];  // where the page of a placed token stands
+#pragma unroll
+      for (int k = 0; k < K; ++k) x[k] = (int)min(t0 + k * gthreads, tokens - 1);
+      // the requests: the first whose tokens end past the token
+      find(s_end, p.B, x, at);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        src[k] = nullptr;
+        pos[k] = -1;
+        off[k] = 0;
+        if (x[k] < total) {
+          const int b = at[k], cached = s_cached[b];
+          pos[k] = clamp_int((long long)cached + (x[k] - (b > 0 ? s_end[b - 1] : 0)));
+          if (s_grant[b] >= 0) {
+            const int i = (int)((unsigned)pos[k] / ps), first = i * (int)ps;
+            off[k] = pos[k] - first;
+            src[k] = first < cached ? &p.block_table[(size_t)b * p.table_stride + i]
+                                    : &p.free_pages[avail - 1 - s_from[b] - i];
+          }
+        }
       }
-      const int cached = s_cached[lo];
-      pos = clamp_int((long long)cached + (t - (lo > 0 ? s_end[lo - 1] : 0)));
-      if (s_grant[lo] >= 0) {
-        const int held = (int)(((unsigned)cached + ps - 1) / ps);
-        const int i = (int)((unsigned)pos / ps);
-        const int page = i < held ? p.block_table[(size_t)lo * p.table_stride + i]
-                                  : p.free_pages[avail - 1 - s_need0[lo] - (i - held)];
-        if (page >= 0 && page < p.num_pages)
-          slot = (long long)page * p.page_size + pos - i * p.page_size;
-      }
+      int page[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) page[k] = src[k] ? *src[k] : -1;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (t0 + k * gthreads < tokens) {
+          p.slot_map[x[k]] = page[k] >= 0 && page[k] < p.num_pages
+                                 ? (long long)page[k] * p.page_size + off[k]
+                                 : -1;
+          p.position[x[k]] = pos[k];
+        }
     }
-    p.slot_map[t] = slot;
-    p.position[t] = pos;
-  }
+  };
+  if (p.max_tokens > gthreads) place(Width<4>());
+  else place(Width<1>());
 }
 
 cudaError_t launch_paged_plan(const attn_plan_t& p, cudaStream_t st) {
@@ -206,13 +263,13 @@ cudaError_t launch_paged_plan(const attn_plan_t& p, cudaStream_t st) {
   const long long n = ((long long)p.max_tokens + 4 * PLAN_THREADS - 1) / (4 * PLAN_THREADS);
   int ranks = 1;
   while (ranks < n && ranks < 8) ranks *= 2;
-  const size_t smem = (size_t)p.B * 4 * sizeof(int);
+  const size_t smem = (size_t)p.B * PLAN_INTS * sizeof(int);
   if (smem + sizeof(Sums) * 64 > (48u << 10)) {
     // past what a launch may use unasked; the most that any call needs, so that
     // calls of several host threads do not lower one another's limit
     const cudaError_t e =
         cudaFuncSetAttribute(k_paged_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(PAGED_MAX_B * 4 * sizeof(int)));
+                             (int)(PAGED_MAX_B * PLAN_INTS * sizeof(int)));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -270,3 +270,24 @@ def test_host_threads_with_different_numbers_of_requests(cuda_lib):
     for t in threads:
         t.join()
     assert not errors, errors[0]
+
+
+@pytest.mark.parametrize("T", [300, 5000])
+def test_few_requests_with_many_pages(cuda_lib, T):
+    # long requests that end, and long chunks, beside others: more pages and
+    # tokens than the cluster has threads, and fewer
+    ps, cols = 16, 3200
+    cached = [50000, 0, 17, 40000, 16, 0, 33, 30000]
+    fresh = [-1, T - 290, 1, -1, 200, 0, -1, 80]
+    r = random.Random(5)
+    pages = list(range(9000))
+    r.shuffle(pages)
+    table, at = [], 0
+    for c in cached:
+        h = -(-c // ps)
+        table.append(pages[at:at + h] + [-5] * (cols - h))
+        at += h
+    stack = pages[at:] + [-3] * at
+    _compare(cached, fresh, stack, len(pages) - at, table, ps, T)
+    # the same with too few free pages for the last ones
+    _compare(cached, fresh, stack, 1, table, ps, T)
