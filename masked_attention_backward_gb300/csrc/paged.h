@@ -8,7 +8,7 @@ namespace mab {
 
 constexpr int PAGED_MAX_B = 4096;    // requests of one call
 constexpr int PAGED_MAX_CTAS = 152;  // CTAs of the attention grid at most (one per SM)
-// A warp's share of a piece in the workspace: O [32 rows, 64 columns], then
+// A warp's share of a piece in the workspace: O [4][32 rows, 16 columns], then
 // (M, l) [32 rows].
 constexpr int PAGED_ML = 32 * 64;
 constexpr int PAGED_WARP_FLOATS = PAGED_ML + 32 * 2;

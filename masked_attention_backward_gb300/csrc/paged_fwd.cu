@@ -337,6 +337,16 @@ __device__ PagedStart cut_of(const PagedParams& p, const Line& line, int parts, 
   return r;
 }
 
+// Columns 4 j .. 4 j + 3 of a row in a warp's share of a piece: 16 columns of a
+// row, then the same of the next row, so that a warp that writes a row per lane
+// touches 16 lines a store, not 32 (row by row a piece's end took 5000 cycles,
+// a unit's 1800), and one that reads a row 8, not 4 (8 columns: 8 and 16; 15
+// single tokens and a chunk of 500: 16 columns 43.2 us, rows 44.2; 5 tokens at
+// 100000 keys: 8 columns 76.5, 16 75.0, rows 73.5).
+__device__ __forceinline__ float4* part_at(float* part, int row, int j) {
+  return reinterpret_cast<float4*>(part + ((j >> 2) * 32 + row) * 16) + (j & 3);
+}
+
 // Row sum and LSE of a row with maximum m_row and sum l_row, the sink (log2
 // domain) joined; *inv is what the row's O is multiplied by.  A row whose sum is
 // NaN (a query or a logit that is not finite) gives NaN.
@@ -770,10 +780,10 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
                              pack2<BF16>(a0[8 * h + 4], a0[8 * h + 5]),
                              pack2<BF16>(a0[8 * h + 6], a0[8 * h + 7]));
           } else if (mine) {
-            float4* dst = reinterpret_cast<float4*>(part + lane * 64 + 16 * q);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              dst[c] = make_float4(a0[4 * c], a0[4 * c + 1], a0[4 * c + 2], a0[4 * c + 3]);
+              *part_at(part, lane, 4 * q + c) =
+                  make_float4(a0[4 * c], a0[4 * c + 1], a0[4 * c + 2], a0[4 * c + 3]);
           }
         }
       }
@@ -1016,10 +1026,12 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
 // Adds up the pieces of the units that a cut fell into, in their order, and
 // stores them: block (c, y) the rows 8 y .. 8 y + 7 of the unit whose first
 // piece is CTA c's last one, a warp per row, 4 columns a lane.  Latency bound:
-// one lane per piece for the weights, and the first 16 pieces' rows on their
-// way before those are known.  (Joined by the last warp to finish inside the
-// kernel above, 19 pieces took 5 to 15 us and the code slowed its loop by 5 %;
-// with four rows a warp one after another they took 15 us more than now.)
+// one lane per piece for the weights, and the first two pieces' rows on their
+// way before those are known (with 16, whose registers left two blocks on an SM,
+// 15 single tokens and a chunk of 500 took 43.1 us, 37.9 now).  (Joined by the
+// last warp to finish inside the kernel above, 19 pieces took 5 to 15 us and the
+// code slowed its loop by 5 %; with four rows a warp one after another they took
+// 15 us more than now.)
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_paged_join(const PagedParams p) {
   using namespace paged_side;
@@ -1053,20 +1065,21 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedParams p) {
       row >= min(p.tile_tokens, u.n - tok0) * p.group)
     return;
   const int pieces = u.cuts + 1;
-  // this row in piece i (slots: 2 c + 1, then those of the CTAs that go on),
-  // from column 64 half on
+  // this row's warp share in piece i (slots: 2 c + 1, then those of the CTAs
+  // that go on), columns from 64 half on
   const int sp = row >> 5, r = row & 31;
-  auto piece = [&](int i, int half) -> const float* {
+  auto piece = [&](int i, int half) -> float* {
     return p.part + (size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * p.slot_floats +
            (2 * sp + half) * PAGED_WARP_FLOATS;
   };
   auto values = [&](int i) -> float4 {
-    return __ldcg(reinterpret_cast<const float4*>(piece(i, lane >> 4) + r * 64) + (lane & 15));
+    return __ldcg(part_at(piece(i, lane >> 4), r, lane & 15));
   };
-  constexpr int EARLY = 16;
+  constexpr int EARLY = 2;
   float4 v[EARLY];
 #pragma unroll
-  for (int i = 0; i < EARLY; ++i) v[i] = values(min(i, pieces - 1));
+  for (int i = 0; i < EARLY; ++i)
+    v[i] = i < pieces ? values(i) : make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int MOST = (PAGED_MAX_CTAS + 31) / 32;  // pieces a lane may know
   float m[MOST], l[MOST], top = -INFINITY, sum = 0.f;
 #pragma unroll
