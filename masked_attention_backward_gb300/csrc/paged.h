@@ -12,11 +12,12 @@ constexpr int PAGED_MAX_CTAS = 152;  // CTAs of the attention grid at most (one 
 // (M, l) [32 rows].
 constexpr int PAGED_ML = 32 * 64;
 constexpr int PAGED_WARP_FLOATS = PAGED_ML + 32 * 2;
-// On the line of all units, in steps of 64 keys: what a unit costs
-// beside its steps (measured: a causal chunk of 8192 took 535 us at 3, 475 at 6,
-// 478 at 9), the least part that a CTA gets (one token at 8000 keys took 20.6 us
-// at 8, 22.7 at 11, 26.8 at 20), and the steps below which a unit is not cut (a
-// chunk of 300 over nothing took 24.7 us when it was, 20.6 when not).
+// On the line of all units, in steps of 64 keys: what a unit costs beside its
+// steps (measured: a causal chunk of 8192 took 465 us at 5, 460 at 6, 462 at 7, a
+// chunk of 300 over nothing 14.2, 15.0, 14.4; at 2 the chunk of 8192 took 20 %
+// more), the least part that a CTA gets (one token at 8000 keys took 20.6 us at 8,
+// 22.7 at 11, 26.8 at 20), and the steps below which a unit is not cut (at 5 and 8
+// a chunk of 300 took 16.4 and 14.4 us, 200 single tokens at 300 keys 78 and 70).
 constexpr int PAGED_UNIT_COST = 7;
 constexpr int PAGED_MIN_COST = 8;
 constexpr int PAGED_MIN_STEPS = 8;

@@ -26,9 +26,9 @@
 // keys spread over the whole GPU, ragged batches load every SM alike, and the
 // workspace is bounded by two pieces per CTA whatever the lengths, which stay
 // on the device.  (The line laid once, by a kernel before this one: 4 to 9 us
-// until the first CTA had its part, 2.5 to 4 now; a window of 1024 over 8192
-// keys 197 -> 189 us, 15 single tokens and a chunk of 500 51 -> 49, 4096
-// requests of 64 keys 99 -> 102.)  The join's blocks wait beside the
+// until the first CTA had its part, 2.5 to 4 now: a window of 1024 over 8192
+// keys took 197 us so and 189 without, 15 single tokens and a chunk of 500 51
+// and 49, 4096 requests of 64 keys 99 and 102.)  The join's blocks wait beside the
 // attention's last CTAs (programmatic launch).
 //
 // The inner loop is that of the BHSD forward kernel (attn_fwd.cu): warp 0 loads
@@ -41,12 +41,12 @@
 // the other unseen rows in shared memory before it multiplies.
 //
 // Measured (one GB300, bf16 unless stated): 64 single tokens at 9000 keys, 64/8
-// heads, 0.350 ms, 6.75 TB/s (16-token pages, [page, row, head], 6.6); 2 at
-// 100000 keys, 32/4 heads, 76 us, 5.4 TB/s; 200 at 300 keys, 32/8 heads, 72 us,
+// heads, 0.348 ms, 6.78 TB/s (16-token pages, [page, row, head], 6.5); 2 at
+// 100000 keys, 32/4 heads, 74 us, 5.5 TB/s; 200 at 300 keys, 32/8 heads, 70 us,
 // latency bound (a unit's start and end, about 5000 cycles, beside 5 steps);
-// chunks of 2048 over 9000 keys, 32/8 heads, 0.45 ms, 1180 TFLOP/s, bound by
+// chunks of 2048 over 9000 keys, 32/8 heads, 0.434 ms, 1230 TFLOP/s, bound by
 // the latency of S, softmax and P V over three buffers (tensor pipe 56 %
-// active); one token at 1000 keys (fp16) 18.6 us, of which the line takes 2.5
+// active); one token at 1000 keys (fp16) 16 us, of which the line takes 2.5
 // and the join 3.  Kept out, measured: one lane per box in place of an elected
 // lane per load (a chunk's loader 940 cycles a step of 1140), a second loader
 // warp for V, four epilogue warps of their own (every polling warp slows the
