@@ -421,3 +421,18 @@ def test_a_query_that_is_not_finite_gives_nan(cuda_lib, reqs, bad):
         assert torch.equal(o2, o) and torch.equal(lse2, lse)
         c.q[t, h, 5] = 0.5
         (o, lse), _ = c.run()
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(353, 8, 2), (705, 4, 1), (4096, 1, 1)])
+def test_more_requests_than_threads(cuda_lib, B, Hq, Hkv):
+    # several requests a thread where the work is laid out: requests without new
+    # tokens, without keys, with several query tiles, with long contexts
+    r = random.Random(B)
+    reqs = []
+    for b in range(B):
+        n = r.choice([0, 1, 1, 1, 2, 5])
+        reqs.append((n, n + r.choice([0, 0, 3, 40, 64, 130])))
+    for b in (0, 31, 32, B // 2, B - 1):
+        reqs[b] = (300, 420)
+    reqs[7], reqs[B - 2] = (1, 5000), (0, 0)
+    _go(reqs, Hq=Hq, Hkv=Hkv, ps=64 if B > 1000 else 16, seed=B)
