@@ -321,7 +321,7 @@ def bwd(q, k, v, o, dO, lse, sink, mask: Mask, scale: float, ws: Optional[torch.
         (ATTN_FLAG_SINGLE_PASS if single_pass else 0)
     shape = shape_of(q, k, flags, mask=mask)
     desc = mask.desc()
-    with _alloc_on(stream):
+    with _alloc_on(stream if out is None or ws is None else None):
         if out is None:
             dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
             dsink = torch.empty_like(sink) if sink is not None else None
