@@ -368,8 +368,10 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUten
         const float lg[2] = {grp == 0 ? l : lo, grp == 0 ? lo : l};
         const float Mx = fmaxf(Mg[0], Mg[1]);
         if (l + lo != l + lo) {
-          // a query or a logit that is not finite
-          w[0] = w[1] = lse = l + lo;
+          // a query or a logit that is not finite (group 1 without a step has no
+          // O_1: what stands there is read by no row)
+          w[0] = lse = l + lo;
+          if (N >= 2) w[1] = w[0];
         } else if (Mx > -INFINITY) {
           // group 1 has steps only when the unit has two or more; a group's
           // weight is zero when its row saw nothing (l = 0)
