@@ -216,7 +216,9 @@ AttnParams params_of(const attn_shape_t* sh, const attn_mask_desc_t* mk, const W
   p.Skv = sh->Skv;
   p.group = sh->Hq / sh->Hkv;
   p.Sq_pad = d.Sq_pad;
-  p.window = mk->kind == ATTN_MASK_SLIDING ? mk->window : 0;
+  // a window longer than the sequence sees no more than one of its length; the
+  // kernels add positions to it in 32 bits
+  if (mk->kind == ATTN_MASK_SLIDING) p.window = mk->window < sh->Sq ? mk->window : sh->Sq;
   p.mask_kind = mask_kind_of(sh, mk);
   if (mk->kind == ATTN_MASK_SLIDING_FIRST) {
     p.window = mk->window;
