@@ -71,7 +71,6 @@ constexpr int NUM_THREADS = 32 * (SM_WARP0 + SM_WARPS);
 constexpr float RESCALE_LOG2 = 8.f;  // M moves when a row maximum exceeds it by this
 constexpr unsigned LOAD_SLEEP_NS = 100;  // polling period of the loader's waits
 constexpr int AHEAD = STAGES + 3;  // steps of a unit issued before the next one's Q
-constexpr int NO_PAGE = (int)0x80000000;
 
 // The warps' shares of the line: cost and units.
 struct LineSums {
@@ -437,20 +436,22 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     const int runs = Q_SUB / p.box_rows;
     const int batch = 32 / runs;  // steps whose pages the lanes look up at once
     const int* row = p.table + (size_t)b * p.table_stride;
-    // lane l: page of run l % runs of step i + l / runs (NO_PAGE: a run without
-    // a seen key), and the run's first row in the page
+    // lane l has run l % runs of step i + l / runs: its first key, whether it
+    // holds a seen one, and its page (past the last where it holds none) and
+    // first row there
     const int l_step = lane / runs, l_run = lane - l_step * runs;
+    auto key_of = [&](int i) { return w.tile(i + l_step) * Q_SUB + l_run * p.box_rows; };
+    auto seen = [&](int i, int k0) {
+      return i + l_step < s0 + N && w.any(k0, k0 + p.box_rows);
+    };
     int row0 = 0;
     auto pages_of = [&](int i) -> int {
-      i += l_step;
-      const int k0 = w.tile(i) * Q_SUB + l_run * p.box_rows;
+      const int k0 = key_of(i);
       const int idx = div_by(k0, p.page_size, p.inv_page_size);
       row0 = k0 - idx * p.page_size;
-      int page = NO_PAGE;
-      if (i < s0 + N && w.any(k0, k0 + p.box_rows)) page = __ldg(row + idx);
-      return page;
+      return seen(i, k0) ? __ldg(row + idx) : p.num_pages;
     };
-    int page = NO_PAGE, prow = 0, next = pages_of(s0), next_row = row0, left = 0;
+    int page = p.num_pages, prow = 0, next = pages_of(s0), next_row = row0, left = 0;
     for (int i = s0; i < s0 + N; ++i, ++m_load, rg_load.next(), --left) {
       const int st = rg_load.i;
       if (i == s0 + AHEAD && !midway()) return false;
@@ -460,7 +461,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         left = batch;
         if ((unsigned)page >= (unsigned)p.num_pages) {
           // past the tensor's end, where a load reads zeros
-          if (page != NO_PAGE) atomicCAS(&wc.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);
+          if (seen(i, key_of(i))) atomicCAS(&wc.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);
           page = p.num_pages;
         }
         next = pages_of(i + batch);  // a batch ahead
