@@ -348,9 +348,9 @@ __device__ __forceinline__ float4* part_at(float* part, int row, int j) {
 
 // Row sum and LSE of a row with maximum m_row and sum l_row, the sink (log2
 // domain) joined; *inv is what the row's O is multiplied by.  A row whose sum is
-// NaN (a query or a logit that is not finite) gives NaN.
+// NaN (a query or a logit that is not finite), or whose sink is, gives NaN.
 __device__ __forceinline__ float finish_row(float m_row, float l_row, float sink2, float* inv) {
-  if (l_row != l_row) return *inv = l_row;
+  if (l_row != l_row || sink2 != sink2) return *inv = l_row + sink2;
   const float top = fmaxf(m_row, sink2);
   *inv = 0.f;
   if (top == -INFINITY) return INFINITY;  // no key and no sink

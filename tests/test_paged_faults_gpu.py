@@ -39,3 +39,21 @@ def test_unseen_entries_are_not_looked_at(cuda_lib):
     c.table[c.table == -7] = -2 ** 31
     (o, lse), status = c.run()
     assert status == mab.ATTN_OK and torch.equal(o, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("reqs", [[(1, 40), (3, 90), (70, 300)], [(1, 6000), (1, 9)]])
+def test_a_sink_that_is_not_a_number_gives_nan(cuda_lib, reqs):
+    # in its own head, whole units and joined ones, and in no other
+    c = Case(reqs, seed=12)
+    (want, wl), _ = c.run()
+    c.sink[1] = math.nan
+    (o, lse), status = c.run()
+    assert status == mab.ATTN_OK
+    assert bool(o[:, 1].isnan().all()) and bool(lse[1].isnan().all())
+    o[:, 1], lse[1] = want[:, 1], wl[1]
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+    # rows that see no key too
+    c.lens.zero_()
+    (o, lse), status = c.run()
+    assert bool(o[:, 1].isnan().all()) and bool(lse[1].isnan().all())
+    assert bool((o[:, 0] == 0).all()) and not bool(lse[0].isnan().any())
