@@ -163,7 +163,9 @@ attn_status_t attn_workspace_size(const attn_shape_t* shape, const attn_mask_des
 /* Forward: O = softmax_with_sink(scale * q k^T, masked) v, and
  * lse[b,h,i] = log(sum_j exp(scale*s_ij) + exp(sink_h)) over visible j.
  * sink may be NULL (no sink).  A row with no visible key and no sink gets
- * O = 0 and lse = +inf.  Outputs: o (dtype), lse (float32). */
+ * O = 0 and lse = +inf.  A row of q that is not finite gets NaN in its own o
+ * and lse alone; where every logit that it sees is -inf, these weigh nothing,
+ * as for a row with no visible key.  Outputs: o (dtype), lse (float32). */
 attn_status_t attn_fwd(const attn_shape_t* shape, const void* q, const void* k, const void* v,
                        const float* sink, const attn_mask_desc_t* mask, float scale, void* o,
                        float* lse, void* ws, size_t ws_bytes, void* stream);
@@ -305,7 +307,9 @@ attn_status_t attn_paged_workspace_size(const attn_shape_t* shape, size_t* bytes
  * those that none of its new tokens sees any more (before the window, past the
  * first keys): pages that left the window may be given back.  Keys and values
  * that some new token sees must be finite.  A row of q that is not finite gets
- * NaN in its own o and lse alone.  A page number outside [0,
+ * NaN in its own o and lse alone; where every logit that it sees is -inf (an
+ * infinite element against keys of the other sign there) these weigh nothing,
+ * and it gets what a row that sees no key does.  A page number outside [0,
  * num_pages) that holds seen keys is not read: it stands for zeros, and
  * attn_get_device_status then returns ATTN_ERR_INVALID_ARG.
  *

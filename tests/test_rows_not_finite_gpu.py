@@ -78,3 +78,49 @@ def test_short_sequences_after_long_ones(cuda_lib, L):
     assert bool(o[:, :, L - 1].isnan().all()) and bool(lse[:, :, L - 1].isnan().all())
     assert torch.equal(o[:, :, :L - 1], want[:, :, :L - 1])
     assert torch.equal(lse[:, :, :L - 1], want_lse[:, :, :L - 1])
+
+
+# An infinite element of a query against keys that are all of one sign there:
+# logits of +inf alone (inf - inf: NaN) or of -inf alone (they weigh nothing).
+@pytest.mark.parametrize("sink", [True, False])
+@pytest.mark.parametrize("keys", [1, 2, 63, 64, 130])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_an_infinite_query_over_keys_of_one_sign(cuda_lib, sign, keys, sink):
+    g = torch.Generator("cuda").manual_seed(keys)
+    r = lambda h: torch.randn(1, h, keys, 128, generator=g, device="cuda").to(F16)
+    q, k, v = r(4), r(2), r(2)
+    k[..., 5] = k[..., 5].abs() + 0.1
+    sk = torch.tensor([0.5, -0.5, 1.0, -1.0], device="cuda") if sink else None
+    want, want_lse = mab.fwd(q, k, v, sk, mab.Mask(kind=mab.ATTN_MASK_CAUSAL), SCALE)
+    rows = sorted({0, keys // 2, keys - 1})
+    bad = q.clone()
+    bad[0, 2, rows, 5] = sign * math.inf
+    got = {"fwd": mab.fwd(bad, k, v, sk, mab.Mask(kind=mab.ATTN_MASK_CAUSAL), SCALE)}
+    # the same keys in pages of 16
+    n = -(-keys // 16)
+    pages = torch.zeros(2, n, 2, 16, 128, dtype=F16, device="cuda")
+    for x, to in zip((k, v), pages):
+        flat = torch.zeros(2, 16 * n, 128, dtype=F16, device="cuda")
+        flat[:, :keys] = x[0]
+        to.copy_(flat.view(2, n, 16, 128).transpose(0, 1))
+    mask = mab.Mask(kind=mab.ATTN_MASK_CAUSAL, cu_seqlens_q=_i32([0, keys]), seqlen_k=_i32([keys]),
+                    total_q=keys, max_seqlen_q=keys, max_seqlen_k=keys)
+    o, lse = mab.paged_fwd(bad[0].transpose(0, 1).contiguous(), mab.PagedCache(*pages),
+                           _i32([list(range(n))]), sk, mask, SCALE)
+    got["paged_fwd"] = (o.transpose(0, 1)[None], lse)
+    torch.cuda.synchronize()
+    for name, (o, lse) in got.items():
+        o, lse = o[0, 2].float(), lse.reshape(4, keys)[2]
+        if sign > 0:
+            assert bool(o[rows].isnan().all()) and bool(lse[rows].isnan().all()), name
+        else:
+            assert bool((o[rows] == 0).all()), name
+            # the sink through a change of base and back: two products and their
+            # constants, each off by 2^-24
+            at = torch.full_like(lse[rows], 1.0 if sink else math.inf)
+            assert torch.allclose(lse[rows], at, rtol=2.0 ** -22, atol=0), name
+        rest = [i for i in range(keys) if i not in rows]
+        assert bool(torch.isfinite(o[rest]).all()) and bool(torch.isfinite(lse[rest]).all()), name
+        if name == "fwd":
+            assert torch.equal(o[rest], want[0, 2].float()[rest])
+            assert torch.equal(lse[rest], want_lse.reshape(4, keys)[2][rest])
