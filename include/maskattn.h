@@ -245,9 +245,10 @@ typedef struct {
  *
  * A request is refused, and keeps its pages and its cached length, when
  * cached + fresh exceeds max_pages * page_size, when its tokens end past
- * max_tokens, or when it needs pages and those that the requests up to and
- * with it need (but for those refused by the first two rules) exceed the free
- * ones: its slots are -1 and its rows of the step's attention mean nothing.
+ * max_tokens (a request without new tokens: when those before it do), or when
+ * it needs pages and those that the requests up to and with it need (but for
+ * those refused by the first two rules) exceed the free ones: its slots are -1
+ * and its rows of the step's attention mean nothing.
  * Entries of the table past a request's pages are left as they were.
  * seqlen_k may be `cached`, free_count_out may be `free_count`; with outputs
  * of their own the call may be repeated and does the same again.  Negative
@@ -294,7 +295,8 @@ attn_status_t attn_paged_workspace_size(const attn_shape_t* shape, size_t* bytes
  * of its pages, and of n new tokens over L keys token i stands at position
  * x = L - n + i (the masks' i): the new tokens end where the keys end.  lse is
  * float32 [Hq, total_q], or NULL when it is not wanted.  A row that sees no
- * key (L = 0, or x < 0) gets O = 0 and LSE = the sink, or +inf without one.
+ * key (L = 0, or x < 0 unless the kind is NONE) gets O = 0 and LSE = the sink,
+ * or +inf without one.
  *
  * mask: kind NONE, CAUSAL, SLIDING or SLIDING_FIRST (Sq and Skv need not be
  * equal); cu_seqlens_q, seqlen_k and total_q are set, seqlen_q and
