@@ -338,7 +338,10 @@ def bwd(q, k, v, o, dO, lse, sink, mask: Mask, scale: float, ws: Optional[torch.
 
 
 def device_status(ws: torch.Tensor, stream=None) -> int:
-    return attn_get_device_status(_ptr(ws), _stream(stream))
+    """Status of the last call that used `ws`, after what its device's current
+    stream, or `stream`, still has to do."""
+    with _one_device(ws):
+        return attn_get_device_status(_ptr(ws), _stream(stream))
 
 
 # ------------------------------------------------------------- paged cache
