@@ -198,6 +198,10 @@ class Mask:
     def packed(self) -> bool:
         return self.cu_seqlens_q is not None
 
+    def tensors(self):
+        return (self.block_mask, self.seqlen_q, self.seqlen_k, self.cu_seqlens_q,
+                self.cu_seqlens_k)
+
     def desc(self) -> attn_mask_desc_t:
         def ptr(t, name):
             if t is None:
@@ -294,6 +298,8 @@ def fwd(q, k, v, sink, mask: Mask, scale: float, ws: Optional[torch.Tensor] = No
     """Forward; returns (o, lse)."""
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _check(t, n)
+    if sink is not None:
+        _int_tensor(sink, "sink", q.shape[1], torch.float32)
     shape = shape_of(q, k, mask=mask)
     lse_shape = (q.shape[1], q.shape[0]) if mask.packed else q.shape[:3]   # [Hq, T] when packed
     desc = mask.desc()
@@ -302,8 +308,9 @@ def fwd(q, k, v, sink, mask: Mask, scale: float, ws: Optional[torch.Tensor] = No
         lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
         if ws is None:
             ws = workspace(shape, desc, q.device)
-    r = attn_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(sink), desc, scale, _ptr(o),
-                 _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
+    with _one_device(q, k, v, sink, ws, *mask.tensors()):
+        r = attn_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(sink), desc, scale, _ptr(o),
+                     _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
     if r != ATTN_OK:
         raise AttnError(r, "attn_fwd")
     return o, lse
@@ -317,6 +324,8 @@ def bwd(q, k, v, o, dO, lse, sink, mask: Mask, scale: float, ws: Optional[torch.
     reduction kernel (ATTN_FLAG_SINGLE_PASS) instead of the dq kernel."""
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (dO, "dO"), (lse, "lse")):
         _check(t, n)
+    if sink is not None:
+        _int_tensor(sink, "sink", q.shape[1], torch.float32)
     flags = (ATTN_FLAG_COMPENSATED if compensated else 0) | \
         (ATTN_FLAG_SINGLE_PASS if single_pass else 0)
     shape = shape_of(q, k, flags, mask=mask)
@@ -329,9 +338,10 @@ def bwd(q, k, v, o, dO, lse, sink, mask: Mask, scale: float, ws: Optional[torch.
             dq, dk, dv, dsink = out
         if ws is None:
             ws = workspace(shape, desc, q.device)
-    r = attn_bwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(sink),
-                 desc, scale, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dsink), _ptr(ws),
-                 ws.numel(), _stream(stream))
+    with _one_device(q, k, v, o, dO, lse, sink, dq, dk, dv, dsink, ws, *mask.tensors()):
+        r = attn_bwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(sink),
+                     desc, scale, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dsink), _ptr(ws),
+                     ws.numel(), _stream(stream))
     if r != ATTN_OK:
         raise AttnError(r, "attn_bwd")
     return dq, dk, dv, dsink
