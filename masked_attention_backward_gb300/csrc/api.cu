@@ -138,8 +138,9 @@ Dims dims_of(const attn_shape_t* sh, const attn_mask_desc_t* mk) {
   Dims d;
   d.Sq_pad = (sh->Sq + PREP_ROWS - 1) / PREP_ROWS * PREP_ROWS;
   const bool blk = mk->kind == ATTN_MASK_BLOCK;
-  d.nqb = blk ? (sh->Sq + mk->bx - 1) / mk->bx : 0;
-  d.nkb = blk ? (sh->Skv + mk->by - 1) / mk->by : 0;
+  // (a block may be longer than the sequence, up to the largest int)
+  d.nqb = blk ? (int)((sh->Sq + (long long)mk->bx - 1) / mk->bx) : 0;
+  d.nkb = blk ? (int)((sh->Skv + (long long)mk->by - 1) / mk->by) : 0;
   d.nQT_k = (sh->Sq + KV_SUB - 1) / KV_SUB;
   d.nKT_k = (sh->Skv + KV_TILE - 1) / KV_TILE;
   d.nQT_q = (sh->Sq + Q_TILE - 1) / Q_TILE;
