@@ -276,7 +276,9 @@ _nothing = contextlib.nullcontext()
 
 def _alloc_on(stream):
     """Tensors that a call makes belong to the stream that it runs on: the
-    allocator reuses a tensor's memory in the order of its own stream."""
+    allocator reuses a tensor's memory in the order of its own stream.  A caller
+    that uses them on another one calls their record_stream(other) before it
+    drops them."""
     return _nothing if stream is None else torch.cuda.stream(stream)
 
 
@@ -295,7 +297,9 @@ def _check(t: torch.Tensor, name: str):
 
 def fwd(q, k, v, sink, mask: Mask, scale: float, ws: Optional[torch.Tensor] = None,
         stream=None):
-    """Forward; returns (o, lse)."""
+    """Forward; returns (o, lse), which belong to `stream` where one is given:
+    before they are dropped, record_stream tells of every other stream that
+    uses them."""
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _check(t, n)
     if sink is not None:
@@ -321,7 +325,9 @@ def bwd(q, k, v, o, dO, lse, sink, mask: Mask, scale: float, ws: Optional[torch.
     """Backward; returns (dq, dk, dv, dsink) (dsink is None without a sink).
     compensated: P and dS enter the contractions as high part + remainder.
     single_pass: dq from partials of the key-stationary kernel, summed by a
-    reduction kernel (ATTN_FLAG_SINGLE_PASS) instead of the dq kernel."""
+    reduction kernel (ATTN_FLAG_SINGLE_PASS) instead of the dq kernel.
+    Gradients that are not given in `out` belong to `stream`, as fwd's results
+    do."""
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (dO, "dO"), (lse, "lse")):
         _check(t, n)
     if sink is not None:
@@ -440,7 +446,8 @@ def paged_plan(cached, fresh, free_pages, free_count, block_table, page_size: in
     and fresh (int32 [B]); free_pages (int32, one entry per page of the cache)
     and block_table (int32 [B, max_pages]) are updated in place.  out: buffers
     of an earlier plan to write (its seqlen_k may be `cached` and its
-    free_count `free_count`)."""
+    free_count `free_count`); a plan made without it belongs to `stream`, as
+    fwd's results do."""
     B = cached.numel()
     for t, n, m in ((cached, "cached", B), (fresh, "fresh", B),
                     (free_pages, "free_pages", free_pages.numel()),
@@ -518,7 +525,8 @@ def paged_workspace(q: torch.Tensor, cache: PagedCache, mask: Mask,
 def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
               ws: Optional[torch.Tensor] = None, out=None, stream=None):
     """Attention of the packed new tokens q [total_q, Hq, 128] over the cache;
-    returns (o, lse).  out: (o, lse) to write, of which lse may be None."""
+    returns (o, lse).  out: (o, lse) to write, of which lse may be None;
+    without it they belong to `stream`, as fwd's results do."""
     cu, lens = mask.cu_seqlens_q, mask.seqlen_k
     if cu is None or lens is None or cu.numel() != lens.numel() + 1:
         raise ValueError("the mask needs cu_seqlens_q [B + 1] and seqlen_k [B]")
