@@ -17,7 +17,7 @@
 // one such tile takes as long as half the grid), and over the others, which
 // have the plain window's walks.  The first grid's pieces leave fp32 sums for
 // k_dkdv_first_join, which runs beside the second.  S 8192, 32/8 heads, window
-// 1024, 4 first keys, bf16: the backward 415 us, 365 for the window alone.
+// 1024, 4 first keys, bf16: the backward 414 us, 382 for the window alone.
 //
 // Sources: tilelang-ascend PR #1 "Add GQA Sink Backward BHSD", commit notes
 // (five contractions + softmax + dS per step; GQA group of query heads per

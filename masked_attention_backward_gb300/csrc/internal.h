@@ -173,7 +173,12 @@ __device__ __forceinline__ int rows_to_store_k(const AttnParams& p, int b, int r
 
 // MK_FIRST: key tiles that hold first keys, and the pieces that each one's
 // walk over every later query is split into at the full lengths: as many as
-// one wave of CTAs holds, none shorter than KV_FIRST_STEPS.
+// one wave of CTAs holds, none shorter than KV_FIRST_STEPS.  Small calls gain
+// most, since nothing runs beside an unsplit walk there; whole backward at 16, 32
+// and 64 steps and unsplit: 2 x 1000, 8/2 heads, window 128, 5 first keys (walks of
+// 64 steps) 28.4, 39.1, 62.7 and 62.6 us; 8192, 32/8 heads, window 1024, 4 first
+// keys (512 steps) 415, 411, 430 and 490; 4096, 8/8 heads, window 512, 4 first keys
+// (64 steps) 65.7, 76.9, 67.0 and 67.2.
 inline int kv_first_tiles(int first) { return (first + KV_TILE - 1) / KV_TILE; }
 inline int kv_first_pieces(int B, int Hq, int Hkv, int Sq, int first) {
   const long long units = (long long)kv_first_tiles(first) * B * Hkv;

@@ -17,7 +17,8 @@ constexpr int PAGED_WARP_FLOATS = PAGED_ML + 32 * 2;
 // chunk of 300 over nothing 14.2, 15.0, 14.4; at 2 the chunk of 8192 took 20 %
 // more), the least part that a CTA gets (one token at 8000 keys took 20.6 us at 8,
 // 22.7 at 11, 26.8 at 20), and the steps below which a unit is not cut (at 5 and 8
-// a chunk of 300 took 16.4 and 14.4 us, 200 single tokens at 300 keys 78 and 70).
+// a chunk of 300 took 16.4 and 14.4 us, 200 single tokens at 300 keys 78 and 70 when
+// this was chosen; 13.6 and 67 now).
 constexpr int PAGED_UNIT_COST = 7;
 constexpr int PAGED_MIN_COST = 8;
 constexpr int PAGED_MIN_STEPS = 8;

@@ -41,10 +41,10 @@
 // the other unseen rows in shared memory before it multiplies.
 //
 // Measured (one GB300, bf16 unless stated): 64 single tokens at 9000 keys, 64/8
-// heads, 0.348 ms, 6.78 TB/s (16-token pages, [page, row, head], 6.5); 2 at
-// 100000 keys, 32/4 heads, 74 us, 5.5 TB/s; 200 at 300 keys, 32/8 heads, 70 us,
+// heads, 0.345 ms, 6.84 TB/s (16-token pages, [page, row, head], 6.6); 2 at
+// 100000 keys, 32/4 heads, 73 us, 5.6 TB/s; 200 at 300 keys, 32/8 heads, 67 us,
 // latency bound (a unit's start and end, about 5000 cycles, beside 5 steps);
-// chunks of 2048 over 9000 keys, 32/8 heads, 0.434 ms, 1230 TFLOP/s, bound by
+// chunks of 2048 over 9000 keys, 32/8 heads, 0.44 ms, 1215 TFLOP/s, bound by
 // the latency of S, softmax and P V over three buffers (tensor pipe 56 %
 // active); one token at 1000 keys (fp16) 16 us, of which the line takes 2.5
 // and the join 3.  Kept out, measured: one lane per box in place of an elected
@@ -1029,7 +1029,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
 // piece is CTA c's last one, a warp per row, 4 columns a lane.  Latency bound:
 // one lane per piece for the weights, and the first two pieces' rows on their
 // way before those are known (with 16, whose registers left two blocks on an SM,
-// 15 single tokens and a chunk of 500 took 43.1 us, 37.9 now).  (Joined by the
+// 15 single tokens and a chunk of 500 took 43.1 us, 37.9 with two).  (Joined by the
 // last warp to finish inside the kernel above, 19 pieces took 5 to 15 us and the
 // code slowed its loop by 5 %; with four rows a warp one after another they took
 // 15 us more than now.)

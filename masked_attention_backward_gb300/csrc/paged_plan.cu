@@ -21,8 +21,8 @@
 // CTA may be writing.  Page numbers are moved by all threads too, whichever
 // request they belong to, by the same search: a warp per request took 35 us for
 // one of 100000 tokens that ended among 64 decodes, now 7.5.  Measured (one GB300, ten
-// calls replayed in a row): 8 decodes 4.4 us, 512 requests with 16384 tokens
-// 10.9 (13.7 with a warp per request and one token at a time).
+// calls replayed in a row): 8 decodes 4.7 us, 512 requests with 16384 tokens
+// 10.7 (13.7 with a warp per request and one token at a time).
 #include <limits.h>
 
 #include <type_traits>

@@ -4,7 +4,7 @@
 // tensor).  A half-warp moves one 256-byte row of K and the same row of V, 16
 // bytes a thread, so that every request of a warp covers whole 128-byte lines
 // on both sides whatever the layout; the slot is the same word for all 16.
-// Measured (one GB300): 16384 tokens of 8 heads 21.8 us, 6.15 TB/s; 32 tokens
+// Measured (one GB300): 16384 tokens of 8 heads 21.7 us, 6.2 TB/s; 32 tokens
 // 1.6 us in a row of calls, the launch.
 #include "paged.h"
 
