@@ -325,6 +325,47 @@ attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* page
                              const attn_mask_desc_t* mask, float scale, void* o, float* lse,
                              void* ws, size_t ws_bytes, void* stream);
 
+/* ---- rotary positions ----
+ *
+ * Pair i of a row at position x is turned by the angle x * w_i and multiplied by
+ * `factor`: (x1, x2) -> factor (x1 cos - x2 sin, x2 cos + x1 sin).  The pairs are
+ * elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when `interleaved` is not 0;
+ * elements from rotary_dim on stay as they are.  rotary_dim is a multiple of 16 up
+ * to 128.  `turns` is a device array [rotary_dim / 2] of w_i / (2 pi) in units of
+ * 2^-64 (modulo 2^64), so that the angle is exact at every position. */
+typedef struct {
+  int rotary_dim;
+  int interleaved;
+  float factor;
+  const unsigned long long* turns;
+} attn_rope_desc_t;
+
+/* A tensor that is turned: element (b, head, token, d) of x is at b * x_batch +
+ * head * x_head + token * x_token + d, and so for y, so that [T, heads, 128] rows
+ * (possibly slices of a wider tensor) and [B, heads, S, 128] are both described.
+ * Strides are in elements, multiples of 8, those of y at least 128; the stride of a
+ * dimension of one is not read.  y may be x with the same strides; otherwise the two
+ * must not overlap, nor may rows of y. */
+typedef struct {
+  const void* x;
+  void* y;
+  int heads;
+  long long x_batch, x_head, x_token;
+  long long y_batch, y_head, y_token;
+} attn_rope_tensor_t;
+
+/* Turns q, and k unless it is NULL, both of `dtype`: B sequences of S tokens.
+ * position: device int32, token t of sequence b stands at position[b *
+ * position_stride + t] (position_stride 0: one row for all); NULL: at t.  Rows at a
+ * negative position are no tokens and are left as y had them.  inverse not 0: the
+ * angles negated, which turns the gradients of y into those of x.  Results are
+ * rounded once.  ATTN_ERR_UNSUPPORTED for an even rotary_dim that is no multiple of
+ * 16. */
+attn_status_t attn_rope(const attn_rope_desc_t* rope, int dtype, int B, int S,
+                        const attn_rope_tensor_t* q, const attn_rope_tensor_t* k,
+                        const int* position, long long position_stride, int inverse,
+                        void* stream);
+
 /* Synchronizes `stream`, then reads the status word that the last call which
  * used `ws` left in the workspace: ATTN_OK, or ATTN_ERR_TIMEOUT when a device
  * wait ran out, or ATTN_ERR_INVALID_ARG when attn_paged_fwd met a page

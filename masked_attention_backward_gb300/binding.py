@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -26,7 +27,7 @@ ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_SLIDING, ATTN_MASK_BLOCK, \
 EXPORTS = ("attn_workspace_size", "attn_fwd", "attn_bwd", "attn_bwd_noalloc",
            "attn_get_device_status", "attn_noalloc_get_device_status", "attn_profile_enable",
            "attn_profile_read", "attn_status_string", "attn_paged_plan", "attn_paged_store",
-           "attn_paged_workspace_size", "attn_paged_fwd")
+           "attn_paged_workspace_size", "attn_paged_fwd", "attn_rope")
 
 
 class attn_shape_t(ctypes.Structure):
@@ -52,6 +53,17 @@ class attn_pages_t(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("page_stride", ctypes.c_longlong),
                 ("head_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong)]
+
+
+class attn_rope_desc_t(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("factor", ctypes.c_float), ("turns", ctypes.c_void_p)]
+
+
+class attn_rope_tensor_t(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int)] + \
+               [(n, ctypes.c_longlong) for n in ("x_batch", "x_head", "x_token", "y_batch",
+                                                 "y_head", "y_token")]
 
 
 class attn_plan_t(ctypes.Structure):
@@ -112,6 +124,10 @@ def load(build: bool = True) -> ctypes.CDLL:
             lib.attn_paged_fwd.argtypes = [ps, pp, vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, vp,
                                            pm, ctypes.c_float, vp, vp, vp, sz, vp]
             lib.attn_paged_fwd.restype = ctypes.c_int
+            pr = ctypes.POINTER(attn_rope_tensor_t)
+            lib.attn_rope.argtypes = [ctypes.POINTER(attn_rope_desc_t), ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_int, pr, pr, vp, ll, ctypes.c_int, vp]
+            lib.attn_rope.restype = ctypes.c_int
             lib.attn_status_string.argtypes = [ctypes.c_int]
             lib.attn_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -218,12 +234,16 @@ class Mask:
                                 self.total_k, self.first)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float16:
+def _code_of(dtype: torch.dtype) -> int:
+    if dtype == torch.float16:
         return ATTN_F16
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return ATTN_BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _code_of(t.dtype)
 
 
 def shape_of(q: torch.Tensor, k: torch.Tensor, flags: int = 0,
@@ -360,6 +380,148 @@ def device_status(ws: torch.Tensor, stream=None) -> int:
         return attn_get_device_status(_ptr(ws), _stream(stream))
 
 
+# ------------------------------------------------------------- rotary positions
+
+def attn_rope(rope: attn_rope_desc_t, dtype, B, S, q, k, position, position_stride, inverse,
+              stream) -> int:
+    return load().attn_rope(ctypes.byref(rope), dtype, B, S, ctypes.byref(q),
+                            None if k is None else ctypes.byref(k), position, position_stride,
+                            inverse, stream)
+
+
+@dataclass
+class RopeScaling:
+    """Rotary frequencies for contexts `factor` times as long as a model was
+    trained on.  kind:
+      "linear"  every frequency divided by factor;
+      "raised"  the base multiplied by factor^(R / (R - 2)), which divides the
+                lowest frequency by factor and keeps the highest (R: rotary_dim);
+      "parts"   pairs that turn more than `high` times in original_length
+                positions keep their frequency, those that turn less than `low`
+                times are divided by factor, the others in between in proportion;
+                cos and sin are multiplied by `attention`, without one by
+                0.1 ln(factor) + 1."""
+    kind: str
+    factor: float
+    original_length: int = 0
+    low: float = 1.0
+    high: float = 32.0
+    attention: Optional[float] = None
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0,
+                     scaling: Optional[RopeScaling] = None):
+    """([rotary_dim / 2] radians a position of each pair, what cos and sin are
+    multiplied by): base^(-2 i / rotary_dim), scaled."""
+    R = rotary_dim
+    if R < 2 or R % 2 or not base > 0:
+        raise ValueError("rotary_dim must be even and positive, base positive")
+    kind = None if scaling is None else scaling.kind
+    if kind not in (None, "linear", "raised", "parts"):
+        raise ValueError(f"unknown scaling {kind!r}")
+    if scaling is not None and not scaling.factor > 0:
+        raise ValueError("the scaling's factor must be positive")
+    if kind == "raised":
+        if R == 2:
+            raise ValueError('"raised" needs more than one pair')
+        base = base * scaling.factor ** (R / (R - 2))
+    w = [base ** (-2 * i / R) for i in range(R // 2)]
+    if kind == "linear":
+        w = [x / scaling.factor for x in w]
+    factor = 1.0 if kind is None or scaling.attention is None else scaling.attention
+    if kind == "parts":
+        if scaling.original_length < 1 or not scaling.high > scaling.low:
+            raise ValueError('"parts" needs original_length and high > low')
+        for i, x in enumerate(w):
+            turns = scaling.original_length * x / (2 * math.pi)
+            keep = min(1.0, max(0.0, (turns - scaling.low) / (scaling.high - scaling.low)))
+            w[i] = x * (keep + (1 - keep) / scaling.factor)
+        if scaling.attention is None:
+            factor = 0.1 * math.log(scaling.factor) + 1 if scaling.factor > 1 else 1.0
+    return w, factor
+
+
+class Rope:
+    """Rotary positions of heads of 128, kept by a program for its models' life:
+    the first rotary_dim elements (a multiple of 16) turn, in pairs (i, i +
+    rotary_dim / 2), or (2 i, 2 i + 1) if interleaved.  frequencies: radians a
+    position of each pair in place of those of base and scaling; factor: what cos
+    and sin are multiplied by then."""
+
+    def __init__(self, rotary_dim: int = 128, base: float = 10000.0, interleaved: bool = False,
+                 scaling: Optional[RopeScaling] = None, frequencies=None, factor: float = 1.0,
+                 device="cuda"):
+        if frequencies is None:
+            frequencies, factor = rope_frequencies(rotary_dim, base, scaling)
+        elif scaling is not None:
+            raise ValueError("frequencies come scaled")
+        w = [float(x) for x in frequencies]
+        if len(w) != rotary_dim // 2 or not all(math.isfinite(x) for x in w):
+            raise ValueError("frequencies must be rotary_dim / 2 finite numbers")
+        # 2^64 turns are one: what a negative or a large frequency comes to
+        turns = [round(x / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for x in w]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns],
+                                  dtype=torch.int64, device=device)
+        self.rotary_dim, self.interleaved, self.factor = rotary_dim, bool(interleaved), factor
+        self.desc = attn_rope_desc_t(rotary_dim, int(self.interleaved), factor,
+                                     self.turns.data_ptr())
+
+
+def _rope_tensor(x: torch.Tensor, y: torch.Tensor) -> attn_rope_tensor_t:
+    xs, ys = x.stride(), y.stride()
+    if x.dim() == 3:   # rows [T, heads, 128]
+        return attn_rope_tensor_t(x.data_ptr(), y.data_ptr(), x.shape[1], 0, xs[1], xs[0], 0,
+                                  ys[1], ys[0])
+    return attn_rope_tensor_t(x.data_ptr(), y.data_ptr(), x.shape[1], *xs[:3], *ys[:3])
+
+
+def rope(rp: Rope, q, k=None, position=None, out=None, stream=None, inverse: bool = False):
+    """Queries and keys turned by their positions, packed rows [T, heads, 128] or
+    [B, heads, S, 128], possibly slices of wider tensors; returns (q, k).  k may
+    be None.  position: int32 [T], or [B, S] or [S]; None: counted from 0 (in
+    every sequence).  Rows at a negative position are not written.  out: (q, k) to
+    write, which may be the inputs themselves; without it they are contiguous and
+    belong to `stream`, as fwd's results do."""
+    if q.dim() not in (3, 4) or q.shape[-1] != 128 or q.stride(-1) != 1:
+        raise ValueError("q must be [T, heads, 128] or [B, heads, S, 128], its last stride 1")
+    at = 0 if q.dim() == 3 else 2
+    S, B = q.shape[at], 1 if q.dim() == 3 else q.shape[0]
+    code = _dtype_code(q)
+    if k is not None and (k.dim() != q.dim() or k.shape[at] != S or k.shape[-1] != 128 or
+                          k.stride(-1) != 1 or k.dtype != q.dtype or
+                          (q.dim() == 4 and k.shape[0] != B)):
+        raise ValueError("k must have q's type, layout and tokens")
+    p_stride = 0
+    if position is not None:
+        if position.dtype != torch.int32 or not position.is_contiguous() or \
+                tuple(position.shape) not in ([(S,)] if q.dim() == 3 else [(S,), (B, S)]):
+            raise ValueError("position must be a contiguous int32 tensor, one a token")
+        p_stride = S if position.dim() == 2 else 0
+    if out is None:
+        with _alloc_on(stream):
+            y = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            z = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    else:
+        y, z = out
+        for o, x, n in ((y, q, "q"), (z, k, "k")):
+            if (o is None) != (x is None) or (o is not None and (
+                    o.shape != x.shape or o.dtype != x.dtype or o.stride(-1) != 1)):
+                raise ValueError(f"out's {n} must be like {n}, its last stride 1")
+    with _one_device(q, k, position, y, z, rp.turns):
+        r = attn_rope(rp.desc, code, B, S, _rope_tensor(q, y),
+                      None if k is None else _rope_tensor(k, z), _ptr(position), p_stride,
+                      int(inverse), _stream(stream))
+    if r != ATTN_OK:
+        raise AttnError(r, "attn_rope")
+    return y, z
+
+
+def rope_bwd(rp: Rope, dq, dk=None, position=None, out=None, stream=None):
+    """The gradients of rope's inputs from those of its outputs, in rope's forms:
+    turned back."""
+    return rope(rp, dq, dk, position, out, stream, inverse=True)
+
+
 # ------------------------------------------------------------- paged cache
 
 def attn_paged_plan(plan: attn_plan_t, stream) -> int:
@@ -420,6 +582,7 @@ class PagedCache:
             raise ValueError("k_pages and v_pages must have the same strides, 1 for the last")
         self.k_pages, self.v_pages, self.layout = k_pages, v_pages, layout
         self.num_pages, self.Hkv, self.page_size = shape[0], shape[hd], shape[td]
+        self.dtype = k_pages.dtype
         self.desc = attn_pages_t(self.num_pages, self.page_size, self.Hkv, _dtype_code(k_pages),
                                  ks[0], ks[hd], ks[td])
 
@@ -485,7 +648,7 @@ def paged_store(cache: PagedCache, k, v, slot_map, stream=None) -> None:
     their slots of the cache (int64 [T]; negative: skipped)."""
     T = slot_map.numel()
     for t, n in ((k, "k"), (v, "v")):
-        if t.dtype != cache.k_pages.dtype or tuple(t.shape) != (T, cache.Hkv, 128) or \
+        if t.dtype != cache.dtype or tuple(t.shape) != (T, cache.Hkv, 128) or \
                 t.stride(2) != 1 or (cache.Hkv > 1 and t.stride(1) != 128):
             raise ValueError(f"{n} must be [T, Hkv, 128] of the cache's type, its heads 128 apart")
     _int_tensor(slot_map, "slot_map", T, torch.int64)
