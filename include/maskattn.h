@@ -366,6 +366,64 @@ attn_status_t attn_rope(const attn_rope_desc_t* rope, int dtype, int B, int S,
                         const int* position, long long position_stride, int inverse,
                         void* stream);
 
+/* ---- paged key/value cache held in 8 bits ----
+ *
+ * Pages as in attn_pages_t, of one-byte codes, and a scale for each block of
+ * `block` (1, 16, 32 or 64, a divisor of page_size) tokens of each kv head: a byte
+ * s that stands for 2^(s - 127), or for NaN when it is 255.  A value is code * scale,
+ * the code an e4m3 number or an int8 from -127 to 127; `dtype` is the 16-bit type of
+ * the values, in which code * scale is exact for every scale that attn_paged8_store
+ * writes.  (Scales of other origin: for ATTN_F16 exponents outside [-24, 15] count as
+ * the nearest of these, for ATTN_BF16 byte 0 as 1.  What the e4m3 codes 0x7f and 0xff
+ * and the int8 code -128 stand for is not defined.)
+ *
+ * Element (page, kv head, row, d) of the K or the V pages is at page * page_stride +
+ * head * head_stride + row * token_stride + d, in bytes, strides multiples of 16 and
+ * at least 128.  Its scale is byte page * scale_page_stride + head *
+ * scale_head_stride + row / block of the K or V scales; these strides are at least
+ * page_size / block, for block = 1 multiples of 16 (and the scales 16-byte aligned).
+ * Other limits as for attn_pages_t. */
+typedef enum { ATTN_E4M3 = 0, ATTN_I8 = 1 } attn_code_t;
+typedef struct {
+  int num_pages, page_size, Hkv;
+  int dtype; /* attn_dtype_t: the values' type */
+  int code;  /* attn_code_t */
+  int block;
+  long long page_stride, head_stride, token_stride;
+  long long scale_page_stride, scale_head_stride;
+} attn_pages8_t;
+
+/* attn_paged_store into an 8-bit cache.  A block's scale is 2^e with the least e for
+ * which its largest magnitude is at most 448 * 2^e (e4m3) or 127 * 2^e (int8), but at
+ * least -15 (e4m3) or -24 (int8) for ATTN_F16 and -110 for ATTN_BF16; codes are
+ * value / scale rounded to nearest even, held back to the largest code whose value is
+ * finite in `dtype`.
+ *
+ * The rows of one call that go to one block must be consecutive, with consecutive
+ * slots, as attn_paged_plan gives them (of other orders the block's content is
+ * undefined, nothing else).  Where they begin at the block's row 0 the block begins
+ * anew, whatever it held.  Where they begin at a row r > 0 its rows before r stay:
+ * the block keeps the larger of its scale and the one that the new rows need, and if
+ * that is the new one the earlier rows' codes are rounded in units of it.  Rows of
+ * the block past the new ones mean nothing afterwards.  A value that is not finite
+ * makes the scale 255: the block reads as NaN until it begins anew. */
+attn_status_t attn_paged8_store(const attn_pages8_t* pages, int T, const void* k, const void* v,
+                                long long k_stride, long long v_stride, const long long* slot_map,
+                                void* k_pages, void* v_pages, uint8_t* k_scales,
+                                uint8_t* v_scales, void* stream);
+
+/* Rows of an 8-bit cache back to 16 bits: row t of k and v ([total, Hkv, 128] of the
+ * pages' dtype) is position start[b] + t - cu_seqlens[b] of the request b whose rows
+ * [cu_seqlens[b], cu_seqlens[b + 1]) hold t (start NULL: all 0; negative ones count
+ * as 0).  cu_seqlens is int32 [B + 1], ascending; rows of no request are left as they
+ * were.  block_table is int32 [B, max_pages], rows table_stride apart; a position
+ * past its pages, or in a page outside [0, num_pages), reads zeros.  B <= 65536. */
+attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, const int* start,
+                               const int* cu_seqlens, const int* block_table, int table_stride,
+                               int max_pages, const void* k_pages, const void* v_pages,
+                               const uint8_t* k_scales, const uint8_t* v_scales, void* k, void* v,
+                               void* stream);
+
 /* Synchronizes `stream`, then reads the status word that the last call which
  * used `ws` left in the workspace: ATTN_OK, or ATTN_ERR_TIMEOUT when a device
  * wait ran out, or ATTN_ERR_INVALID_ARG when attn_paged_fwd met a page

@@ -27,7 +27,8 @@ ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_SLIDING, ATTN_MASK_BLOCK, \
 EXPORTS = ("attn_workspace_size", "attn_fwd", "attn_bwd", "attn_bwd_noalloc",
            "attn_get_device_status", "attn_noalloc_get_device_status", "attn_profile_enable",
            "attn_profile_read", "attn_status_string", "attn_paged_plan", "attn_paged_store",
-           "attn_paged_workspace_size", "attn_paged_fwd", "attn_rope")
+           "attn_paged_workspace_size", "attn_paged_fwd", "attn_rope", "attn_paged8_store",
+           "attn_paged8_load")
 
 
 class attn_shape_t(ctypes.Structure):
@@ -64,6 +65,16 @@ class attn_rope_tensor_t(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int)] + \
                [(n, ctypes.c_longlong) for n in ("x_batch", "x_head", "x_token", "y_batch",
                                                  "y_head", "y_token")]
+
+
+ATTN_E4M3, ATTN_I8 = 0, 1
+
+
+class attn_pages8_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("num_pages", "page_size", "Hkv", "dtype", "code",
+                                            "block")] + \
+               [(n, ctypes.c_longlong) for n in ("page_stride", "head_stride", "token_stride",
+                                                 "scale_page_stride", "scale_head_stride")]
 
 
 class attn_plan_t(ctypes.Structure):
@@ -124,10 +135,17 @@ def load(build: bool = True) -> ctypes.CDLL:
             lib.attn_paged_fwd.argtypes = [ps, pp, vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, vp,
                                            pm, ctypes.c_float, vp, vp, vp, sz, vp]
             lib.attn_paged_fwd.restype = ctypes.c_int
-            pr = ctypes.POINTER(attn_rope_tensor_t)
+            pr, p8 = ctypes.POINTER(attn_rope_tensor_t), ctypes.POINTER(attn_pages8_t)
             lib.attn_rope.argtypes = [ctypes.POINTER(attn_rope_desc_t), ctypes.c_int, ctypes.c_int,
                                       ctypes.c_int, pr, pr, vp, ll, ctypes.c_int, vp]
             lib.attn_rope.restype = ctypes.c_int
+            lib.attn_paged8_store.argtypes = [p8, ctypes.c_int, vp, vp, ll, ll, vp, vp, vp, vp, vp,
+                                              vp]
+            lib.attn_paged8_store.restype = ctypes.c_int
+            lib.attn_paged8_load.argtypes = [p8, ctypes.c_int, ctypes.c_int, vp, vp, vp,
+                                             ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp,
+                                             vp]
+            lib.attn_paged8_load.restype = ctypes.c_int
             lib.attn_status_string.argtypes = [ctypes.c_int]
             lib.attn_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -547,6 +565,19 @@ def attn_paged_fwd(shape, pages, q, k_pages, v_pages, block_table, table_stride,
                                  ctypes.c_float(scale), o, lse, ws, ws_bytes, stream)
 
 
+def attn_paged8_store(pages: attn_pages8_t, T, k, v, k_stride, v_stride, slot_map, k_pages,
+                      v_pages, k_scales, v_scales, stream) -> int:
+    return load().attn_paged8_store(ctypes.byref(pages), T, k, v, k_stride, v_stride, slot_map,
+                                    k_pages, v_pages, k_scales, v_scales, stream)
+
+
+def attn_paged8_load(pages: attn_pages8_t, B, total, start, cu_seqlens, block_table, table_stride,
+                     max_pages, k_pages, v_pages, k_scales, v_scales, k, v, stream) -> int:
+    return load().attn_paged8_load(ctypes.byref(pages), B, total, start, cu_seqlens, block_table,
+                                   table_stride, max_pages, k_pages, v_pages, k_scales, v_scales,
+                                   k, v, stream)
+
+
 def _one_device(*tensors):
     """All tensors on one CUDA device: a guard that makes it current."""
     devs = {t.get_device() for t in tensors if t is not None}
@@ -585,6 +616,67 @@ class PagedCache:
         self.dtype = k_pages.dtype
         self.desc = attn_pages_t(self.num_pages, self.page_size, self.Hkv, _dtype_code(k_pages),
                                  ks[0], ks[hd], ks[td])
+
+
+class PagedCache8:
+    """The pages of a key/value cache held in 8 bits: k_pages and v_pages as in
+    PagedCache but of torch.float8_e4m3fn or torch.int8, and k_scales and
+    v_scales, uint8 [pages, Hkv, page_size // block], of which each byte s stands
+    for the factor 2^(s - 127) of `block` tokens of a head (1, 16, 32 or 64; 255:
+    NaN).  dtype: the 16-bit type of the values, torch.bfloat16 or float16."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
+                 v_scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                 layout: str = "HND"):
+        if layout not in ("HND", "NHD"):
+            raise ValueError(f"unknown layout {layout!r}")
+        shape = k_pages.shape
+        if len(shape) != 4 or shape[3] != 128 or v_pages.shape != shape:
+            raise ValueError("k_pages and v_pages must be [pages, ., ., 128] of one shape")
+        code = {torch.float8_e4m3fn: ATTN_E4M3, torch.int8: ATTN_I8}.get(k_pages.dtype)
+        if code is None:
+            raise TypeError(f"unsupported type of codes {k_pages.dtype}")
+        if v_pages.dtype != k_pages.dtype or \
+                len({t.device for t in (k_pages, v_pages, k_scales, v_scales)}) != 1:
+            raise ValueError("k_pages and v_pages must have one type, all tensors one device")
+        hd, td = (1, 2) if layout == "HND" else (2, 1)
+        P, Hkv, ps = shape[0], shape[hd], shape[td]
+        per = k_scales.shape[2] if k_scales.dim() == 3 else 0
+        for t in (k_scales, v_scales):
+            if t.dtype != torch.uint8 or per < 1 or ps % per or tuple(t.shape) != (P, Hkv, per):
+                raise ValueError("the scales must be uint8 [pages, Hkv, page_size // block]")
+        # a dimension of one element may have any stride
+        ks, vs = ([128 if n == 1 else m for n, m in zip(shape, t.stride())]
+                  for t in (k_pages, v_pages))
+        if ks != vs or ks[3] != 1:
+            raise ValueError("k_pages and v_pages must have the same strides, 1 for the last")
+        kss, vss = ([per if n == 1 else m for n, m in zip((P, Hkv), t.stride())] +
+                    [1 if per == 1 else t.stride(2)] for t in (k_scales, v_scales))
+        if kss != vss or kss[2] != 1:
+            raise ValueError("k_scales and v_scales must have the same strides, 1 for the last")
+        self.k_pages, self.v_pages, self.layout, self.dtype = k_pages, v_pages, layout, dtype
+        self.k_scales, self.v_scales = k_scales, v_scales
+        self.num_pages, self.Hkv, self.page_size, self.block = P, Hkv, ps, ps // per
+        self.desc = attn_pages8_t(P, ps, Hkv, _code_of(dtype), code, self.block, ks[0], ks[hd],
+                                  ks[td], kss[0], kss[1])
+
+    @staticmethod
+    def empty(num_pages: int, Hkv: int, page_size: int, block: int = 16,
+              codes: torch.dtype = torch.float8_e4m3fn, dtype: torch.dtype = torch.bfloat16,
+              layout: str = "HND", device="cuda") -> "PagedCache8":
+        """A cache of pages that hold nothing yet."""
+        shape = (num_pages, Hkv, page_size, 128) if layout == "HND" else \
+            (num_pages, page_size, Hkv, 128)
+        if block < 1 or page_size % block:
+            raise ValueError("block must divide page_size")
+        pages = [torch.empty(shape, dtype=codes, device=device) for _ in range(2)]
+        scales = [torch.empty(num_pages, Hkv, page_size // block, dtype=torch.uint8,
+                              device=device) for _ in range(2)]
+        return PagedCache8(*pages, *scales, dtype, layout)
+
+    def pointers(self):
+        return (self.k_pages.data_ptr(), self.v_pages.data_ptr(), self.k_scales.data_ptr(),
+                self.v_scales.data_ptr())
 
 
 @dataclass
@@ -643,9 +735,11 @@ def paged_plan(cached, fresh, free_pages, free_count, block_table, page_size: in
     return out
 
 
-def paged_store(cache: PagedCache, k, v, slot_map, stream=None) -> None:
+def paged_store(cache, k, v, slot_map, stream=None) -> None:
     """Rows of k and v ([T, Hkv, 128], possibly slices of a larger tensor) into
-    their slots of the cache (int64 [T]; negative: skipped)."""
+    their slots of the cache, a PagedCache or PagedCache8 (int64 [T]; negative:
+    skipped).  A PagedCache8 wants the rows of each block of tokens consecutive,
+    as a plan's slot_map has them."""
     T = slot_map.numel()
     for t, n in ((k, "k"), (v, "v")):
         if t.dtype != cache.dtype or tuple(t.shape) != (T, cache.Hkv, 128) or \
@@ -653,6 +747,14 @@ def paged_store(cache: PagedCache, k, v, slot_map, stream=None) -> None:
             raise ValueError(f"{n} must be [T, Hkv, 128] of the cache's type, its heads 128 apart")
     _int_tensor(slot_map, "slot_map", T, torch.int64)
     row = cache.Hkv * 128
+    if isinstance(cache, PagedCache8):
+        with _one_device(cache.k_pages, k, v, slot_map):
+            r = attn_paged8_store(cache.desc, T, k.data_ptr(), v.data_ptr(),
+                                  k.stride(0) if T > 1 else row, v.stride(0) if T > 1 else row,
+                                  slot_map.data_ptr(), *cache.pointers(), _stream(stream))
+        if r != ATTN_OK:
+            raise AttnError(r, "attn_paged8_store")
+        return
     with _one_device(cache.k_pages, k, v, slot_map):
         r = attn_paged_store(cache.desc, T, k.data_ptr(), v.data_ptr(),
                              k.stride(0) if T > 1 else row, v.stride(0) if T > 1 else row,
@@ -660,6 +762,43 @@ def paged_store(cache: PagedCache, k, v, slot_map, stream=None) -> None:
                              cache.v_pages.data_ptr(), _stream(stream))
     if r != ATTN_OK:
         raise AttnError(r, "attn_paged_store")
+
+
+def paged_load(cache: PagedCache8, block_table, cu_seqlens, total: int, start=None, out=None,
+               stream=None):
+    """Rows of an 8-bit cache back to 16 bits: (k, v) [total, Hkv, 128], of which
+    rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 are request b's positions from
+    start[b] on (int32 [B + 1] and [B]; start None: from 0).  Rows of no request
+    are not written.  out: (k, v) to write; without it they belong to `stream`, as
+    fwd's results do."""
+    if not isinstance(cache, PagedCache8):
+        raise TypeError("paged_load reads a PagedCache8")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_pages] with rows of stride 1")
+    B, cols = block_table.shape
+    _int_tensor(cu_seqlens, "cu_seqlens", B + 1)
+    if start is not None:
+        _int_tensor(start, "start", B)
+    if out is None:
+        with _alloc_on(stream):
+            k, v = (torch.empty(total, cache.Hkv, 128, dtype=cache.dtype,
+                                device=cache.k_pages.device) for _ in range(2))
+    else:
+        k, v = out
+        for t, n in ((k, "k"), (v, "v")):
+            if tuple(t.shape) != (total, cache.Hkv, 128) or t.dtype != cache.dtype or \
+                    not t.is_contiguous():
+                raise ValueError(f"{n} must be a contiguous [total, Hkv, 128] tensor of the "
+                                 "cache's type")
+    with _one_device(cache.k_pages, block_table, cu_seqlens, start, k, v):
+        r = attn_paged8_load(cache.desc, B, total, _ptr(start), cu_seqlens.data_ptr(),
+                             block_table.data_ptr(), block_table.stride(0) if B > 1 else cols,
+                             cols, *cache.pointers(), k.data_ptr(), v.data_ptr(),
+                             _stream(stream))
+    if r != ATTN_OK:
+        raise AttnError(r, "attn_paged8_load")
+    return k, v
 
 
 def paged_mask(kind: int, plan: PagedPlan, total_q: int, max_seqlen_q: int, max_seqlen_k: int,

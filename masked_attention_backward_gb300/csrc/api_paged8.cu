@@ -1,0 +1,96 @@
+// api_paged8.cu -- the C ABI of the 8-bit cache (declared in
+// include/maskattn.h): argument checks, then the launches, on the caller's
+// stream.  Nothing is allocated and nothing is read back.
+#include "paged8.h"
+
+using namespace mab;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+attn_status_t check_pages8(const attn_pages8_t* pg, Pages8* out) {
+  if (!pg || (pg->dtype != ATTN_F16 && pg->dtype != ATTN_BF16) ||
+      (pg->code != ATTN_E4M3 && pg->code != ATTN_I8) || pg->Hkv < 1 || pg->Hkv > 65535 ||
+      pg->num_pages < 1 || pg->page_size < 1 || pg->page_size > 65536 ||
+      (long long)pg->num_pages * pg->page_size >= (1ll << 31))
+    return ATTN_ERR_INVALID_ARG;
+  // 16-byte rows for the copies; below 2^40 bytes for the tensor maps
+  for (long long s : {pg->page_stride, pg->head_stride, pg->token_stride})
+    if (s < HEAD_DIM || s % 16 != 0 || s >= (1ll << 40)) return ATTN_ERR_INVALID_ARG;
+  if (pg->page_size % 16 != 0 ||
+      (pg->block != 1 && pg->block != 16 && pg->block != 32 && pg->block != 64))
+    return ATTN_ERR_UNSUPPORTED;
+  if (pg->page_size % pg->block != 0) return ATTN_ERR_INVALID_ARG;
+  // a page's scales of a head lie together; one a token is read 16 at a time
+  for (long long s : {pg->scale_page_stride, pg->scale_head_stride})
+    if (s < pg->page_size / pg->block || s >= (1ll << 40) || (pg->block == 1 && s % 16 != 0))
+      return ATTN_ERR_INVALID_ARG;
+  int shift = 0;
+  while ((1 << shift) < pg->block) ++shift;
+  *out = {pg->num_pages,    pg->page_size,   pg->Hkv,          pg->block,
+          shift,            pg->page_stride, pg->head_stride,  pg->token_stride,
+          pg->scale_page_stride, pg->scale_head_stride};
+  return ATTN_OK;
+}
+
+attn_status_t check_buffers8(const attn_pages8_t* pg, const void* k_pages, const void* v_pages,
+                             const uint8_t* k_scales, const uint8_t* v_scales) {
+  const size_t a = pg->block == 1 ? 16 : 1;
+  return k_pages && v_pages && k_scales && v_scales && aligned(k_pages, 16) &&
+                 aligned(v_pages, 16) && aligned(k_scales, a) && aligned(v_scales, a)
+             ? ATTN_OK
+             : ATTN_ERR_INVALID_ARG;
+}
+
+attn_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_paged8_store(const attn_pages8_t* pages, int T, const void* k, const void* v,
+                                long long k_stride, long long v_stride, const long long* slot_map,
+                                void* k_pages, void* v_pages, uint8_t* k_scales,
+                                uint8_t* v_scales, void* stream) {
+  Pages8 pg;
+  attn_status_t r = check_pages8(pages, &pg);
+  if (r != ATTN_OK) return r;
+  // rows * heads is a 32-bit index
+  if (T < 0 || (long long)T * pages->Hkv >= (1ll << 31) - 16) return ATTN_ERR_INVALID_ARG;
+  if (T == 0) return ATTN_OK;
+  const long long row = (long long)pages->Hkv * HEAD_DIM;
+  if (!k || !v || !slot_map || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8) ||
+      k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return ATTN_ERR_INVALID_ARG;
+  r = check_buffers8(pages, k_pages, v_pages, k_scales, v_scales);
+  if (r != ATTN_OK) return r;
+  return cuda_status(launch_paged8_store(pages->dtype == ATTN_BF16, pages->code == ATTN_I8, pg, T,
+                                         k, v, k_stride, v_stride, slot_map, k_pages, v_pages,
+                                         k_scales, v_scales, static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, const int* start,
+                               const int* cu_seqlens, const int* block_table, int table_stride,
+                               int max_pages, const void* k_pages, const void* v_pages,
+                               const uint8_t* k_scales, const uint8_t* v_scales, void* k, void* v,
+                               void* stream) {
+  Pages8 pg;
+  attn_status_t r = check_pages8(pages, &pg);
+  if (r != ATTN_OK) return r;
+  if (B < 1 || B > 65536 || total < 0 || max_pages < 1 || table_stride < max_pages ||
+      (long long)max_pages * pages->page_size >= (1ll << 31))
+    return ATTN_ERR_INVALID_ARG;
+  if (total == 0) return ATTN_OK;
+  if (!cu_seqlens || !aligned(cu_seqlens, 4) || (start && !aligned(start, 4)) || !block_table ||
+      !aligned(block_table, 4) || !k || !v || !aligned(k, 16) || !aligned(v, 16))
+    return ATTN_ERR_INVALID_ARG;
+  r = check_buffers8(pages, k_pages, v_pages, k_scales, v_scales);
+  if (r != ATTN_OK) return r;
+  return cuda_status(launch_paged8_load(pages->dtype == ATTN_BF16, pages->code == ATTN_I8, pg, B,
+                                        total, start, cu_seqlens, block_table, table_stride,
+                                        max_pages, k_pages, v_pages, k_scales, v_scales, k, v,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
