@@ -424,6 +424,18 @@ attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, con
                                const uint8_t* k_scales, const uint8_t* v_scales, void* k, void* v,
                                void* stream);
 
+/* attn_paged_fwd over an 8-bit cache: the attention over the values that the codes
+ * and scales stand for, exactly (attn_paged8_load gives the same ones).  Workspace of
+ * attn_paged_workspace_size; masks, lengths, results and statuses as attn_paged_fwd
+ * has them.  A block whose scale is 255 reads as NaN, which a new token must not see,
+ * as it must not see other values that are not finite. */
+attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pages, const void* q,
+                              const void* k_pages, const void* v_pages, const uint8_t* k_scales,
+                              const uint8_t* v_scales, const int* block_table, int table_stride,
+                              int max_pages, const float* sink, const attn_mask_desc_t* mask,
+                              float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                              void* stream);
+
 /* Synchronizes `stream`, then reads the status word that the last call which
  * used `ws` left in the workspace: ATTN_OK, or ATTN_ERR_TIMEOUT when a device
  * wait ran out, or ATTN_ERR_INVALID_ARG when attn_paged_fwd met a page

@@ -28,7 +28,7 @@ EXPORTS = ("attn_workspace_size", "attn_fwd", "attn_bwd", "attn_bwd_noalloc",
            "attn_get_device_status", "attn_noalloc_get_device_status", "attn_profile_enable",
            "attn_profile_read", "attn_status_string", "attn_paged_plan", "attn_paged_store",
            "attn_paged_workspace_size", "attn_paged_fwd", "attn_rope", "attn_paged8_store",
-           "attn_paged8_load")
+           "attn_paged8_load", "attn_paged8_fwd")
 
 
 class attn_shape_t(ctypes.Structure):
@@ -146,6 +146,10 @@ def load(build: bool = True) -> ctypes.CDLL:
                                              ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp,
                                              vp]
             lib.attn_paged8_load.restype = ctypes.c_int
+            lib.attn_paged8_fwd.argtypes = [ps, p8, vp, vp, vp, vp, vp, vp, ctypes.c_int,
+                                            ctypes.c_int, vp, pm, ctypes.c_float, vp, vp, vp, sz,
+                                            vp]
+            lib.attn_paged8_fwd.restype = ctypes.c_int
             lib.attn_status_string.argtypes = [ctypes.c_int]
             lib.attn_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -578,6 +582,15 @@ def attn_paged8_load(pages: attn_pages8_t, B, total, start, cu_seqlens, block_ta
                                    k, v, stream)
 
 
+def attn_paged8_fwd(shape, pages: attn_pages8_t, q, k_pages, v_pages, k_scales, v_scales,
+                    block_table, table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes,
+                    stream) -> int:
+    return load().attn_paged8_fwd(ctypes.byref(shape), ctypes.byref(pages), q, k_pages, v_pages,
+                                  k_scales, v_scales, block_table, table_stride, max_pages, sink,
+                                  ctypes.byref(mask), ctypes.c_float(scale), o, lse, ws, ws_bytes,
+                                  stream)
+
+
 def _one_device(*tensors):
     """All tensors on one CUDA device: a guard that makes it current."""
     devs = {t.get_device() for t in tensors if t is not None}
@@ -616,6 +629,9 @@ class PagedCache:
         self.dtype = k_pages.dtype
         self.desc = attn_pages_t(self.num_pages, self.page_size, self.Hkv, _dtype_code(k_pages),
                                  ks[0], ks[hd], ks[td])
+
+    def pointers(self):
+        return self.k_pages.data_ptr(), self.v_pages.data_ptr()
 
 
 class PagedCache8:
@@ -811,12 +827,12 @@ def paged_mask(kind: int, plan: PagedPlan, total_q: int, max_seqlen_q: int, max_
                 max_seqlen_k=max_seqlen_k)
 
 
-def paged_shape(q: torch.Tensor, cache: PagedCache, mask: Mask) -> attn_shape_t:
+def paged_shape(q: torch.Tensor, cache, mask: Mask) -> attn_shape_t:
     return attn_shape_t(mask.seqlen_k.numel(), q.shape[1], cache.Hkv, mask.max_seqlen_q,
                         mask.max_seqlen_k, q.shape[2], _dtype_code(q), 0)
 
 
-def paged_workspace(q: torch.Tensor, cache: PagedCache, mask: Mask,
+def paged_workspace(q: torch.Tensor, cache, mask: Mask,
                     shape: Optional[attn_shape_t] = None) -> torch.Tensor:
     r, n = attn_paged_workspace_size(shape or paged_shape(q, cache, mask))
     if r != ATTN_OK:
@@ -824,10 +840,10 @@ def paged_workspace(q: torch.Tensor, cache: PagedCache, mask: Mask,
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
-def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
+def paged_fwd(q, cache, block_table, sink, mask: Mask, scale: float,
               ws: Optional[torch.Tensor] = None, out=None, stream=None):
-    """Attention of the packed new tokens q [total_q, Hq, 128] over the cache;
-    returns (o, lse).  out: (o, lse) to write, of which lse may be None;
+    """Attention of the packed new tokens q [total_q, Hq, 128] over the cache, a
+    PagedCache or PagedCache8; returns (o, lse).  out: (o, lse) to write, of which lse may be None;
     without it they belong to `stream`, as fwd's results do."""
     cu, lens = mask.cu_seqlens_q, mask.seqlen_k
     if cu is None or lens is None or cu.numel() != lens.numel() + 1:
@@ -836,7 +852,7 @@ def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
         raise ValueError("q must be a contiguous [total_q, Hq, 128] tensor")
     T, Hq, _ = q.shape
     dtype, B = q.dtype, lens.numel()
-    if dtype != cache.k_pages.dtype:
+    if dtype != cache.dtype:
         raise ValueError("q and the cache must have one type")
     if block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B, max_pages]")
@@ -861,12 +877,13 @@ def paged_fwd(q, cache: PagedCache, block_table, sink, mask: Mask, scale: float,
         if ws is None:
             with _alloc_on(stream):
                 ws = paged_workspace(q, cache, mask, shape)
-        r = attn_paged_fwd(shape, cache.desc, q.data_ptr(), cache.k_pages.data_ptr(),
-                           cache.v_pages.data_ptr(), block_table.data_ptr(),
-                           row_stride if B > 1 else cols, cols, _ptr(sink), mask.desc(), scale,
-                           o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
+        call, name = (attn_paged8_fwd, "attn_paged8_fwd") if isinstance(cache, PagedCache8) else \
+            (attn_paged_fwd, "attn_paged_fwd")
+        r = call(shape, cache.desc, q.data_ptr(), *cache.pointers(), block_table.data_ptr(),
+                 row_stride if B > 1 else cols, cols, _ptr(sink), mask.desc(), scale,
+                 o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream))
     if r != ATTN_OK:
-        raise AttnError(r, "attn_paged_fwd")
+        raise AttnError(r, name)
     return o, lse
 
 

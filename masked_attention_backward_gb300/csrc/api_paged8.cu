@@ -1,7 +1,9 @@
 // api_paged8.cu -- the C ABI of the 8-bit cache (declared in
 // include/maskattn.h): argument checks, then the launches, on the caller's
 // stream.  Nothing is allocated and nothing is read back.
+#include "paged.h"
 #include "paged8.h"
+#include "tmap.h"
 
 using namespace mab;
 
@@ -91,6 +93,41 @@ attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, con
                                         total, start, cu_seqlens, block_table, table_stride,
                                         max_pages, k_pages, v_pages, k_scales, v_scales, k, v,
                                         static_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pages, const void* q,
+                              const void* k_pages, const void* v_pages, const uint8_t* k_scales,
+                              const uint8_t* v_scales, const int* block_table, int table_stride,
+                              int max_pages, const float* sink, const attn_mask_desc_t* mask,
+                              float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                              void* stream) {
+  attn_status_t r = check_paged_shape(shape);
+  Pages8 pg;
+  if (r == ATTN_OK) r = check_pages8(pages, &pg);
+  if (r != ATTN_OK) return r;
+  if (pages->dtype != shape->dtype || pages->Hkv != shape->Hkv) return ATTN_ERR_INVALID_ARG;
+  Paged8Params p;
+  CUtensorMap tQ, tK, tV;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  bool work = false;
+  r = paged_call(shape, pages->num_pages, pages->page_size, q, k_pages, v_pages, block_table,
+                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st, &p, &tQ,
+                 &work);
+  if (r != ATTN_OK || !work) return r;
+  r = check_buffers8(pages, k_pages, v_pages, k_scales, v_scales);
+  if (r != ATTN_OK) return r;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.scale_page_stride = pg.scale_page_stride;
+  p.scale_head_stride = pg.scale_head_stride;
+  p.scale_shift = pg.shift;
+  auto pages_map = [&](CUtensorMap* m, const void* base) {
+    return make_pages8_map(m, base, pg.num_pages, pg.page_size, pg.Hkv, pg.page_stride,
+                           pg.head_stride, pg.token_stride, (uint32_t)p.box_rows);
+  };
+  if (!pages_map(&tK, k_pages) || !pages_map(&tV, v_pages)) return ATTN_ERR_CUDA;
+  return cuda_status(launch_paged8_fwd(shape->dtype == ATTN_BF16, pages->code == ATTN_I8, p, tQ,
+                                       tK, tV, st));
 }
 
 }  // extern "C"

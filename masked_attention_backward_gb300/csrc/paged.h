@@ -55,12 +55,30 @@ struct PagedParams {
   int slot_floats;
 };
 
+// ... and over a cache of 8-bit codes.
+struct Paged8Params : PagedParams {
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  long long scale_page_stride, scale_head_stride;
+  int scale_shift;  // log2 of the tokens that share a scale
+};
+
+attn_status_t check_paged_shape(const attn_shape_t* sh);
+attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size, const void* q,
+                         const void* k_pages, const void* v_pages, const int* block_table,
+                         int table_stride, int max_pages, const float* sink,
+                         const attn_mask_desc_t* mask, float scale, void* o, float* lse, void* ws,
+                         size_t ws_bytes, cudaStream_t st, PagedParams* out, CUtensorMap* tQ,
+                         bool* work);
+
 cudaError_t launch_paged_plan(const attn_plan_t& p, cudaStream_t st);
 cudaError_t launch_paged_store(const attn_pages_t& pg, int T, const void* k, const void* v,
                                long long k_stride, long long v_stride, const long long* slot_map,
                                void* k_pages, void* v_pages, cudaStream_t st);
 cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap& tQ,
                              const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
+cudaError_t launch_paged8_fwd(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tQ,
+                              const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ uint32_t cluster_rank() {

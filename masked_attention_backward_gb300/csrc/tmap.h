@@ -104,4 +104,22 @@ inline bool make_pages_map(CUtensorMap* m, const void* base, bool bf16, int64_t 
   return r == CUDA_SUCCESS;
 }
 
+// ... and pages of one-byte codes, strides in bytes: a box is `rows` whole rows of
+// 128 bytes.
+inline bool make_pages8_map(CUtensorMap* m, const void* base, int64_t pages, int64_t page_size,
+                            int64_t heads, int64_t page_stride, int64_t head_stride,
+                            int64_t token_stride, uint32_t rows) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {128, (cuuint64_t)page_size, (cuuint64_t)heads, (cuuint64_t)pages};
+  cuuint64_t strides[3] = {(cuuint64_t)token_stride, (cuuint64_t)head_stride,
+                           (cuuint64_t)page_stride};
+  cuuint32_t box[4] = {128, rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace mab

@@ -1,0 +1,287 @@
+"""Attention over the 8-bit cache against plain 64-bit attention over the values
+that its codes and scales stand for, one request and head at a time, within
+attn64's bounds (the values are exact in 16 bits, so no rounding joins those of the
+16-bit cache).  Unless a test says otherwise, rows and blocks that no new token
+sees hold codes without a number and scales of NaN, and the table holds -7 where no
+key of a page is seen."""
+import math
+import random
+
+import pytest
+import torch
+
+import attn64
+import quant64
+from masked_attention_backward_gb300 import binding as mab
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+SCALE = 1.0 / math.sqrt(128)
+NONE, CAUSAL, SLIDING, FIRST = (mab.ATTN_MASK_NONE, mab.ATTN_MASK_CAUSAL, mab.ATTN_MASK_SLIDING,
+                                mab.ATTN_MASK_SLIDING_FIRST)
+FORMS = [("e4m3", F16), ("e4m3", BF16), ("i8", F16), ("i8", BF16)]
+IDS = ["e4m3-f16", "e4m3-bf16", "i8-f16", "i8-bf16"]
+
+
+class Case:
+    """reqs: (new tokens, keys) of each request."""
+
+    def __init__(self, reqs, Hq=4, Hkv=2, ps=16, block=16, form=("e4m3", BF16), layout="HND",
+                 kind=CAUSAL, window=0, first=0, sink=True, seed=0, pad=0, spare_cols=1,
+                 spread=3):
+        g = torch.Generator("cpu").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g)
+        code, dtype = form
+        self.reqs, self.kind, self.window, self.first = reqs, kind, window, first
+        self.Hq, self.Hkv, self.ps, self.dtype = Hq, Hkv, ps, dtype
+        held = [-(-L // ps) for _, L in reqs]
+        P, cols = sum(held) + 3, max(held) + spare_cols
+        ids = list(range(P))
+        random.Random(seed).shuffle(ids)
+        table = torch.full((len(reqs), cols), -7, dtype=torch.int32)
+        self.vis, live = [], torch.zeros(P, ps, dtype=torch.bool)
+        at, rows = 0, []
+        for b, (n, L) in enumerate(reqs):
+            x, j = torch.arange(L - n, L), torch.arange(L)
+            vis = attn64.window_first(x, j, None if kind == CAUSAL else window,
+                                      first if kind == FIRST else 0)
+            if kind == NONE:
+                vis = torch.ones(n, L, dtype=torch.bool)
+            seen = vis.any(0)
+            pages = torch.tensor(ids[at:at + held[b]], dtype=torch.long)
+            at += held[b]
+            rows.append(pages[j // ps] * ps + j % ps if L else torch.zeros(0, dtype=torch.long))
+            live.view(-1)[rows[b][seen]] = True
+            for c in range(held[b]):
+                if bool(seen[c * ps:(c + 1) * ps].any()):
+                    table[b, c] = int(pages[c])
+            self.vis.append(vis.cuda())
+        caches = []
+        per = ps // block
+        for _ in range(2):
+            # each block at a magnitude of its own, its exponent up to two larger than
+            # need be (as one that joined larger rows has it)
+            c = quant64.Cache64(P, Hkv, ps, block, code, dtype)
+            m = torch.randint(-spread, spread + 1, (P, Hkv, per), generator=g)
+            top = math.frexp(quant64.TOP[code])[1]
+            c.exp = m + 3 - top + torch.randint(0, 3, m.shape, generator=g)
+            x = r(P, ps, Hkv, 128).double() * \
+                torch.exp2(m.double()).repeat_interleave(block, 2).transpose(1, 2)[..., None]
+            unit = torch.exp2(c.exp.double()).repeat_interleave(block, 2).transpose(1, 2)[..., None]
+            c.num = quant64.nearest(code, x / unit, quant64.TOP[code])
+            caches.append(c)
+        vals = [c.values(torch.arange(P * ps)) for c in caches]
+        self.k = [vals[0][s].cuda() for s in rows]
+        self.v = [vals[1][s].cuda() for s in rows]
+        self.cache = quant64.make(*caches, layout)
+        # what nobody sees
+        dead = ~live
+        junk = 0x7f if code == "e4m3" else 0x80
+        d = dead[:, None, :, None] if layout == "HND" else dead[:, :, None, None]
+        for c in (self.cache.k_pages, self.cache.v_pages):
+            u = c.view(torch.uint8)
+            u.copy_(torch.where(d.cuda(), torch.full_like(u, junk), u))
+        gone = dead.view(P, 1, per, block).all(3).expand(P, Hkv, per).cuda()
+        for s in (self.cache.k_scales, self.cache.v_scales):
+            s.copy_(torch.where(gone, torch.full_like(s, 255), s))
+        self.table = table.cuda()
+        self.T = sum(n for n, _ in reqs) + pad
+        self.q = r(self.T, Hq, 128).to(dtype).cuda()
+        self.sink = r(Hq).cuda() if sink else None
+        cu = [0]
+        for n, _ in reqs:
+            cu.append(cu[-1] + n)
+        self.cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        self.lens = torch.tensor([L for _, L in reqs], dtype=torch.int32, device="cuda")
+        self.mask = mab.Mask(kind=kind, window=window, first=first, cu_seqlens_q=self.cu,
+                             seqlen_k=self.lens, total_q=self.T,
+                             max_seqlen_q=max(max(n for n, _ in reqs), 1),
+                             max_seqlen_k=max(max(L for _, L in reqs), 1))
+
+    def run(self, **kw):
+        ws = mab.paged_workspace(self.q, self.cache, self.mask)
+        ws.fill_(0xff)
+        out = (torch.full_like(self.q, 7.0),
+               torch.full((self.Hq, self.T), 7.0, device="cuda"))
+        mab.paged_fwd(self.q, self.cache, self.table, self.sink, self.mask, SCALE, ws=ws, out=out,
+                      **kw)
+        torch.cuda.synchronize()
+        return out, mab.device_status(ws)
+
+    def check(self, o, lse):
+        g, t0 = self.Hq // self.Hkv, 0
+        for b, (n, L) in enumerate(self.reqs):
+            for h in range(self.Hq):
+                ro, rl, ob, lb = attn64.head_fwd(
+                    self.q[t0:t0 + n, h], self.k[b][:, h // g], self.v[b][:, h // g], self.vis[b],
+                    None if self.sink is None else float(self.sink[h]), SCALE)
+                attn64.check(f"o of request {b} head {h}", o[t0:t0 + n, h], ro, ob)
+                attn64.check(f"lse of request {b} head {h}", lse[h, t0:t0 + n], rl, lb)
+            t0 += n
+        # rows behind the last request stay as they were
+        assert bool((o[t0:] == 7).all()) and bool((lse[:, t0:] == 7).all())
+
+
+def _go(*a, **kw):
+    c = Case(*a, **kw)
+    (o, lse), status = c.run()
+    assert status == mab.ATTN_OK
+    c.check(o, lse)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+@pytest.mark.parametrize("L", [1, 2, 15, 16, 17, 63, 64, 65, 127, 129, 640, 1001])
+def test_one_token(cuda_lib, L, form):
+    _go([(1, L)], form=form, block=1 if L % 3 else 16, sink=L % 2 == 0, seed=L)
+
+
+@pytest.mark.parametrize("n,L", [(1, 1), (2, 2), (3, 70), (64, 64), (65, 65), (127, 300),
+                                 (200, 1000), (500, 500)])
+@pytest.mark.parametrize("kind,window,first", [(CAUSAL, 0, 0), (SLIDING, 1, 0), (SLIDING, 70, 0),
+                                               (FIRST, 40, 3), (FIRST, 100, 130), (NONE, 0, 0)])
+def test_chunks(cuda_lib, n, L, kind, window, first):
+    _go([(n, L)], kind=kind, window=window, first=first, seed=n + L, pad=3,
+        block=1 if n % 2 else 16, form=FORMS[(n + window) % 4])
+
+
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+@pytest.mark.parametrize("ps,block", [(16, 1), (16, 16), (32, 32), (48, 1), (48, 16), (64, 64),
+                                      (80, 16), (128, 32), (128, 64), (256, 1)])
+def test_pages(cuda_lib, ps, block, layout):
+    _go([(1, 700), (5, 333), (40, 41)], ps=ps, block=block, layout=layout, seed=ps,
+        form=FORMS[ps // 16 % 4])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (5, 1), (8, 1), (9, 1), (16, 2), (33, 1),
+                                    (64, 8), (128, 1)])
+@pytest.mark.parametrize("n", [1, 2, 4, 17])
+def test_heads(cuda_lib, Hq, Hkv, n):
+    _go([(n, 150), (1, 30)], Hq=Hq, Hkv=Hkv, seed=Hq + n, form=FORMS[n % 4], block=16)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+@pytest.mark.parametrize("new", [1, 4])
+def test_long_context_over_many_ctas(cuda_lib, form, new):
+    _go([(new, 20011)], Hq=8, Hkv=2, ps=64, block=64 if new == 1 else 1, form=form, seed=new)
+
+
+@pytest.mark.parametrize("kind,window,first", [(CAUSAL, 0, 0), (FIRST, 200, 5)])
+def test_ragged_batch(cuda_lib, kind, window, first):
+    """Requests without new tokens, without keys, single tokens, chunks."""
+    r = random.Random(7)
+    reqs = [(1, r.randint(1, 900)) for _ in range(12)]
+    reqs += [(0, 50), (0, 0), (130, 700), (3, 3), (1, 1), (9, 2000), (0, 0), (2, 511)]
+    r.shuffle(reqs)
+    _go(reqs, Hq=8, Hkv=2, ps=32, block=16, kind=kind, window=window, first=first, pad=5, seed=3)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+def test_more_new_tokens_than_keys(cuda_lib, form):
+    """Rows before position zero see nothing: the sink, or +inf."""
+    for sink in (True, False):
+        c = Case([(1, 40), (1, 8)], form=form, sink=sink)
+        # request 0 brings one token over no key at all
+        c.lens[0] = 0
+        c.reqs[0] = (1, 0)
+        c.vis[0], c.k[0], c.v[0] = c.vis[0][:, :0], c.k[0][:0], c.v[0][:0]
+        (o, lse), status = c.run()
+        assert status == mab.ATTN_OK
+        c.check(o, lse)
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_bad_page(cuda_lib, n):
+    """A page outside the cache stands for zeros, and the status says so."""
+    c = Case([(n, 100)], ps=16, block=1, form=("i8", F16))
+    for bad in (c.cache.num_pages, -1, -2 ** 31, 2 ** 31 - 1):
+        c.table[0, 2] = bad
+        c.k[0][32:48] = 0
+        c.v[0][32:48] = 0
+        (o, lse), status = c.run()
+        assert status == mab.ATTN_ERR_INVALID_ARG
+        c.check(o, lse)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+@pytest.mark.parametrize("n", [1, 20])
+def test_extreme_scales(cuda_lib, form, n):
+    """Exponents over the whole range that the store gives values of size 2^-12
+    to 2^12, beside each other."""
+    _go([(n, 300)], form=form, block=16, spread=6, seed=5)
+    _go([(n, 300)], form=form, block=1, spread=6, seed=6)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_query_rows_not_finite(cuda_lib, n):
+    """A row of q that is not finite gives NaN in its own o and lse alone."""
+    c = Case([(n, 200), (1, 90)], Hq=4, Hkv=1, form=("e4m3", BF16))
+    (o0, l0), _ = c.run()
+    c.q[0, 2, 5] = float("nan")
+    (o, lse), status = c.run()
+    assert status == mab.ATTN_OK
+    assert bool(torch.isnan(o[0, 2]).all()) and bool(torch.isnan(lse[2, 0]))
+    o[0, 2], lse[2, 0] = o0[0, 2], l0[2, 0]
+    assert torch.equal(o, o0) and torch.equal(lse, l0)
+
+
+@pytest.mark.parametrize("n", [1, 50])
+def test_captured_with_other_lengths(cuda_lib, n):
+    a = Case([(n, 1000), (n, 64), (n, 2000)], ps=32, form=("e4m3", F16), seed=1)
+    ws = mab.paged_workspace(a.q, a.cache, a.mask)
+    out = (torch.full_like(a.q, 7.0), torch.full((a.Hq, a.T), 7.0, device="cuda"))
+    call = lambda: mab.paged_fwd(a.q, a.cache, a.table, a.sink, a.mask, SCALE, ws=ws, out=out)
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    b = Case([(n, 300), (n, 1999), (n, 51)], ps=32, form=("e4m3", F16), seed=2)
+    P = b.cache.num_pages
+    assert P <= a.cache.num_pages
+    for x, y in ((a.cache.k_pages, b.cache.k_pages), (a.cache.v_pages, b.cache.v_pages)):
+        x.view(torch.uint8)[:P].copy_(y.view(torch.uint8)[:P])
+    for x, y in ((a.cache.k_scales, b.cache.k_scales), (a.cache.v_scales, b.cache.v_scales)):
+        x[:P].copy_(y[:P])
+    cols = min(a.table.shape[1], b.table.shape[1])
+    a.table[:, :cols].copy_(b.table[:, :cols])
+    a.lens.copy_(b.lens)
+    a.q.copy_(b.q)
+    a.sink.copy_(b.sink)
+    g.replay()
+    torch.cuda.synchronize()
+    assert mab.device_status(ws) == mab.ATTN_OK
+    b.check(*out)
+
+
+def test_repeats_are_equal(cuda_lib):
+    for n in (1, 3, 70):
+        c = Case([(n, 5000), (n, 900), (n, 77)], Hq=8, Hkv=2, ps=32, seed=n)
+        (o0, l0), _ = c.run()
+        for _ in range(5):
+            (o, lse), _ = c.run()
+            assert torch.equal(o, o0) and torch.equal(lse, l0)
+
+
+def test_no_lse_and_other_stream(cuda_lib):
+    c = Case([(1, 300), (20, 100)], form=("i8", BF16))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    o, lse = mab.paged_fwd(c.q, c.cache, c.table, c.sink, c.mask, SCALE, stream=st)
+    st.synchronize()
+    c.check(o, lse)
+    out = torch.empty_like(c.q)
+    mab.paged_fwd(c.q, c.cache, c.table, c.sink, c.mask, SCALE, out=(out, None))
+    assert torch.equal(out, o)
+
+
+def test_waits_that_run_out(cuda_lib, monkeypatch):
+    """The loader issues nothing: the call ends with a status."""
+    c = Case([(40, 500)])
+    monkeypatch.setenv("MASKATTN_TEST_NO_LOADS", "1")
+    monkeypatch.setenv("MASKATTN_WAIT_TIMEOUT_NS", "20000000")
+    _, status = c.run()
+    monkeypatch.delenv("MASKATTN_TEST_NO_LOADS")
+    monkeypatch.delenv("MASKATTN_WAIT_TIMEOUT_NS")
+    assert status == mab.ATTN_ERR_TIMEOUT
+    (o, lse), status = c.run()
+    assert status == mab.ATTN_OK
+    c.check(o, lse)
