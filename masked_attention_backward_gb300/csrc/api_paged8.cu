@@ -121,13 +121,16 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   p.scale_page_stride = pg.scale_page_stride;
   p.scale_head_stride = pg.scale_head_stride;
   p.scale_shift = pg.shift;
+  const bool bf16 = shape->dtype == ATTN_BF16, i8 = pages->code == ATTN_I8;
+  if (p.tile_rows <= PAGED8_ROWS)
+    return cuda_status(launch_paged8_rows(bf16, i8, p, q, k_pages, v_pages, pg.page_stride,
+                                          pg.head_stride, pg.token_stride, st));
   auto pages_map = [&](CUtensorMap* m, const void* base) {
     return make_pages8_map(m, base, pg.num_pages, pg.page_size, pg.Hkv, pg.page_stride,
                            pg.head_stride, pg.token_stride, (uint32_t)p.box_rows);
   };
   if (!pages_map(&tK, k_pages) || !pages_map(&tV, v_pages)) return ATTN_ERR_CUDA;
-  return cuda_status(launch_paged8_fwd(shape->dtype == ATTN_BF16, pages->code == ATTN_I8, p, tQ,
-                                       tK, tV, st));
+  return cuda_status(launch_paged8_fwd(bf16, i8, p, tQ, tK, tV, st));
 }
 
 }  // extern "C"

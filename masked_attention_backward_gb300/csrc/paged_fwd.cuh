@@ -1311,6 +1311,20 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedParams p) {
   *reinterpret_cast<uint2*>(p.out + ((size_t)tok * p.Hq + head) * HEAD_DIM + 4 * lane) = o;
 }
 
+template <bool BF16>
+cudaError_t launch_paged_join(const PagedParams& p, cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((p.tile_rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, k_paged_join<BF16>, p);
+}
+
 template <bool BF16, int FORM>
 cudaError_t launch_paged(const paged_params_t<FORM>& p, const CUtensorMap& tQ,
                          const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st) {
@@ -1326,15 +1340,7 @@ cudaError_t launch_paged(const paged_params_t<FORM>& p, const CUtensorMap& tQ,
   cfg.stream = st;
   e = cudaLaunchKernelEx(&cfg, kern, tQ, tK, tV, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((p.tile_rows + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_paged_join<BF16>, static_cast<const PagedParams&>(p));
+  return launch_paged_join<BF16>(p, st);
 }
 
 }  // namespace mab

@@ -95,24 +95,21 @@ __device__ __forceinline__ uint32_t add16x2(uint32_t a, uint32_t b) {
 //     their places, which leaves the exponent 120 too small.
 template <bool BF16, bool I8>
 __device__ __forceinline__ uint32_t code_pair(uint32_t a, uint32_t b, int lo, int hi) {
-  const uint32_t pick = (uint32_t)(lo | hi << 4);  // two bytes
-  if (I8 && !BF16) {
-    const uint32_t u = __byte_perm(a, b, pick) ^ 0x8080u;
-    return add16x2<false>(__byte_perm(u, 0x64646464u, 0x4140), 0xe480e480u);  // - 1152
-  }
   if (I8) {
-    const uint32_t u = __byte_perm(a, b, pick);
-    const uint32_t w = __byte_perm(u, 0, 0x4140);  // a byte a half
+    // a byte at the foot of each half, anything above it
+    const uint32_t u = __byte_perm(a, b, (uint32_t)(lo | hi << 8));
+    if (!BF16) return add16x2<false>((u & 0x00ff00ffu) ^ 0x64806480u, 0xe480e480u);  // - 1152
     // 128 + low bits, less 128, or 256 for a set sign
-    return add16x2<true>((w & 0x007f007fu) | 0x43004300u, (w & 0x00800080u) | 0xc300c300u);
+    return add16x2<true>((u & 0x007f007fu) | 0x43004300u, (u & 0x00800080u) | 0xc300c300u);
   }
   if (!BF16) {
     uint32_t d;
-    const uint16_t two = (uint16_t)__byte_perm(a, b, pick);
+    const uint16_t two = (uint16_t)__byte_perm(a, b, (uint32_t)(lo | hi << 4));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(two));
     return d;
   }
-  const uint32_t h = __byte_perm(__byte_perm(a, b, pick), 0, 0x1404);  // in the high bytes
+  // a byte at the head of each half, anything below it
+  const uint32_t h = __byte_perm(a, b, (uint32_t)(lo << 4 | hi << 12));
   return mul16x2<true>(((h >> 4) & 0x07f007f0u) | (h & 0x80008000u), 0x7b807b80u);  // 2^120
 }
 
@@ -122,6 +119,13 @@ template <bool BF16, bool I8>
 __device__ __forceinline__ uint2 values_of(uint32_t codes, uint32_t scale2) {
   return make_uint2(mul16x2<BF16>(code_pair<BF16, I8>(codes, codes, 0, 1), scale2),
                     mul16x2<BF16>(code_pair<BF16, I8>(codes, codes, 2, 3), scale2));
+}
+
+// A scale byte as fp32 (the same numbers as scale_pair's).
+template <bool BF16>
+__device__ __forceinline__ float scale_float(int s) {
+  const int e = BF16 ? max(s, 1) : min(max(s, 127 - 24), 127 + 15);
+  return __int_as_float(s == SCALE_NAN ? 0x7fffffff : e << 23);
 }
 
 }  // namespace mab
