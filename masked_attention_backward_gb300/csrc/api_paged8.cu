@@ -122,7 +122,8 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   p.scale_head_stride = pg.scale_head_stride;
   p.scale_shift = pg.shift;
   const bool bf16 = shape->dtype == ATTN_BF16, i8 = pages->code == ATTN_I8;
-  if (p.tile_rows <= PAGED8_ROWS)
+  // (whose offsets inside 16 rows are 32-bit)
+  if (p.tile_rows <= PAGED8_ROWS && pg.token_stride < (1 << 27))
     return cuda_status(launch_paged8_rows(bf16, i8, p, q, k_pages, v_pages, pg.page_stride,
                                           pg.head_stride, pg.token_stride, st));
   auto pages_map = [&](CUtensorMap* m, const void* base) {

@@ -86,13 +86,20 @@ __device__ __forceinline__ uint32_t add16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// e4m3 codes `lo` and `hi` (bytes of a, b) as a pair of bf16 values times 2^-120:
+// sign, exponent and mantissa in their places.
+__device__ __forceinline__ uint32_t code_bits(uint32_t a, uint32_t b, int lo, int hi) {
+  // a byte at the head of each half, anything below it
+  const uint32_t h = __byte_perm(a, b, (uint32_t)(lo << 4 | hi << 12));
+  return ((h >> 4) & 0x07f007f0u) | (h & 0x80008000u);
+}
+
 // Codes `lo` and `hi` (bytes of the register pair a, b as __byte_perm counts
 // them) as a pair of 16-bit values, exactly.
 //   int8: the byte becomes the low bits of a number whose exponent makes its
 //     unit 1 (f16: 1024 + (c + 128); bf16, which has seven bits below the first:
 //     128 + the low seven), and what was added is taken off;
-//   e4m3 to f16: the conversion; to bf16: sign, exponent and mantissa moved to
-//     their places, which leaves the exponent 120 too small.
+//   e4m3 to f16: the conversion; to bf16: code_bits, times 2^120.
 template <bool BF16, bool I8>
 __device__ __forceinline__ uint32_t code_pair(uint32_t a, uint32_t b, int lo, int hi) {
   if (I8) {
@@ -108,9 +115,7 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t a, uint32_t b, int lo, in
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(two));
     return d;
   }
-  // a byte at the head of each half, anything below it
-  const uint32_t h = __byte_perm(a, b, (uint32_t)(lo << 4 | hi << 12));
-  return mul16x2<true>(((h >> 4) & 0x07f007f0u) | (h & 0x80008000u), 0x7b807b80u);  // 2^120
+  return mul16x2<true>(code_bits(a, b, lo, hi), 0x7b807b80u);  // 2^120
 }
 
 // Four codes times their block's scale (a pair, scale_pair): exact for scales

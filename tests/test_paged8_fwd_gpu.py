@@ -211,6 +211,45 @@ def test_extreme_scales(cuda_lib, form, n):
     _go([(n, 300)], form=form, block=1, spread=6, seed=6)
 
 
+@pytest.mark.parametrize("form", FORMS, ids=IDS)
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_one_key_gives_its_value(cuda_lib, form, n):
+    """A row that sees one key has that key's value, for every code and for scales
+    from the least to the largest that the store writes: nothing is rounded on the
+    way to O.  Row i sees key i alone (a window of one)."""
+    code, dtype = form
+    for e in (quant64.LEAST[form], -9, 0, 7) + ((60, 119) if dtype == BF16 else ()):
+        c = Case([(n, n)], Hq=2, Hkv=1, form=form, block=1, kind=SLIDING, window=1, sink=False)
+        num = torch.arange(256, dtype=torch.uint8)
+        num[127 if code == "e4m3" else 128] = 0
+        if code == "e4m3":
+            num[255] = 0
+        rows = torch.stack([num[:128], num[128:]])[torch.arange(16) % 2]   # of a page
+        pages = rows.view(1, 1, 16, 128).expand(c.cache.k_pages.shape)
+        c.cache.v_pages.view(torch.uint8).copy_(pages)
+        c.cache.v_scales.fill_(e + 127)
+        (o, lse), status = c.run()
+        assert status == mab.ATTN_OK
+        want = rows.view(quant64.TYPES[code]).float()[torch.arange(n) % 16].double() * 2.0 ** e
+        assert torch.equal(o.cpu().double(), want[:, None].expand(n, 2, 128))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -20, 2.0 ** 20, 2.0 ** 100])
+def test_query_magnitudes(cuda_lib, size, n):
+    """bf16 queries of any size over keys of the opposite one."""
+    c = Case([(n, 200)], form=("e4m3", BF16), block=16, spread=0)
+    e = round(math.log2(size))
+    c.q.mul_(size)
+    for s, k in ((c.cache.k_scales, c.k),):
+        s.copy_(torch.where(s == 255, s, s - e) if abs(e) < 100 else
+                torch.where(s == 255, s, (s.int() - e).clamp(1, 254).to(torch.uint8)))
+        k[0].mul_(2.0 ** -e)
+    (o, lse), status = c.run()
+    assert status == mab.ATTN_OK
+    c.check(o, lse)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_query_rows_not_finite(cuda_lib, n):
     """A row of q that is not finite gives NaN in its own o and lse alone."""
