@@ -122,16 +122,14 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   p.scale_head_stride = pg.scale_head_stride;
   p.scale_shift = pg.shift;
   const bool bf16 = shape->dtype == ATTN_BF16, i8 = pages->code == ATTN_I8;
-  // (whose offsets inside 16 rows are 32-bit)
-  if (p.tile_rows <= PAGED8_ROWS && pg.token_stride < (1 << 27))
-    return cuda_status(launch_paged8_rows(bf16, i8, p, q, k_pages, v_pages, pg.page_stride,
-                                          pg.head_stride, pg.token_stride, st));
+  const bool few = p.tile_rows <= PAGED8_ROWS;
   auto pages_map = [&](CUtensorMap* m, const void* base) {
     return make_pages8_map(m, base, pg.num_pages, pg.page_size, pg.Hkv, pg.page_stride,
-                           pg.head_stride, pg.token_stride, (uint32_t)p.box_rows);
+                           pg.head_stride, pg.token_stride, few ? 16u : (uint32_t)p.box_rows);
   };
   if (!pages_map(&tK, k_pages) || !pages_map(&tV, v_pages)) return ATTN_ERR_CUDA;
-  return cuda_status(launch_paged8_fwd(bf16, i8, p, tQ, tK, tV, st));
+  return cuda_status(few ? launch_paged8_rows(bf16, i8, p, tK, tV, q, st)
+                         : launch_paged8_fwd(bf16, i8, p, tQ, tK, tV, st));
 }
 
 }  // extern "C"

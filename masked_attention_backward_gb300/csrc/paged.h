@@ -81,9 +81,8 @@ cudaError_t launch_paged8_fwd(bool bf16, bool i8, const Paged8Params& p, const C
                               const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
 // ... for calls of at most PAGED8_ROWS rows (tokens times query heads of a kv head).
 constexpr int PAGED8_ROWS = 16;
-cudaError_t launch_paged8_rows(bool bf16, bool i8, const Paged8Params& p, const void* q,
-                               const void* k_pages, const void* v_pages, long long page_stride,
-                               long long head_stride, long long token_stride, cudaStream_t st);
+cudaError_t launch_paged8_rows(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tK,
+                               const CUtensorMap& tV, const void* q, cudaStream_t st);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ uint32_t cluster_rank() {

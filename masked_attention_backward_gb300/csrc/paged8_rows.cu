@@ -17,9 +17,8 @@
 // values (f16, whose small probabilities times a small scale would lose bits).
 //
 // Warps share nothing while they walk a unit's keys, 16 at a time each in turn:
-// every thread brings its own 16-byte pieces by cp.async into its own slots,
-// which are free of bank conflicts and need no barrier.  At a piece's end the
-// warps' O, M and l meet in shared memory.
+// each brings its own slices into a ring of its own.  At a piece's end the warps'
+// O, M and l meet in shared memory.
 #include "paged_fwd.cuh"
 
 namespace mab {
@@ -97,8 +96,11 @@ struct Rows {
   static constexpr int MERGE = 128 / WARPS;     // rows whose shares meet at a time
   static constexpr int O_STRIDE = 132;          // floats: rows on other banks
   struct Smem {
-    uint4 ring[WARPS][STAGES][8][32];           // K: 4 pieces a lane, V: 4
-    uint32_t scales[WARPS][STAGES][8];          // a scale a token: 16 bytes of K, 16 of V
+    // K's and V's rows of a slice (128B swizzle), and 16 scales of each where every
+    // token has its own
+    uint8_t ring[WARPS][STAGES][2][16 * 128];
+    uint8_t scales[WARPS][STAGES][2][16];
+    uint64_t full[WARPS][STAGES];
     uint2 q[Q_REGS ? 1 : NT][8][32];            // Q's fragments
     float O[WARPS][MERGE][O_STRIDE];
     float ml[WARPS][N][2];                      // (M, l)
@@ -107,6 +109,7 @@ struct Rows {
     Unit unit[3];                               // unit j at j % 3, j + 2 known at j's end
     Pieces pieces;
     unsigned bad_page;
+    int abort_flag;
   };
   static_assert((PAGED_MAX_B + 1) * 8 + PAGED_MAX_B * 12 <= sizeof(Smem::ring),
                 "the line of the most requests fits the ring");
@@ -135,35 +138,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// 16 bytes to shared memory; the second form zeros where `there` is false (then
-// nothing is read).
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copy16_if(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(there ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy4_if(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(there ? 4 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// Waits until at most n of the committed groups are pending (n < 3).
-__device__ __forceinline__ void copies_wait(int n) {
-  if (n <= 0)
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (n == 1)
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
-}
-
 // Unit of a bf16 unit's O: probabilities that meet e4m3's moved bits (2^120 too
 // small) come times 2^112.
 template <bool I8>
@@ -171,17 +145,10 @@ constexpr float V_UNIT = I8 ? 1.f : 0x1p-8f;
 
 }  // namespace rows_side
 
-// Where the rows of q and of the pages are.
-struct RowsParams : Paged8Params {
-  const uint16_t* q;
-  const uint8_t* k_pages;
-  const uint8_t* v_pages;
-  long long page_stride, head_stride, token_stride;
-};
-
 template <bool BF16, bool I8, int NT>
 __global__ void __launch_bounds__(rows_side::Rows<NT>::THREADS, 1)
-k_paged8_rows(const __grid_constant__ RowsParams p) {
+k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CUtensorMap tV,
+              const uint16_t* __restrict__ q_rows, const __grid_constant__ Paged8Params p) {
   using namespace rows_side;
   using R = Rows<NT>;
   constexpr int WARPS = R::WARPS, STAGES = R::STAGES, LAG = R::LAG;
@@ -191,7 +158,16 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;  // row and column pair of the fragments
   grid_launch_dependents();               // the join's blocks may wait beside this grid
-  if (threadIdx.x == 0) s.bad_page = 0;
+  WaitCtx wc{p.cta_status + blockIdx.x, &s.abort_flag, p.timeout_ns};
+  if (threadIdx.x == 0) {
+    s.bad_page = 0;
+    s.abort_flag = 0;
+    *wc.status = DevStatus{};
+    for (int i = 0; i < WARPS * STAGES; ++i) mbar_init(smem_u32(&s.full[0][0] + i), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tK);
+    tma_prefetch_desc(&tV);
+  }
   {
     const Line line = line_at(s.ring, p.B);
     const int parts = lay_line(p, line, s.sums);
@@ -202,7 +178,9 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
         if (warp == 1) p.start[blockIdx.x + 1] = at;  // for the join
       }
     }
-    __syncthreads();  // the ring is free of the line
+    // the loads into the ring come after these generic accesses to it
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
   }
   if (warp == 0) {
     if (lane == 0) {
@@ -222,7 +200,7 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
   int u_slot = 0, u_cnt = 0, u_at = 0;
   auto slices = [&](const Unit& x) { return x.N < 0 ? 0 : (4 * x.N - warp + WARPS - 1) / WARPS; };
   // Lane l looks slice i + l up: its page (-1: no seen key, or no such page) ...
-  constexpr int ALL = 1, WHOLE = 2, NONE = 4;  // flags below the slice's first key
+  constexpr int WHOLE = 1, NONE = 2, BIG = 4;  // flags below the slice's first key
   auto first_key = [&](const Unit& u, const Walk& w, int i) {
     const int sl = warp + WARPS * (i + lane);
     return w.tile(u.s0 + (sl >> 2)) * Q_SUB + 16 * (sl & 3);
@@ -238,34 +216,42 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
     s.bad_page = 1;
     return -1;
   };
-  // ... and where its rows and scales are: batch of the 32 slices from u_at on
-  int b_key = 0, b_scale = 0, page_next = -1;
-  long long b_base = 0, b_sat = 0;
+  // ... and where its rows and scales are: batch of the 32 slices from u_at on.
+  // (Flags: every row sees all 16 keys; no page, zeros stand in; V's exponent is past
+  // what the moved bits take.)
+  int b_key = 0, b_page = 0, b_row = 0, page_next = -1;
+  long long b_sat = 0;            // a scale a token: their offset
+  float b_ks = 1.f, b_vs = 1.f;   // a scale for 16 tokens or more: the scales
   auto batch = [&](int page) {
     const Unit& u = s.unit[u_slot];
     const Walk w(p, u.n, u.L, 0);
     const int k0 = first_key(u, w, u_at);
-    const int r0 = k0 - div_by(k0, p.page_size, p.inv_page_size) * p.page_size;
+    b_row = k0 - div_by(k0, p.page_size, p.inv_page_size) * p.page_size;
     const int x0 = u.L - u.n;
     const bool whole = (p.causal ? k0 + 16 <= x0 + 1 : k0 + 16 <= u.L) &&
                        (!p.causal || k0 > u.L - 1 - p.window || k0 + 16 <= p.first);
-    b_key = k0 | (w.all(k0, k0 + 16) ? ALL : 0) | (whole ? WHOLE : 0) | (page < 0 ? NONE : 0);
-    b_base = max(page, 0) * p.page_stride + u.kvh * p.head_stride + r0 * p.token_stride;
-    b_sat = max(page, 0) * p.scale_page_stride + u.kvh * p.scale_head_stride +
-            (r0 >> p.scale_shift);
-    b_scale = 127 | 127 << 8;
-    if (p.scale_shift > 0 && page >= 0)
-      b_scale = __ldg(p.k_scales + b_sat) | __ldg(p.v_scales + b_sat) << 8;
+    b_key = k0 | (whole ? WHOLE : 0) | (page < 0 ? NONE : 0);
+    b_page = page < 0 ? p.num_pages : page;  // past the tensor's end a load reads zeros
+    const long long sat = max(page, 0) * p.scale_page_stride + u.kvh * p.scale_head_stride +
+                          (b_row >> p.scale_shift);
+    if (p.scale_shift == 0) {
+      b_sat = sat;
+    } else {
+      b_ks = b_vs = 1.f;
+      if (page >= 0) {
+        const int v = __ldg(p.v_scales + sat);
+        b_ks = scale_float<BF16>(__ldg(p.k_scales + sat));
+        b_vs = scale_float<BF16>(v);
+        if (v > 127 + 7) b_key |= BIG;
+      }
+    }
     page_next = page_of(u, u_at + 32);
   };
-  // this thread's pieces of a slice: K rows g and g + 8, bytes 16 c and 64 + 16 c on;
-  // V rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9, bytes 16 g on
-  const int ts = (int)p.token_stride;
-  const int k_off = g * ts + 16 * c, v_off = 2 * c * ts + 16 * g;
-  // A slice on its way: its first key and flags, and its scales (K's byte, V's the
-  // next one) where 16 tokens or more share one.
+  // A slice on its way: its first key and flags, and its scales where 16 tokens or
+  // more share one.
   struct Slice {
-    int key, scale;
+    int key;
+    float ks, vs;
   };
   bool more = false;  // the next unit may be taken up
   int page_nxt = -1;  // its first batch's pages
@@ -282,40 +268,28 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
     } else if ((u_at & 31) == 0 && u_at > 0) {
       batch(page_next);
     }
-    const int i = u_at & 31;
+    const int i = u_at & 31, kvh = s.unit[u_slot].kvh;
     sl.key = __shfl_sync(0xffffffffu, b_key, i);
-    sl.scale = __shfl_sync(0xffffffffu, b_scale, i);
-    const long long base = __shfl_sync(0xffffffffu, b_base, i);
-    uint4* to = &s.ring[warp][stage][0][lane];
-    const uint8_t* k = p.k_pages + base + k_off;
-    const uint8_t* v = p.v_pages + base + v_off;
-    if ((sl.key & (ALL | NONE)) == ALL) {
-      copy16(to, k);
-      copy16(to + 32, k + 64);
-      copy16(to + 64, k + 8 * ts);
-      copy16(to + 96, k + 8 * ts + 64);
-      copy16(to + 128, v);
-      copy16(to + 160, v + ts);
-      copy16(to + 192, v + 8 * ts);
-      copy16(to + 224, v + 9 * ts);
-    } else {
-      const Walk w(p, s.unit[u_slot].n, s.unit[u_slot].L, 0);
-      const int k0 = sl.key & ~15;
-#pragma unroll 1
-      for (int j = 0; j < 8; ++j) {
-        const int r = j < 4 ? g + 8 * (j >> 1) : 2 * c + (j & 1) + 8 * ((j - 4) >> 1);
-        const uint8_t* src = (j < 4 ? p.k_pages + 16 * c + 64 * (j & 1) : p.v_pages + 16 * g) +
-                             base + (long long)r * ts;
-        copy16_if(to + 32 * j, src, !(sl.key & NONE) && w.sees(k0 + r));
-      }
+    const int page = __shfl_sync(0xffffffffu, b_page, i);
+    const int row = __shfl_sync(0xffffffffu, b_row, i);
+    const uint32_t fb = smem_u32(&s.full[warp][stage]);
+    const uint32_t to = smem_u32(s.ring[warp][stage][0]);
+    const bool own_scales = p.scale_shift == 0 && !(sl.key & NONE);
+    if (!p.test_no_loads) {
+      if (lane == 0) mbar_arrive_expect_tx(fb, 2 * 16 * 128 + (own_scales ? 32 : 0));
+      __syncwarp();
+      tma_load_4d_w(to, &tK, 0, row, kvh, page, fb);
+      tma_load_4d_w(to + 16 * 128, &tV, 0, row, kvh, page, fb);
     }
     if (p.scale_shift == 0) {
       const long long sat = __shfl_sync(0xffffffffu, b_sat, i);
-      if (lane < 8)
-        copy4_if(&s.scales[warp][stage][lane],
-                 (lane < 4 ? p.k_scales : p.v_scales) + sat + 4 * (lane & 3), !(sl.key & NONE));
+      if (lane < 2 && own_scales && !p.test_no_loads)
+        bulk_load(smem_u32(s.scales[warp][stage][lane]), (lane ? p.v_scales : p.k_scales) + sat,
+                  16, fb);
+    } else {
+      sl.ks = __shfl_sync(0xffffffffu, b_ks, i);
+      sl.vs = __shfl_sync(0xffffffffu, b_vs, i);
     }
-    copies_commit();
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     ++u_at;
     return true;
@@ -324,9 +298,11 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
   // slices on their way, the earliest first
   Slice way[LAG + 1];
   int on_way = 0;
-  int from_stage = 0;  // of the earliest
+  int from_stage = 0;  // of the earliest, and the parity of its use
+  uint32_t from_ph = 0;
+  bool ok = true;
 #pragma unroll
-  for (int i = 0; i <= LAG; ++i) way[i].key = way[i].scale = 0;
+  for (int i = 0; i <= LAG; ++i) way[i] = {0, 1.f, 1.f};
   u_cnt = slices(s.unit[0]);
   if (u_cnt > 0) batch(page_of(s.unit[0], 0));
   auto fill = [&]() {
@@ -344,7 +320,7 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
     for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
     if (n < x.n * p.group && x.N > 0) {
       const int tl = n / p.group;
-      const uint16_t* q = p.q + ((long long)(x.off + tl) * p.Hq + x.kvh * p.group +
+      const uint16_t* q = q_rows + ((long long)(x.off + tl) * p.Hq + x.kvh * p.group +
                                  (n - tl * p.group)) * HEAD_DIM + 16 * c;
       v[0] = __ldg(reinterpret_cast<const uint4*>(q));
       v[1] = __ldg(reinterpret_cast<const uint4*>(q + 8));
@@ -420,28 +396,37 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
     }
     const int cnt = slices(cur);
 #pragma unroll 1
-    for (int i = 0; i < cnt; ++i) {
+    for (int i = 0; i < cnt && ok; ++i) {
       fill();
-      copies_wait(on_way - 1);
-      __syncwarp();
+      ok = mbar_wait_warp(smem_u32(&s.full[warp][from_stage]), from_ph, wc, TAG_KV_FULL);
+      if (!ok) break;
       const Slice sl = way[0];
-      const int st = from_stage;
-      const uint4* from = &s.ring[warp][st][0][lane];
-      // scales of keys g and g + 8 of K, and of 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of V
-      float kf[2];
-      int vb[4];
+      const uint8_t* rk = s.ring[warp][from_stage][0];
+      const uint8_t* rv = s.ring[warp][from_stage][1];
+      // scales of keys g and g + 8 of K, and of V: of these, or (f16) of 2 c, 2 c + 1,
+      // 2 c + 8 and 2 c + 9 as pairs
+      float kf[2] = {sl.ks, sl.ks}, vf[2] = {sl.vs, sl.vs};
+      bool big = sl.key & BIG;
+      uint32_t s01 = 0, s23 = 0;
       if (p.scale_shift == 0) {
-        const uint8_t* sc = reinterpret_cast<const uint8_t*>(s.scales[warp][st]);
-        kf[0] = scale_float<BF16>(sc[g]);
-        kf[1] = scale_float<BF16>(sc[g + 8]);
-        const uint16_t* sv = reinterpret_cast<const uint16_t*>(sc + 16);
-        vb[0] = sv[c] & 255;
-        vb[1] = sv[c] >> 8;
-        vb[2] = sv[c + 4] & 255;
-        vb[3] = sv[c + 4] >> 8;
-      } else {
-        kf[0] = kf[1] = scale_float<BF16>(sl.scale & 255);
-        vb[0] = vb[1] = vb[2] = vb[3] = sl.scale >> 8;
+        const uint8_t* sk = s.scales[warp][from_stage][0];
+        const uint8_t* sv = s.scales[warp][from_stage][1];
+        const bool none = sl.key & NONE;
+        kf[0] = none ? 1.f : scale_float<BF16>(sk[g]);
+        kf[1] = none ? 1.f : scale_float<BF16>(sk[g + 8]);
+        if (BF16) {
+          const int lo = none ? 127 : sv[g], hi = none ? 127 : sv[g + 8];
+          vf[0] = scale_float<true>(lo);
+          vf[1] = scale_float<true>(hi);
+          if (!I8) big = __any_sync(0xffffffffu, max(lo, hi) > 127 + 7);
+        } else {
+          const uint32_t a = none ? 0x7f7fu : *reinterpret_cast<const uint16_t*>(sv + 2 * c);
+          const uint32_t b = none ? 0x7f7fu : *reinterpret_cast<const uint16_t*>(sv + 2 * c + 8);
+          s01 = (scale_pair<false>(a & 255) & 0xffffu) | (scale_pair<false>(a >> 8) << 16);
+          s23 = (scale_pair<false>(b & 255) & 0xffffu) | (scale_pair<false>(b >> 8) << 16);
+        }
+      } else if (!BF16) {
+        s01 = s23 = pack2<false>(sl.vs, sl.vs);
       }
       // ---- scores: f16 products of the codes themselves
       float sc[NT][4];
@@ -453,14 +438,14 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
           for (int j = 0; j < 4; ++j) sc[t][j] = s1[t][j] = 0.f;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const uint4 a = from[32 * hf], b = from[32 * (2 + hf)];
+          // bytes 16 c on of rows g and g + 8, then bytes 64 + 16 c on
+          const uint8_t* at = rk + ((g * 128 + ((c ^ g) << 4)) ^ (64 * hf));
+          const uint4 a = *reinterpret_cast<const uint4*>(at);
+          const uint4 b = *reinterpret_cast<const uint4*>(at + 1024);
           const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = code_pair<false, I8>(aw[j], aw[j], 0, 1);
-            const uint32_t a1 = code_pair<false, I8>(bw[j], bw[j], 0, 1);
-            const uint32_t a2 = code_pair<false, I8>(aw[j], aw[j], 2, 3);
-            const uint32_t a3 = code_pair<false, I8>(bw[j], bw[j], 2, 3);
+            const uint2 pa = word_pairs<false, I8>(aw[j]), pb = word_pairs<false, I8>(bw[j]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               uint2 q;
@@ -468,7 +453,7 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
                 q = make_uint2(qf[(8 * hf + 2 * j) % 16], qf[(8 * hf + 2 * j + 1) % 16]);
               else
                 q = s.q[t][4 * hf + j][lane];
-              mma16816<false>(hf ? s1[t] : sc[t], a0, a1, a2, a3, q.x, q.y);
+              mma16816<false>(hf ? s1[t] : sc[t], pa.x, pb.x, pa.y, pb.y, q.x, q.y);
             }
           }
         }
@@ -478,6 +463,12 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
           for (int j = 0; j < 4; ++j)
             sc[t][j] = (sc[t][j] + s1[t][j]) * (kf[j >> 1] * col[t][j & 1]);
       }
+      // V: bytes 16 g on of rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+      const uint8_t* av = rv + 2 * c * 128 + ((g ^ (2 * c)) << 4);
+      const uint8_t* bv = rv + (2 * c + 1) * 128 + ((g ^ (2 * c + 1)) << 4);
+      uint4 v[4] = {*reinterpret_cast<const uint4*>(av), *reinterpret_cast<const uint4*>(bv),
+                    *reinterpret_cast<const uint4*>(av + 1024),
+                    *reinterpret_cast<const uint4*>(bv + 1024)};
       if (!(sl.key & WHOLE)) {  // some row does not see some key
         const int k0 = sl.key & ~15, rows = cur.n * p.group;
         const Walk w(p, cur.n, cur.L, 0);
@@ -495,11 +486,21 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
               if (!sees) sc[t][i + 2 * j] = -INFINITY;
             }
           }
-        // (a block of 16 tokens or more that holds a seen key has a scale for it)
-        if (p.scale_shift == 0)
+        // keys that no row sees may hold anything, and 0 * NaN is NaN (a block of 16
+        // tokens or more that holds a seen key has a scale for it)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (!w.sees(k0 + 2 * c + (j & 1) + 8 * (j >> 1))) vb[j] = 127;
+        for (int j = 0; j < 4; ++j)
+          if (!w.sees(k0 + 2 * c + (j & 1) + 8 * (j >> 1))) {
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (!BF16 && p.scale_shift == 0) {
+              uint32_t& pair = j < 2 ? s01 : s23;
+              pair &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
+            }
+          }
+        if (BF16 && p.scale_shift == 0)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (!w.sees(k0 + g + 8 * j)) vf[j] = 0.f;
       }
       // ---- the running maximum: moved when a score exceeds it by more than 8
       bool moves = false;
@@ -528,29 +529,13 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
             }
           }
       }
-      // ---- probabilities as B fragments; for bf16 times V's scale, in units of
-      // 2^V_UNIT (a power of two each, so exactly)
-      float vf[2] = {1.f, 1.f};  // of this thread's scores' keys, g and g + 8
-      bool raw = true;           // V's codes are taken as moved bits, 2^120 too small
+      // ---- probabilities as B fragments; for bf16 times V's scale (a power of two, so
+      // exactly), in O's unit
       if (BF16) {
-        int lo = vb[0], hi = vb[0];
-        if (p.scale_shift == 0) {
-          // lane g / 2 of the quad has the bytes of keys g and g + 8
-          const int src = (lane & 28) | (g >> 1);
-          lo = __shfl_sync(0xffffffffu, vb[0] | vb[1] << 8, src);
-          hi = __shfl_sync(0xffffffffu, vb[2] | vb[3] << 8, src);
-          lo = (g & 1) ? lo >> 8 : lo & 255;
-          hi = (g & 1) ? hi >> 8 : hi & 255;
-        }
-        // probabilities are at most 2^8, so that times 2^112 they want exponents of
-        // at most 7
-        if (!I8) raw = !__any_sync(0xffffffffu, max(lo, hi) > 127 + 7);
-        vf[0] = scale_float<true>(lo) * V_UNIT<I8>;
-        vf[1] = scale_float<true>(hi) * V_UNIT<I8>;
-        if (!I8 && raw) {
-          vf[0] *= 0x1p120f;
-          vf[1] *= 0x1p120f;
-        }
+        // at most 2^8 each, so that times 2^112 they want exponents of at most 7
+        const float unit = V_UNIT<I8> * (!I8 && !big ? 0x1p120f : 1.f);
+        vf[0] *= unit;
+        vf[1] *= unit;
       }
       uint32_t pf[NT][2];
 #pragma unroll
@@ -568,49 +553,56 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
         pf[t][1] = transpose8x8(pack2<BF16>(e[2], e[3]));
       }
       // ---- O^T += V^T P^T
-      const uint4 v0 = from[32 * 4], v1 = from[32 * 5], v2 = from[32 * 6], v3 = from[32 * 7];
-      const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-      const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
-      uint32_t s01 = 0, s23 = 0;
-      if (!BF16) {
-        s01 = (scale_pair<BF16>(vb[0]) & 0xffffu) | (scale_pair<BF16>(vb[1]) << 16);
-        s23 = (scale_pair<BF16>(vb[2]) & 0xffffu) | (scale_pair<BF16>(vb[3]) << 16);
-      }
-      auto add_values = [&](auto&& pair) {
+      const uint32_t vw[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
+                                 {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
+      auto add_values = [&](auto bits) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int wd = k >> 1, by = 2 * (k & 1);
-          uint32_t a0 = pair(w0[wd], w1[wd], by, 4 + by);
-          uint32_t a1 = pair(w0[wd], w1[wd], by + 1, 5 + by);
-          uint32_t a2 = pair(w2[wd], w3[wd], by, 4 + by);
-          uint32_t a3 = pair(w2[wd], w3[wd], by + 1, 5 + by);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t lo[4], hi[4];
+          cross_pairs<BF16, I8, decltype(bits)::value>(vw[0][k], vw[1][k], lo);
+          cross_pairs<BF16, I8, decltype(bits)::value>(vw[2][k], vw[3][k], hi);
           if (!BF16) {
-            a0 = mul16x2<false>(a0, s01);
-            a1 = mul16x2<false>(a1, s01);
-            a2 = mul16x2<false>(a2, s23);
-            a3 = mul16x2<false>(a3, s23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              lo[j] = mul16x2<false>(lo[j], s01);
+              hi[j] = mul16x2<false>(hi[j], s23);
+            }
           }
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma16816<BF16>(acc[t][k], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+          for (int t = 0; t < NT; ++t) {
+            mma16816<BF16>(acc[t][2 * k], lo[0], lo[1], hi[0], hi[1], pf[t][0], pf[t][1]);
+            mma16816<BF16>(acc[t][2 * k + 1], lo[2], lo[3], hi[2], hi[3], pf[t][0], pf[t][1]);
+          }
         }
       };
-      auto exact_pair = [](uint32_t a, uint32_t b, int x, int y) {
-        return code_pair<BF16, I8>(a, b, x, y);
-      };
       if constexpr (BF16 && !I8) {
-        if (raw)
-          add_values([](uint32_t a, uint32_t b, int x, int y) { return code_bits(a, b, x, y); });
+        if (big)
+          add_values(std::false_type());
         else
-          add_values(exact_pair);
+          add_values(std::true_type());
       } else {
-        add_values(exact_pair);
+        add_values(std::false_type());
       }
-      __syncwarp();  // the scales' slot is read
+      __syncwarp();  // the stage is read
 #pragma unroll
       for (int j = 0; j < LAG; ++j) way[j] = way[j + 1];
       --on_way;
-      from_stage = from_stage + 1 == STAGES ? 0 : from_stage + 1;
+      if (++from_stage == STAGES) {
+        from_stage = 0;
+        from_ph ^= 1u;
+      }
+    }
+    if (!ok) {  // gives up: its copies in flight land first
+      for (; on_way > 0 && !p.test_no_loads; --on_way) {
+        mbar_drain_warp(smem_u32(&s.full[warp][from_stage]), from_ph, wc.timeout_ns);
+        if (++from_stage == STAGES) {
+          from_stage = 0;
+          from_ph ^= 1u;
+        }
+      }
+      on_way = 0;
+      more = false;
+      u_at = u_cnt;
     }
 
     // ---- the piece's end: the warps' shares meet, MERGE rows at a time
@@ -690,44 +682,36 @@ k_paged8_rows(const __grid_constant__ RowsParams p) {
     slot = next_slot;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    DevStatus st{};
-    st.code = s.bad_page ? (unsigned)ATTN_ERR_INVALID_ARG : 0u;
-    p.cta_status[blockIdx.x] = st;
-  }
+  if (threadIdx.x == 0 && s.bad_page) atomicCAS(&wc.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);
 }
 
 template <bool BF16, bool I8, int NT>
-cudaError_t launch_rows(const RowsParams& p, cudaStream_t st) {
+cudaError_t launch_rows(const Paged8Params& p, const CUtensorMap& tK, const CUtensorMap& tV,
+                        const void* q, cudaStream_t st) {
   using R = rows_side::Rows<NT>;
   const auto kern = k_paged8_rows<BF16, I8, NT>;
   constexpr int smem = (int)sizeof(typename R::Smem) + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)p.grid, R::THREADS, smem, st>>>(p);
+  kern<<<(unsigned)p.grid, R::THREADS, smem, st>>>(tK, tV, static_cast<const uint16_t*>(q), p);
   e = cudaGetLastError();
   return e == cudaSuccess ? launch_paged_join<BF16>(p, st) : e;
 }
 
 template <bool BF16, bool I8>
-cudaError_t launch_rows_of(int rows, const RowsParams& p, cudaStream_t st) {
-  return rows <= 8 ? launch_rows<BF16, I8, 1>(p, st) : launch_rows<BF16, I8, 2>(p, st);
+cudaError_t launch_rows_of(const Paged8Params& p, const CUtensorMap& tK, const CUtensorMap& tV,
+                           const void* q, cudaStream_t st) {
+  return p.tile_rows <= 8 ? launch_rows<BF16, I8, 1>(p, tK, tV, q, st)
+                          : launch_rows<BF16, I8, 2>(p, tK, tV, q, st);
 }
 
-cudaError_t launch_paged8_rows(bool bf16, bool i8, const Paged8Params& base, const void* q,
-                               const void* k_pages, const void* v_pages, long long page_stride,
-                               long long head_stride, long long token_stride, cudaStream_t st) {
-  RowsParams p;
-  static_cast<Paged8Params&>(p) = base;
-  p.q = static_cast<const uint16_t*>(q);
-  p.k_pages = static_cast<const uint8_t*>(k_pages);
-  p.v_pages = static_cast<const uint8_t*>(v_pages);
-  p.page_stride = page_stride;
-  p.head_stride = head_stride;
-  p.token_stride = token_stride;
-  const int rows = p.tile_rows;
-  if (i8) return bf16 ? launch_rows_of<true, true>(rows, p, st) : launch_rows_of<false, true>(rows, p, st);
-  return bf16 ? launch_rows_of<true, false>(rows, p, st) : launch_rows_of<false, false>(rows, p, st);
+cudaError_t launch_paged8_rows(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tK,
+                               const CUtensorMap& tV, const void* q, cudaStream_t st) {
+  if (i8)
+    return bf16 ? launch_rows_of<true, true>(p, tK, tV, q, st)
+                : launch_rows_of<false, true>(p, tK, tV, q, st);
+  return bf16 ? launch_rows_of<true, false>(p, tK, tV, q, st)
+              : launch_rows_of<false, false>(p, tK, tV, q, st);
 }
 
 }  // namespace mab

@@ -73,12 +73,12 @@ __device__ __forceinline__ uint2 rescale(uint2 c, int s0, int s1) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     float f[4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float2 x = unpack2<false>(code_pair<false, I8>(w[i], 0, 2 * j, 2 * j + 1));
-      f[2 * j] = x.x * unit;
-      f[2 * j + 1] = x.y * unit;
-    }
+    const uint2 v = word_pairs<false, I8>(w[i]);
+    const float2 x = unpack2<false>(v.x), y = unpack2<false>(v.y);
+    f[0] = x.x * unit;
+    f[1] = x.y * unit;
+    f[2] = y.x * unit;
+    f[3] = y.y * unit;
     r[i] = codes_of<I8>(f[0], f[1], f[2], f[3]);
   }
   return make_uint2(r[0], r[1]);

@@ -86,44 +86,84 @@ __device__ __forceinline__ uint32_t add16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// e4m3 codes `lo` and `hi` (bytes of a, b) as a pair of bf16 values times 2^-120:
-// sign, exponent and mantissa in their places.
-__device__ __forceinline__ uint32_t code_bits(uint32_t a, uint32_t b, int lo, int hi) {
-  // a byte at the head of each half, anything below it
-  const uint32_t h = __byte_perm(a, b, (uint32_t)(lo << 4 | hi << 12));
-  return ((h >> 4) & 0x07f007f0u) | (h & 0x80008000u);
-}
-
-// Codes `lo` and `hi` (bytes of the register pair a, b as __byte_perm counts
-// them) as a pair of 16-bit values, exactly.
+// Codes to 16-bit values, exactly.
 //   int8: the byte becomes the low bits of a number whose exponent makes its
 //     unit 1 (f16: 1024 + (c + 128); bf16, which has seven bits below the first:
 //     128 + the low seven), and what was added is taken off;
-//   e4m3 to f16: the conversion; to bf16: code_bits, times 2^120.
+//   e4m3 to f16: the conversion; to bf16: sign, exponent and mantissa moved to
+//     their places, which leaves the exponent 120 too small (BITS: left so).
+
+// The four codes of a word as pairs (0, 1) and (2, 3).
 template <bool BF16, bool I8>
-__device__ __forceinline__ uint32_t code_pair(uint32_t a, uint32_t b, int lo, int hi) {
+__device__ __forceinline__ uint2 word_pairs(uint32_t w) {
+  if (I8 && !BF16) {
+    const uint32_t u = w ^ 0x80808080u;
+    return make_uint2(add16x2<false>(__byte_perm(u, 0x64646464u, 0x4140), 0xe480e480u),
+                      add16x2<false>(__byte_perm(u, 0x64646464u, 0x4342), 0xe480e480u));
+  }
   if (I8) {
-    // a byte at the foot of each half, anything above it
-    const uint32_t u = __byte_perm(a, b, (uint32_t)(lo | hi << 8));
-    if (!BF16) return add16x2<false>((u & 0x00ff00ffu) ^ 0x64806480u, 0xe480e480u);  // - 1152
     // 128 + low bits, less 128, or 256 for a set sign
-    return add16x2<true>((u & 0x007f007fu) | 0x43004300u, (u & 0x00800080u) | 0xc300c300u);
+    const uint32_t a = __byte_perm(w, 0, 0x4140), b = __byte_perm(w, 0, 0x4342);
+    return make_uint2(add16x2<true>((a & 0x007f007fu) | 0x43004300u, (a & 0x00800080u) | 0xc300c300u),
+                      add16x2<true>((b & 0x007f007fu) | 0x43004300u, (b & 0x00800080u) | 0xc300c300u));
   }
   if (!BF16) {
-    uint32_t d;
-    const uint16_t two = (uint16_t)__byte_perm(a, b, (uint32_t)(lo | hi << 4));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(two));
+    uint2 d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(d.x), "=r"(d.y)
+        : "r"(w));
     return d;
   }
-  return mul16x2<true>(code_bits(a, b, lo, hi), 0x7b807b80u);  // 2^120
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+  return make_uint2(
+      mul16x2<true>(((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), 0x7b807b80u),  // 2^120
+      mul16x2<true>(((b >> 4) & 0x07f007f0u) | (b & 0x80008000u), 0x7b807b80u));
+}
+
+// The codes of words a and b as pairs (a's byte i, b's byte i).
+template <bool BF16, bool I8, bool BITS>
+__device__ __forceinline__ void cross_pairs(uint32_t a, uint32_t b, uint32_t (&d)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!I8 && !BF16) {
+      const uint2 v = word_pairs<false, false>(__byte_perm(a, b, i == 0 ? 0x5140 : 0x7362));
+      d[2 * i] = v.x;
+      d[2 * i + 1] = v.y;
+      continue;
+    }
+    // a's two bytes, b's two bytes: the first of each at the foot of its half
+    const uint32_t y = i == 0 ? __byte_perm(a, b, 0x5410) : __byte_perm(a, b, 0x7632);
+    if (I8 && !BF16) {
+      const uint32_t u = y ^ 0x80808080u;
+      d[2 * i] = add16x2<false>(__byte_perm(u, 0x64646464u, 0x4240), 0xe480e480u);
+      d[2 * i + 1] = add16x2<false>(__byte_perm(u, 0x64646464u, 0x4341), 0xe480e480u);
+    } else if (I8) {
+      const uint32_t z = y >> 8;
+      d[2 * i] = add16x2<true>((y & 0x007f007fu) | 0x43004300u, (y & 0x00800080u) | 0xc300c300u);
+      d[2 * i + 1] =
+          add16x2<true>((z & 0x007f007fu) | 0x43004300u, (z & 0x00800080u) | 0xc300c300u);
+    } else {
+      // byte << 4, its sign on from bit 11 to 15 (products, off the busier pipe); the
+      // other byte of the half comes down instead
+      uint32_t e = (y & 0x00ff00ffu) * 16u + (y & 0x00800080u) * 240u;
+      uint32_t o = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
+      if (!BITS) {
+        e = mul16x2<true>(e, 0x7b807b80u);  // 2^120
+        o = mul16x2<true>(o, 0x7b807b80u);
+      }
+      d[2 * i] = e;
+      d[2 * i + 1] = o;
+    }
+  }
 }
 
 // Four codes times their block's scale (a pair, scale_pair): exact for scales
 // that the store writes.
 template <bool BF16, bool I8>
 __device__ __forceinline__ uint2 values_of(uint32_t codes, uint32_t scale2) {
-  return make_uint2(mul16x2<BF16>(code_pair<BF16, I8>(codes, codes, 0, 1), scale2),
-                    mul16x2<BF16>(code_pair<BF16, I8>(codes, codes, 2, 3), scale2));
+  const uint2 v = word_pairs<BF16, I8>(codes);
+  return make_uint2(mul16x2<BF16>(v.x, scale2), mul16x2<BF16>(v.y, scale2));
 }
 
 // A scale byte as fp32 (the same numbers as scale_pair's).

@@ -312,9 +312,10 @@ def test_no_lse_and_other_stream(cuda_lib):
     assert torch.equal(out, o)
 
 
-def test_waits_that_run_out(cuda_lib, monkeypatch):
+@pytest.mark.parametrize("n", [1, 40])
+def test_waits_that_run_out(cuda_lib, n, monkeypatch):
     """The loader issues nothing: the call ends with a status."""
-    c = Case([(40, 500)])
+    c = Case([(n, 500)])
     monkeypatch.setenv("MASKATTN_TEST_NO_LOADS", "1")
     monkeypatch.setenv("MASKATTN_WAIT_TIMEOUT_NS", "20000000")
     _, status = c.run()
