@@ -80,24 +80,26 @@ constexpr int COL_O = 0;         // O accumulator of group g at COL_O + 128 g
 constexpr int COL_QA = 256;      // Q as the A operand, 64 columns of 16-bit pairs
 constexpr int COL_S = 320;       // S buffer b at COL_S + 64 b
 constexpr int SM_WARPS = 8;      // softmax warps, two groups of four
-constexpr int CV_WARPS = 4;      // converting warps
+constexpr int CV_WARPS = 8;      // converting warps, four for K and four for V
 constexpr float RESCALE_LOG2 = 8.f;  // M moves when a row maximum exceeds it by this
 constexpr unsigned LOAD_SLEEP_NS = 100;  // polling period of the loader's waits
 // Warps and rings of a form.
 template <int FORM>
 struct Cfg {
   static constexpr bool Q8 = FORM != ROWS16;
-  static constexpr int STAGES = Q8 ? 3 : 5;     // ring of 16-bit K / V tiles
-  static constexpr int LD_STAGES = 5;           // ring that the loads go to
+  static constexpr int STAGES = Q8 ? 4 : 5;     // ring of 16-bit K / V tiles
+  static constexpr int LD_STAGES = Q8 ? 3 : 5;  // ring that the loads go to
   static constexpr int SM_WARP0 = Q8 ? 4 : 3;   // first softmax warp
   static constexpr int CV_WARP0 = SM_WARP0 + SM_WARPS;
   static constexpr int NUM_THREADS = 32 * (CV_WARP0 + (Q8 ? CV_WARPS : 0));
-  static constexpr int AHEAD = LD_STAGES + 3;   // steps of a unit issued before the next one's Q
-  // registers of the warps that wait and copy, and of the softmax warps: 8 warps
-  // each, of 16 * 128
-  static constexpr int REGS_FEW = 72, REGS_SOFTMAX = 184;
+  static constexpr int AHEAD = 8;               // steps of a unit issued before the next one's Q
+  // registers of the warps that wait and convert (12), and of the softmax warps (8):
+  // of 20 * 96 that are launched
+  static constexpr int REGS_FEW = 56, REGS_SOFTMAX = 152;
 };
-static_assert(Cfg<CODES_I8>::REGS_FEW + Cfg<CODES_I8>::REGS_SOFTMAX == 2 * 128, "the launch's");
+static_assert(12 * Cfg<CODES_I8>::REGS_FEW + 8 * Cfg<CODES_I8>::REGS_SOFTMAX <= 20 * 96 &&
+                  Cfg<CODES_I8>::NUM_THREADS == 20 * 32,
+              "shares of the launch's registers");
 
 // The warps' shares of the line: cost and units.
 template <int NUM_THREADS>
@@ -115,12 +117,12 @@ struct Unit {
 };
 
 // What the converting warps add: the codes' ring (128B swizzle), and the scales
-// of each warp's 16 rows of 32 steps, two batches: [warp][batch][step][K, V][row].
+// of each warp's 16 rows of 32 steps, two batches: [warp][batch][step][row].
 template <int LD_STAGES>
 struct __align__(1024) Smem8 {
   uint8_t K8[LD_STAGES][Q_SUB * 128];
   uint8_t V8[LD_STAGES][Q_SUB * 128];
-  uint8_t scales[CV_WARPS][2][32][2][16];
+  uint8_t scales[CV_WARPS][2][32][16];
   uint64_t bar_ld_full[LD_STAGES];
   uint64_t bar_ld_empty[LD_STAGES];
 };
@@ -850,6 +852,14 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
             a0[2 * c] = x.x;
             a0[2 * c + 1] = x.y;
           }
+          if constexpr (Q8 && BF16) {  // back from the converted tiles' order of d
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float x = a0[4 * c + 1];
+              a0[4 * c + 1] = a0[4 * c + 2];
+              a0[4 * c + 2] = x;
+            }
+          }
           if (whole) {
             // through shared memory, so that a row's 128 bytes leave together
 #pragma unroll
@@ -916,6 +926,14 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
           w[4 * c + 1] = v.y;
           w[4 * c + 2] = v.z;
           w[4 * c + 3] = v.w;
+        }
+        if constexpr (Q8 && BF16) {  // the order of d in the converted tiles
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t a = w[2 * c], b = w[2 * c + 1];
+            w[2 * c] = __byte_perm(a, b, 0x5410);
+            w[2 * c + 1] = __byte_perm(a, b, 0x7632);
+          }
         }
         tmem_st32(lane_base + COL_QA + 32 * grp, w);
         tmem_wait_st();
@@ -1097,94 +1115,98 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   } else if constexpr (Q8) {
     // ------------------------------------------------------------ converting warps
     if (warp >= C::CV_WARP0) {
-      const int cw = warp - C::CV_WARP0;
+      constexpr bool I8 = FORM == CODES_I8;
+      const int cw = warp - C::CV_WARP0, slice = cw & 3;
+      const bool is_v = cw >= 4;
+      const uint8_t* all_scales = is_v ? p.v_scales : p.k_scales;
       // this thread's row of a step, and which half of it
-      const int srow = lane >> 1, row = 16 * cw + srow, half = lane & 1;
+      const int srow = lane >> 1, row = 16 * slice + srow, half = lane & 1;
       bool ok = true;
       Cyc<LD_STAGES> lg;
       Cyc<STAGES> rg;
       int m = 0;  // step counter across units
       for (int j = 0; ok; ++j) {
         if (!mbar_wait_warp(smem_u32(&s.bar_q_full), j & 1, wc, TAG_Q)) break;
-        const Unit un = s.unit;
-        if (un.N < 0) break;
+        const int N = s.unit.N, s0 = s.unit.s0, kvh = s.unit.kvh;
+        if (N < 0) break;
+        const Walk w(p, s.unit.n, s.unit.L, s.unit.tok0);
+        const int* table = p.table + (size_t)s.unit.b * p.table_stride;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
-        const Walk w(p, un.n, un.L, un.tok0);
-        const int* table = p.table + (size_t)un.b * p.table_stride;
-        const int end = un.s0 + un.N;
-        // Lane l looks up step i + l: the page of this warp's 16 rows there (-1
-        // where none of them is seen, or the page is not there), and their scales.
+        // Lane l looks up step i + l of the piece: the page of this warp's 16 rows
+        // there (-1 where none of them is seen, or the page is not there), and their
+        // scales.
         auto page_of = [&](int i) -> int {
-          const int k0 = w.tile(i + lane) * Q_SUB + 16 * cw;
-          if (i + lane >= end || !w.any(k0, k0 + 16)) return -1;
+          const int k0 = w.tile(s0 + i + lane) * Q_SUB + 16 * slice;
+          if (i + lane >= N || !w.any(k0, k0 + 16)) return -1;
           const int pg = __ldg(table + div_by(k0, p.page_size, p.inv_page_size));
           return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
         };
-        uint4 ksc, vsc;  // 16 bytes each
-        auto scales_of = [&](int i, int pg) {
-          ksc = vsc = make_uint4(0u, 0u, 0u, 0u);
-          if (pg < 0) return;
-          const int k0 = w.tile(i + lane) * Q_SUB + 16 * cw;
+        auto scales_of = [&](int i, int pg) -> uint4 {
+          if (pg < 0) return make_uint4(0u, 0u, 0u, 0u);
+          const int k0 = w.tile(s0 + i + lane) * Q_SUB + 16 * slice;
           const int r = k0 - div_by(k0, p.page_size, p.inv_page_size) * p.page_size;
-          const long long at = pg * p.scale_page_stride + un.kvh * p.scale_head_stride +
+          const long long at = pg * p.scale_page_stride + kvh * p.scale_head_stride +
                                (r >> p.scale_shift);
-          if (p.scale_shift == 0) {
-            ksc = __ldg(reinterpret_cast<const uint4*>(p.k_scales + at));
-            vsc = __ldg(reinterpret_cast<const uint4*>(p.v_scales + at));
-          } else {
-            const uint32_t a = __ldg(p.k_scales + at) * 0x01010101u;
-            const uint32_t b = __ldg(p.v_scales + at) * 0x01010101u;
-            ksc = make_uint4(a, a, a, a);
-            vsc = make_uint4(b, b, b, b);
-          }
+          if (p.scale_shift == 0) return __ldg(reinterpret_cast<const uint4*>(all_scales + at));
+          const uint32_t a = __ldg(all_scales + at) * 0x01010101u;
+          return make_uint4(a, a, a, a);
         };
-        auto keep_scales = [&](int batch) {
-          uint4* to = reinterpret_cast<uint4*>(s.scales[cw][batch & 1][lane][0]);
-          to[0] = ksc;
-          to[1] = vsc;
-          __syncwarp();
-        };
-        scales_of(un.s0, page_of(un.s0));
-        int page = page_of(un.s0 + 32);
-        for (int i = un.s0; ok && i < end; ++i, ++m, lg.next(), rg.next()) {
-          const int at = i - un.s0;
-          if ((at & 31) == 0) {
+        uint4 sc = scales_of(0, page_of(0));
+        int page = page_of(32);
+        for (int i = 0; ok && i < N; ++i, ++m, lg.next(), rg.next()) {
+          if ((i & 31) == 0) {
             __syncwarp();  // the batch before the last is read
-            keep_scales(at >> 5);
-            scales_of(i + 32, page);  // a batch ahead
+            *reinterpret_cast<uint4*>(s.scales[cw][(i >> 5) & 1][lane]) = sc;
+            __syncwarp();
+            sc = scales_of(i + 32, page);  // a batch ahead
             page = page_of(i + 64);
           }
+          const int sb = s.scales[cw][(i >> 5) & 1][i & 31][srow];
+          const bool seen = w.sees(w.tile(s0 + i) * Q_SUB + row);
+          // e4m3 to bf16: one product while every exponent is at most 7
+          const bool small = BF16 && !I8 && !__any_sync(0xffffffffu, seen && sb > 127 + 7);
+          const uint32_t scale2 =
+              small ? scale_pair<BF16>(sb == SCALE_NAN ? sb : min(max(sb, 1) + 120, 254))
+                    : scale_pair<BF16>(sb);
           ok = mbar_wait_warp(smem_u32(&s.bar_ld_full[lg.i]), lg.ph, wc, TAG_LD_FULL);
           if (ok && m >= STAGES)
             ok = mbar_wait_warp(smem_u32(&s.bar_kv_empty[rg.i]), rg.ph ^ 1u, wc, TAG_KV_EMPTY);
           if (!ok) break;
-          const bool seen = w.sees(w.tile(i) * Q_SUB + row);
-          const uint8_t* sc = &s.scales[cw][(at >> 5) & 1][at & 31][0][srow];
-          const uint32_t ks2 = scale_pair<BF16>(sc[0]), vs2 = scale_pair<BF16>(sc[16]);
-          auto convert = [&](const uint8_t* codes, uint8_t* tile, uint32_t scale2) {
-            // 16-byte units: 4 half + c of the code row become 2 c and 2 c + 1 of
-            // the half's 128-byte row, both swizzled by the row; the halves take
-            // them in orders that keep them off each other's banks
+          const uint8_t* from = (is_v ? s.V8[lg.i] : s.K8[lg.i]) + row * 128;
+          uint8_t* to = (is_v ? s.V[rg.i] : s.K[rg.i]) + half * (Q_SUB * 128) + row * 128;
+          auto convert = [&](auto one) {
+            constexpr bool SMALL = decltype(one)::value;
+            // 16-byte units: 4 half + c of the code row become 2 c and 2 c + 1 of the
+            // half's 128-byte row, both swizzled by the row; the halves take them in
+            // orders that keep them off each other's banks
+            uint4 v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              v[c] = *reinterpret_cast<const uint4*>(
+                  from + (((4 * half + (c ^ (half << 1))) ^ (row & 7)) << 4));
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
               const int c = cc ^ (half << 1);
-              uint4 v = *reinterpret_cast<const uint4*>(
-                  codes + row * 128 + (((4 * half + c) ^ (row & 7)) << 4));
-              uint2 a = values_of<BF16, FORM == CODES_I8>(v.x, scale2);
-              uint2 b = values_of<BF16, FORM == CODES_I8>(v.y, scale2);
-              uint2 d = values_of<BF16, FORM == CODES_I8>(v.z, scale2);
-              uint2 e = values_of<BF16, FORM == CODES_I8>(v.w, scale2);
+              uint2 a = tile_words<BF16, I8, SMALL>(v[cc].x, scale2);
+              uint2 b = tile_words<BF16, I8, SMALL>(v[cc].y, scale2);
+              uint2 d = tile_words<BF16, I8, SMALL>(v[cc].z, scale2);
+              uint2 e = tile_words<BF16, I8, SMALL>(v[cc].w, scale2);
               if (!seen) a = b = d = e = make_uint2(0u, 0u);
-              uint8_t* to = tile + half * (Q_SUB * 128) + row * 128;
               *reinterpret_cast<uint4*>(to + (((2 * c) ^ (row & 7)) << 4)) =
                   make_uint4(a.x, a.y, b.x, b.y);
               *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ (row & 7)) << 4)) =
                   make_uint4(d.x, d.y, e.x, e.y);
             }
           };
-          convert(s.K8[lg.i], s.K[rg.i], ks2);
-          convert(s.V8[lg.i], s.V[rg.i], vs2);
+          if constexpr (BF16 && !I8) {
+            if (small)
+              convert(std::true_type());
+            else
+              convert(std::false_type());
+          } else {
+            convert(std::false_type());
+          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {

@@ -158,6 +158,30 @@ __device__ __forceinline__ void cross_pairs(uint32_t a, uint32_t b, uint32_t (&d
   }
 }
 
+// The four codes of a word times a scale pair, for the matrix unit's tiles: as pairs
+// (0, 1), (2, 3) for f16, and (0, 2), (1, 3) for bf16, which spares putting bytes
+// together that lie apart.  SMALL: the scale pair is 2^120 times the scale (whose
+// exponent is at most 7), so that e4m3's moved bits need one product.
+template <bool BF16, bool I8, bool SMALL>
+__device__ __forceinline__ uint2 tile_words(uint32_t w, uint32_t scale2) {
+  uint2 v;
+  if (!BF16) {
+    v = word_pairs<false, I8>(w);
+  } else if (I8) {
+    const uint32_t z = w >> 8;
+    v.x = add16x2<true>((w & 0x007f007fu) | 0x43004300u, (w & 0x00800080u) | 0xc300c300u);
+    v.y = add16x2<true>((z & 0x007f007fu) | 0x43004300u, (z & 0x00800080u) | 0xc300c300u);
+  } else {
+    v.x = (w & 0x00ff00ffu) * 16u + (w & 0x00800080u) * 240u;
+    v.y = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+    if (!SMALL) {
+      v.x = mul16x2<true>(v.x, 0x7b807b80u);  // 2^120
+      v.y = mul16x2<true>(v.y, 0x7b807b80u);
+    }
+  }
+  return make_uint2(mul16x2<BF16>(v.x, scale2), mul16x2<BF16>(v.y, scale2));
+}
+
 // Four codes times their block's scale (a pair, scale_pair): exact for scales
 // that the store writes.
 template <bool BF16, bool I8>
