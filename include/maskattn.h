@@ -424,9 +424,11 @@ attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, con
                                const uint8_t* k_scales, const uint8_t* v_scales, void* k, void* v,
                                void* stream);
 
+/* Workspace bytes of attn_paged8_fwd, as attn_paged_workspace_size. */
+attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, size_t* bytes);
+
 /* attn_paged_fwd over an 8-bit cache: the attention over the values that the codes
- * and scales stand for, exactly (attn_paged8_load gives the same ones).  Workspace of
- * attn_paged_workspace_size; masks, lengths, results and statuses as attn_paged_fwd
+ * and scales stand for, exactly (attn_paged8_load gives the same ones); masks, lengths, results and statuses as attn_paged_fwd
  * has them.  A block whose scale is 255 reads as NaN, which a new token must not see,
  * as it must not see other values that are not finite. */
 attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pages, const void* q,

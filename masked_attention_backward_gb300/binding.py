@@ -28,7 +28,7 @@ EXPORTS = ("attn_workspace_size", "attn_fwd", "attn_bwd", "attn_bwd_noalloc",
            "attn_get_device_status", "attn_noalloc_get_device_status", "attn_profile_enable",
            "attn_profile_read", "attn_status_string", "attn_paged_plan", "attn_paged_store",
            "attn_paged_workspace_size", "attn_paged_fwd", "attn_rope", "attn_paged8_store",
-           "attn_paged8_load", "attn_paged8_fwd")
+           "attn_paged8_load", "attn_paged8_workspace_size", "attn_paged8_fwd")
 
 
 class attn_shape_t(ctypes.Structure):
@@ -146,6 +146,8 @@ def load(build: bool = True) -> ctypes.CDLL:
                                              ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp,
                                              vp]
             lib.attn_paged8_load.restype = ctypes.c_int
+            lib.attn_paged8_workspace_size.argtypes = [ps, ctypes.POINTER(sz)]
+            lib.attn_paged8_workspace_size.restype = ctypes.c_int
             lib.attn_paged8_fwd.argtypes = [ps, p8, vp, vp, vp, vp, vp, vp, ctypes.c_int,
                                             ctypes.c_int, vp, pm, ctypes.c_float, vp, vp, vp, sz,
                                             vp]
@@ -582,6 +584,12 @@ def attn_paged8_load(pages: attn_pages8_t, B, total, start, cu_seqlens, block_ta
                                    k, v, stream)
 
 
+def attn_paged8_workspace_size(shape: attn_shape_t):
+    n = ctypes.c_size_t(0)
+    r = load().attn_paged8_workspace_size(ctypes.byref(shape), ctypes.byref(n))
+    return r, n.value
+
+
 def attn_paged8_fwd(shape, pages: attn_pages8_t, q, k_pages, v_pages, k_scales, v_scales,
                     block_table, table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes,
                     stream) -> int:
@@ -834,9 +842,12 @@ def paged_shape(q: torch.Tensor, cache, mask: Mask) -> attn_shape_t:
 
 def paged_workspace(q: torch.Tensor, cache, mask: Mask,
                     shape: Optional[attn_shape_t] = None) -> torch.Tensor:
-    r, n = attn_paged_workspace_size(shape or paged_shape(q, cache, mask))
+    call, name = (attn_paged8_workspace_size, "attn_paged8_workspace_size") \
+        if isinstance(cache, PagedCache8) else \
+        (attn_paged_workspace_size, "attn_paged_workspace_size")
+    r, n = call(shape or paged_shape(q, cache, mask))
     if r != ATTN_OK:
-        raise AttnError(r, "attn_paged_workspace_size")
+        raise AttnError(r, name)
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 

@@ -63,10 +63,11 @@ struct PagedLayout {
   int tile_tokens, tile_rows, slot_floats;
 };
 
-PagedLayout paged_layout(const attn_shape_t* sh) {
+// tile: rows of a query tile at most.
+PagedLayout paged_layout(const attn_shape_t* sh, int tile) {
   PagedLayout L;
   const int group = sh->Hq / sh->Hkv;
-  L.tile_tokens = Q_TILE / group < sh->Sq ? Q_TILE / group : sh->Sq;
+  L.tile_tokens = tile / group < sh->Sq ? tile / group : sh->Sq;
   L.tile_rows = L.tile_tokens * group;
   L.slot_floats = (L.tile_rows + 31) / 32 * 2 * PAGED_WARP_FLOATS;
   size_t off = 0;
@@ -88,6 +89,10 @@ attn_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : A
 
 namespace mab {
 
+size_t paged_workspace(const attn_shape_t* shape, int tile) {
+  return paged_layout(shape, tile).total;
+}
+
 // What the attentions over 16-bit and 8-bit pages share: the checks behind those
 // of shape and pages, the parameters, and the map of q.  *work is false when no
 // token is new anywhere: then the call is done.
@@ -95,8 +100,8 @@ attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size
                          const void* k_pages, const void* v_pages, const int* block_table,
                          int table_stride, int max_pages, const float* sink,
                          const attn_mask_desc_t* mask, float scale, void* o, float* lse, void* ws,
-                         size_t ws_bytes, cudaStream_t st, PagedParams* out, CUtensorMap* tQ,
-                         bool* work) {
+                         size_t ws_bytes, cudaStream_t st, int tile, PagedParams* out,
+                         CUtensorMap* tQ, bool* work) {
   if (!mask || !(scale > 0.f) || !isfinite(scale) || max_pages < 1 || table_stride < max_pages ||
       slots_of(max_pages, page_size) < 0)
     return ATTN_ERR_INVALID_ARG;
@@ -127,7 +132,7 @@ attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size
       !aligned(mask->cu_seqlens_q, 4) || !aligned(mask->seqlen_k, 4) || mask->total_q < 0)
     return ATTN_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return ATTN_ERR_INVALID_ARG;
-  const PagedLayout L = paged_layout(shape);
+  const PagedLayout L = paged_layout(shape, tile);
   if (ws_bytes < L.total) return ATTN_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(ws);
   *work = false;
@@ -221,7 +226,7 @@ attn_status_t attn_paged_workspace_size(const attn_shape_t* shape, size_t* bytes
   if (!bytes) return ATTN_ERR_INVALID_ARG;
   const attn_status_t r = check_paged_shape(shape);
   if (r != ATTN_OK) return r;
-  *bytes = paged_layout(shape).total;
+  *bytes = paged_workspace(shape, Q_TILE);
   return ATTN_OK;
 }
 
@@ -239,8 +244,8 @@ attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* page
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   bool work = false;
   r = paged_call(shape, pages->num_pages, pages->page_size, q, k_pages, v_pages, block_table,
-                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st, &p, &tQ,
-                 &work);
+                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st, Q_TILE,
+                 &p, &tQ, &work);
   if (r != ATTN_OK || !work) return r;
   const bool bf16 = shape->dtype == ATTN_BF16;
   auto pages_map = [&](CUtensorMap* m, const void* base) {

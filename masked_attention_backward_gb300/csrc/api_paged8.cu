@@ -95,6 +95,14 @@ attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, con
                                         static_cast<cudaStream_t>(stream)));
 }
 
+attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, size_t* bytes) {
+  if (!bytes) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t r = check_paged_shape(shape);
+  if (r != ATTN_OK) return r;
+  *bytes = paged_workspace(shape, PAGED8_TILE);
+  return ATTN_OK;
+}
+
 attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pages, const void* q,
                               const void* k_pages, const void* v_pages, const uint8_t* k_scales,
                               const uint8_t* v_scales, const int* block_table, int table_stride,
@@ -111,8 +119,8 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   bool work = false;
   r = paged_call(shape, pages->num_pages, pages->page_size, q, k_pages, v_pages, block_table,
-                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st, &p, &tQ,
-                 &work);
+                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st,
+                 PAGED8_TILE, &p, &tQ, &work);
   if (r != ATTN_OK || !work) return r;
   r = check_buffers8(pages, k_pages, v_pages, k_scales, v_scales);
   if (r != ATTN_OK) return r;
@@ -129,7 +137,7 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   };
   if (!pages_map(&tK, k_pages) || !pages_map(&tV, v_pages)) return ATTN_ERR_CUDA;
   return cuda_status(few ? launch_paged8_rows(bf16, i8, p, tK, tV, q, st)
-                         : launch_paged8_fwd(bf16, i8, p, tQ, tK, tV, st));
+                         : launch_paged8_chunk(bf16, i8, p, tQ, tK, tV, st));
 }
 
 }  // extern "C"

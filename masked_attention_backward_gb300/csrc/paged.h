@@ -68,8 +68,9 @@ attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size
                          const void* k_pages, const void* v_pages, const int* block_table,
                          int table_stride, int max_pages, const float* sink,
                          const attn_mask_desc_t* mask, float scale, void* o, float* lse, void* ws,
-                         size_t ws_bytes, cudaStream_t st, PagedParams* out, CUtensorMap* tQ,
-                         bool* work);
+                         size_t ws_bytes, cudaStream_t st, int tile, PagedParams* out,
+                         CUtensorMap* tQ, bool* work);
+size_t paged_workspace(const attn_shape_t* shape, int tile);
 
 cudaError_t launch_paged_plan(const attn_plan_t& p, cudaStream_t st);
 cudaError_t launch_paged_store(const attn_pages_t& pg, int T, const void* k, const void* v,
@@ -77,10 +78,12 @@ cudaError_t launch_paged_store(const attn_pages_t& pg, int T, const void* k, con
                                void* k_pages, void* v_pages, cudaStream_t st);
 cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap& tQ,
                              const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
-cudaError_t launch_paged8_fwd(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tQ,
-                              const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
-// ... for calls of at most PAGED8_ROWS rows (tokens times query heads of a kv head).
+// Query rows (tokens times query heads of a kv head) of a call over 8-bit codes up to
+// which they go through k_paged8_rows, and of a tile of k_paged8_chunk.
 constexpr int PAGED8_ROWS = 16;
+constexpr int PAGED8_TILE = 256;
+cudaError_t launch_paged8_chunk(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tQ,
+                                const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
 cudaError_t launch_paged8_rows(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tK,
                                const CUtensorMap& tV, const void* q, cudaStream_t st);
 

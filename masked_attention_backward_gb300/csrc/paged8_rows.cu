@@ -1,6 +1,6 @@
 // paged8_rows.cu -- attention of a few new tokens over an 8-bit paged cache.
 //
-// The same operation, work line, cuts and join as paged_fwd.cuh, for calls whose
+// The same operation, work line, cuts and join as paged_fwd.cu, for calls whose
 // tokens and query heads of a kv head make few rows (single tokens, a few
 // speculated ones).  Bound: HBM, 256 bytes a key and kv head.  At the copy rate an
 // SM gets 23 codes a cycle, and the way through shared memory that the matrix
@@ -19,7 +19,10 @@
 // Warps share nothing while they walk a unit's keys, 16 at a time each in turn:
 // each brings its own slices into a ring of its own.  At a piece's end the warps'
 // O, M and l meet in shared memory.
-#include "paged_fwd.cuh"
+#include <type_traits>
+
+#include "paged_line.cuh"
+#include "quant8.cuh"
 
 namespace mab {
 
