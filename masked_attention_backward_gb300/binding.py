@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import threading
 from dataclasses import dataclass
@@ -99,6 +100,8 @@ _lib = None
 def load(build: bool = True) -> ctypes.CDLL:
     """Load libmaskattn.so (building it first when sources are newer)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build() if build else _build.LIB
@@ -215,6 +218,14 @@ def attn_profile_read(capacity: int = 16):
 
 # ------------------------------------------------------------- torch helpers
 
+def _ints_ptr(t: Optional[torch.Tensor], name: str):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor")
+    return t.data_ptr()
+
+
 @dataclass
 class Mask:
     kind: int = ATTN_MASK_NONE
@@ -243,18 +254,13 @@ class Mask:
                 self.cu_seqlens_k)
 
     def desc(self) -> attn_mask_desc_t:
-        def ptr(t, name):
-            if t is None:
-                return None
-            if t.dtype != torch.int32 or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous int32 tensor")
-            return t.data_ptr()
         bm = self.block_mask
         return attn_mask_desc_t(self.kind, self.window, self.bx, self.by,
                                 None if bm is None else bm.data_ptr(),
-                                ptr(self.seqlen_q, "seqlen_q"), ptr(self.seqlen_k, "seqlen_k"),
-                                ptr(self.cu_seqlens_q, "cu_seqlens_q"),
-                                ptr(self.cu_seqlens_k, "cu_seqlens_k"), self.total_q,
+                                _ints_ptr(self.seqlen_q, "seqlen_q"),
+                                _ints_ptr(self.seqlen_k, "seqlen_k"),
+                                _ints_ptr(self.cu_seqlens_q, "cu_seqlens_q"),
+                                _ints_ptr(self.cu_seqlens_k, "cu_seqlens_k"), self.total_q,
                                 self.total_k, self.first)
 
 
@@ -506,25 +512,27 @@ def rope(rp: Rope, q, k=None, position=None, out=None, stream=None, inverse: boo
     every sequence).  Rows at a negative position are not written.  out: (q, k) to
     write, which may be the inputs themselves; without it they are contiguous and
     belong to `stream`, as fwd's results do."""
-    if q.dim() not in (3, 4) or q.shape[-1] != 128 or q.stride(-1) != 1:
+    qs, xs = tuple(q.shape), q.stride()
+    rows = len(qs) == 3
+    if not (rows or len(qs) == 4) or qs[-1] != 128 or xs[-1] != 1:
         raise ValueError("q must be [T, heads, 128] or [B, heads, S, 128], its last stride 1")
-    at = 0 if q.dim() == 3 else 2
-    S, B = q.shape[at], 1 if q.dim() == 3 else q.shape[0]
+    S, B = (qs[0], 1) if rows else (qs[2], qs[0])
     code = _dtype_code(q)
-    if k is not None and (k.dim() != q.dim() or k.shape[at] != S or k.shape[-1] != 128 or
-                          k.stride(-1) != 1 or k.dtype != q.dtype or
-                          (q.dim() == 4 and k.shape[0] != B)):
-        raise ValueError("k must have q's type, layout and tokens")
+    if k is not None:
+        ks = tuple(k.shape)
+        if ks[:1] + ks[2:] != qs[:1] + qs[2:] or k.stride(-1) != 1 or k.dtype != q.dtype:
+            raise ValueError("k must have q's type, layout and tokens")
     p_stride = 0
     if position is not None:
+        shape = tuple(position.shape)
         if position.dtype != torch.int32 or not position.is_contiguous() or \
-                tuple(position.shape) not in ([(S,)] if q.dim() == 3 else [(S,), (B, S)]):
+                not (shape == (S,) or (shape == (B, S) and not rows)):
             raise ValueError("position must be a contiguous int32 tensor, one a token")
-        p_stride = S if position.dim() == 2 else 0
+        p_stride = S if len(shape) == 2 else 0
     if out is None:
         with _alloc_on(stream):
-            y = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            z = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            y = torch.empty(qs, dtype=q.dtype, device=q.device)
+            z = None if k is None else torch.empty(ks, dtype=q.dtype, device=q.device)
     else:
         y, z = out
         for o, x, n in ((y, q, "q"), (z, k, "k")):
@@ -595,8 +603,7 @@ def attn_paged8_fwd(shape, pages: attn_pages8_t, q, k_pages, v_pages, k_scales, 
                     stream) -> int:
     return load().attn_paged8_fwd(ctypes.byref(shape), ctypes.byref(pages), q, k_pages, v_pages,
                                   k_scales, v_scales, block_table, table_stride, max_pages, sink,
-                                  ctypes.byref(mask), ctypes.c_float(scale), o, lse, ws, ws_bytes,
-                                  stream)
+                                  ctypes.byref(mask), scale, o, lse, ws, ws_bytes, stream)
 
 
 def _one_device(*tensors):
@@ -642,6 +649,19 @@ class PagedCache:
         return self.k_pages.data_ptr(), self.v_pages.data_ptr()
 
 
+_CODES = {torch.float8_e4m3fn: ATTN_E4M3, torch.int8: ATTN_I8}
+
+
+def _strides(a: torch.Tensor, b: torch.Tensor, shape, one: int):
+    """Strides that a and b share, `one` for dimensions of one element, which may
+    have any; None where they differ."""
+    s, t = a.stride(), b.stride()
+    if s == t and 1 not in shape:
+        return s
+    s = [one if n == 1 else m for n, m in zip(shape, s)]
+    return s if s == [one if n == 1 else m for n, m in zip(shape, t)] else None
+
+
 class PagedCache8:
     """The pages of a key/value cache held in 8 bits: k_pages and v_pages as in
     PagedCache but of torch.float8_e4m3fn or torch.int8, and k_scales and
@@ -654,35 +674,34 @@ class PagedCache8:
                  layout: str = "HND"):
         if layout not in ("HND", "NHD"):
             raise ValueError(f"unknown layout {layout!r}")
-        shape = k_pages.shape
-        if len(shape) != 4 or shape[3] != 128 or v_pages.shape != shape:
+        shape = tuple(k_pages.shape)
+        if len(shape) != 4 or shape[3] != 128 or tuple(v_pages.shape) != shape:
             raise ValueError("k_pages and v_pages must be [pages, ., ., 128] of one shape")
-        code = {torch.float8_e4m3fn: ATTN_E4M3, torch.int8: ATTN_I8}.get(k_pages.dtype)
+        code = _CODES.get(k_pages.dtype)
         if code is None:
             raise TypeError(f"unsupported type of codes {k_pages.dtype}")
-        if v_pages.dtype != k_pages.dtype or \
-                len({t.device for t in (k_pages, v_pages, k_scales, v_scales)}) != 1:
+        if v_pages.dtype != k_pages.dtype or not (
+                k_pages.get_device() == v_pages.get_device() == k_scales.get_device() ==
+                v_scales.get_device()):
             raise ValueError("k_pages and v_pages must have one type, all tensors one device")
         hd, td = (1, 2) if layout == "HND" else (2, 1)
         P, Hkv, ps = shape[0], shape[hd], shape[td]
         per = k_scales.shape[2] if k_scales.dim() == 3 else 0
-        for t in (k_scales, v_scales):
-            if t.dtype != torch.uint8 or per < 1 or ps % per or tuple(t.shape) != (P, Hkv, per):
-                raise ValueError("the scales must be uint8 [pages, Hkv, page_size // block]")
-        # a dimension of one element may have any stride
-        ks, vs = ([128 if n == 1 else m for n, m in zip(shape, t.stride())]
-                  for t in (k_pages, v_pages))
-        if ks != vs or ks[3] != 1:
+        if per < 1 or ps % per or k_scales.dtype != torch.uint8 or \
+                v_scales.dtype != torch.uint8 or tuple(k_scales.shape) != (P, Hkv, per) or \
+                tuple(v_scales.shape) != (P, Hkv, per):
+            raise ValueError("the scales must be uint8 [pages, Hkv, page_size // block]")
+        ks = _strides(k_pages, v_pages, shape, 128)
+        if ks is None or ks[3] != 1:
             raise ValueError("k_pages and v_pages must have the same strides, 1 for the last")
-        kss, vss = ([per if n == 1 else m for n, m in zip((P, Hkv), t.stride())] +
-                    [1 if per == 1 else t.stride(2)] for t in (k_scales, v_scales))
-        if kss != vss or kss[2] != 1:
+        ss = _strides(k_scales, v_scales, (P, Hkv, per), per)
+        if ss is None or (per > 1 and ss[2] != 1):
             raise ValueError("k_scales and v_scales must have the same strides, 1 for the last")
         self.k_pages, self.v_pages, self.layout, self.dtype = k_pages, v_pages, layout, dtype
         self.k_scales, self.v_scales = k_scales, v_scales
         self.num_pages, self.Hkv, self.page_size, self.block = P, Hkv, ps, ps // per
         self.desc = attn_pages8_t(P, ps, Hkv, _code_of(dtype), code, self.block, ks[0], ks[hd],
-                                  ks[td], kss[0], kss[1])
+                                  ks[td], ss[0], ss[1])
 
     @staticmethod
     def empty(num_pages: int, Hkv: int, page_size: int, block: int = 16,
@@ -840,14 +859,21 @@ def paged_shape(q: torch.Tensor, cache, mask: Mask) -> attn_shape_t:
                         mask.max_seqlen_k, q.shape[2], _dtype_code(q), 0)
 
 
-def paged_workspace(q: torch.Tensor, cache, mask: Mask,
-                    shape: Optional[attn_shape_t] = None) -> torch.Tensor:
-    call, name = (attn_paged8_workspace_size, "attn_paged8_workspace_size") \
-        if isinstance(cache, PagedCache8) else \
+@functools.lru_cache(maxsize=256)
+def _paged_workspace_bytes(eight: bool, *shape) -> int:
+    call, name = (attn_paged8_workspace_size, "attn_paged8_workspace_size") if eight else \
         (attn_paged_workspace_size, "attn_paged_workspace_size")
-    r, n = call(shape or paged_shape(q, cache, mask))
+    r, n = call(attn_shape_t(*shape, 0))
     if r != ATTN_OK:
         raise AttnError(r, name)
+    return n
+
+
+def paged_workspace(q: torch.Tensor, cache, mask: Mask,
+                    shape: Optional[attn_shape_t] = None) -> torch.Tensor:
+    sh = shape or paged_shape(q, cache, mask)
+    n = _paged_workspace_bytes(isinstance(cache, PagedCache8), sh.B, sh.Hq, sh.Hkv, sh.Sq, sh.Skv,
+                               sh.D, sh.dtype)
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 

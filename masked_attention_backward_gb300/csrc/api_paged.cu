@@ -94,8 +94,8 @@ size_t paged_workspace(const attn_shape_t* shape, int tile) {
 }
 
 // What the attentions over 16-bit and 8-bit pages share: the checks behind those
-// of shape and pages, the parameters, and the map of q.  *work is false when no
-// token is new anywhere: then the call is done.
+// of shape and pages, the parameters, and the map of q where it is wanted.  *work is
+// false when no token is new anywhere: then the call is done.
 attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size, const void* q,
                          const void* k_pages, const void* v_pages, const int* block_table,
                          int table_stride, int max_pages, const float* sink,
@@ -176,8 +176,8 @@ attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
   p.grid = sms < PAGED_MAX_CTAS ? sms : PAGED_MAX_CTAS;
-  if (!make_rows_map(tQ, q, shape->dtype == ATTN_BF16, p.total_q, p.Hq, (uint32_t)p.group,
-                     (uint32_t)p.tile_tokens))
+  if (tQ && !make_rows_map(tQ, q, shape->dtype == ATTN_BF16, p.total_q, p.Hq, (uint32_t)p.group,
+                           (uint32_t)p.tile_tokens))
     return ATTN_ERR_CUDA;
   *work = true;
   return ATTN_OK;

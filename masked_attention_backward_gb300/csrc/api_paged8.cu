@@ -117,10 +117,12 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   Paged8Params p;
   CUtensorMap tQ, tK, tV;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // few rows (as tile_rows will have it): a kernel that reads q's rows itself
+  const bool few = (long long)shape->Sq * (shape->Hq / shape->Hkv) <= PAGED8_ROWS;
   bool work = false;
   r = paged_call(shape, pages->num_pages, pages->page_size, q, k_pages, v_pages, block_table,
                  table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st,
-                 PAGED8_TILE, &p, &tQ, &work);
+                 PAGED8_TILE, &p, few ? nullptr : &tQ, &work);
   if (r != ATTN_OK || !work) return r;
   r = check_buffers8(pages, k_pages, v_pages, k_scales, v_scales);
   if (r != ATTN_OK) return r;
@@ -130,7 +132,6 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   p.scale_head_stride = pg.scale_head_stride;
   p.scale_shift = pg.shift;
   const bool bf16 = shape->dtype == ATTN_BF16, i8 = pages->code == ATTN_I8;
-  const bool few = p.tile_rows <= PAGED8_ROWS;
   auto pages_map = [&](CUtensorMap* m, const void* base) {
     return make_pages8_map(m, base, pg.num_pages, pg.page_size, pg.Hkv, pg.page_stride,
                            pg.head_stride, pg.token_stride, few ? 16u : (uint32_t)p.box_rows);
