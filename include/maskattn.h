@@ -424,8 +424,15 @@ attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, con
                                const uint8_t* k_scales, const uint8_t* v_scales, void* k, void* v,
                                void* stream);
 
-/* Workspace bytes of attn_paged8_fwd, as attn_paged_workspace_size. */
-attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, size_t* bytes);
+/* Workspace bytes of attn_paged8_fwd: the least for mask = NULL, as
+ * attn_paged_workspace_size; with the call's mask (of which kind, window, first and
+ * total_q are read) with room besides for the rows that chunks see, in 16 bits: 512
+ * bytes for each key (up to Skv, or those of the window) of each kv head and request
+ * that may have a chunk.  With that much attn_paged8_fwd writes them there once, where
+ * with less every query tile makes them anew: chunks of 1900 tokens over 8000 keys take
+ * half the time.  The results of both differ by roundings. */
+attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, const attn_mask_desc_t* mask,
+                                         size_t* bytes);
 
 /* attn_paged_fwd over an 8-bit cache: the attention over the values that the codes
  * and scales stand for, exactly (attn_paged8_load gives the same ones); masks, lengths, results and statuses as attn_paged_fwd

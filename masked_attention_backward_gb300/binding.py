@@ -149,7 +149,7 @@ def load(build: bool = True) -> ctypes.CDLL:
                                              ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp,
                                              vp]
             lib.attn_paged8_load.restype = ctypes.c_int
-            lib.attn_paged8_workspace_size.argtypes = [ps, ctypes.POINTER(sz)]
+            lib.attn_paged8_workspace_size.argtypes = [ps, pm, ctypes.POINTER(sz)]
             lib.attn_paged8_workspace_size.restype = ctypes.c_int
             lib.attn_paged8_fwd.argtypes = [ps, p8, vp, vp, vp, vp, vp, vp, ctypes.c_int,
                                             ctypes.c_int, vp, pm, ctypes.c_float, vp, vp, vp, sz,
@@ -592,9 +592,11 @@ def attn_paged8_load(pages: attn_pages8_t, B, total, start, cu_seqlens, block_ta
                                    k, v, stream)
 
 
-def attn_paged8_workspace_size(shape: attn_shape_t):
+def attn_paged8_workspace_size(shape: attn_shape_t, mask: Optional[attn_mask_desc_t] = None):
     n = ctypes.c_size_t(0)
-    r = load().attn_paged8_workspace_size(ctypes.byref(shape), ctypes.byref(n))
+    r = load().attn_paged8_workspace_size(ctypes.byref(shape),
+                                          None if mask is None else ctypes.byref(mask),
+                                          ctypes.byref(n))
     return r, n.value
 
 
@@ -859,21 +861,36 @@ def paged_shape(q: torch.Tensor, cache, mask: Mask) -> attn_shape_t:
                         mask.max_seqlen_k, q.shape[2], _dtype_code(q), 0)
 
 
+# the most that paged_workspace adds for the 16-bit rows of an 8-bit cache's chunks
+PAGED8_ROOM = 2 << 30
+
+
 @functools.lru_cache(maxsize=256)
-def _paged_workspace_bytes(eight: bool, *shape) -> int:
-    call, name = (attn_paged8_workspace_size, "attn_paged8_workspace_size") if eight else \
-        (attn_paged_workspace_size, "attn_paged_workspace_size")
-    r, n = call(attn_shape_t(*shape, 0))
+def _paged_workspace_bytes(shape, mask) -> int:
+    sh = attn_shape_t(*shape, 0)
+    if mask is None:
+        r, n = attn_paged_workspace_size(sh)
+    else:
+        r, n = attn_paged8_workspace_size(sh)
+        if r == ATTN_OK:
+            kind, window, first, total_q = mask
+            _, more = attn_paged8_workspace_size(
+                sh, attn_mask_desc_t(kind=kind, window=window, first=first, total_q=total_q))
+            n = more if more - n <= PAGED8_ROOM else n
     if r != ATTN_OK:
-        raise AttnError(r, name)
+        raise AttnError(r, "attn_paged_workspace_size" if mask is None else
+                        "attn_paged8_workspace_size")
     return n
 
 
 def paged_workspace(q: torch.Tensor, cache, mask: Mask,
                     shape: Optional[attn_shape_t] = None) -> torch.Tensor:
+    """A workspace of paged_fwd; for a PagedCache8 and chunks with room for the rows
+    that they see in 16 bits, up to PAGED8_ROOM bytes."""
     sh = shape or paged_shape(q, cache, mask)
-    n = _paged_workspace_bytes(isinstance(cache, PagedCache8), sh.B, sh.Hq, sh.Hkv, sh.Sq, sh.Skv,
-                               sh.D, sh.dtype)
+    n = _paged_workspace_bytes((sh.B, sh.Hq, sh.Hkv, sh.Sq, sh.Skv, sh.D, sh.dtype),
+                               (mask.kind, mask.window, mask.first, mask.total_q)
+                               if isinstance(cache, PagedCache8) else None)
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 

@@ -1,6 +1,7 @@
 // api_paged.cu -- the C ABI of the paged key/value cache (declared in
 // include/maskattn.h): argument checks, then the launches, on the caller's
 // stream.  Nothing is allocated and nothing is read back.
+#include <limits.h>
 #include <math.h>
 #include <string.h>
 
@@ -63,11 +64,10 @@ struct PagedLayout {
   int tile_tokens, tile_rows, slot_floats;
 };
 
-// tile: rows of a query tile at most.
-PagedLayout paged_layout(const attn_shape_t* sh, int tile) {
+PagedLayout paged_layout(const attn_shape_t* sh) {
   PagedLayout L;
   const int group = sh->Hq / sh->Hkv;
-  L.tile_tokens = tile / group < sh->Sq ? tile / group : sh->Sq;
+  L.tile_tokens = Q_TILE / group < sh->Sq ? Q_TILE / group : sh->Sq;
   L.tile_rows = L.tile_tokens * group;
   L.slot_floats = (L.tile_rows + 31) / 32 * 2 * PAGED_WARP_FLOATS;
   size_t off = 0;
@@ -89,9 +89,7 @@ attn_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : A
 
 namespace mab {
 
-size_t paged_workspace(const attn_shape_t* shape, int tile) {
-  return paged_layout(shape, tile).total;
-}
+size_t paged_workspace(const attn_shape_t* shape) { return paged_layout(shape).total; }
 
 // What the attentions over 16-bit and 8-bit pages share: the checks behind those
 // of shape and pages, the parameters, and the map of q where it is wanted.  *work is
@@ -100,8 +98,8 @@ attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size
                          const void* k_pages, const void* v_pages, const int* block_table,
                          int table_stride, int max_pages, const float* sink,
                          const attn_mask_desc_t* mask, float scale, void* o, float* lse, void* ws,
-                         size_t ws_bytes, cudaStream_t st, int tile, PagedParams* out,
-                         CUtensorMap* tQ, bool* work) {
+                         size_t ws_bytes, cudaStream_t st, PagedParams* out, CUtensorMap* tQ,
+                         bool* work) {
   if (!mask || !(scale > 0.f) || !isfinite(scale) || max_pages < 1 || table_stride < max_pages ||
       slots_of(max_pages, page_size) < 0)
     return ATTN_ERR_INVALID_ARG;
@@ -132,7 +130,7 @@ attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size
       !aligned(mask->cu_seqlens_q, 4) || !aligned(mask->seqlen_k, 4) || mask->total_q < 0)
     return ATTN_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return ATTN_ERR_INVALID_ARG;
-  const PagedLayout L = paged_layout(shape, tile);
+  const PagedLayout L = paged_layout(shape);
   if (ws_bytes < L.total) return ATTN_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(ws);
   *work = false;
@@ -171,6 +169,7 @@ attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size
   p.start = reinterpret_cast<PagedStart*>(w + L.start);
   p.part = reinterpret_cast<float*>(w + L.part);
   p.slot_floats = L.slot_floats;
+  p.tokens_hi = INT_MAX;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -226,7 +225,7 @@ attn_status_t attn_paged_workspace_size(const attn_shape_t* shape, size_t* bytes
   if (!bytes) return ATTN_ERR_INVALID_ARG;
   const attn_status_t r = check_paged_shape(shape);
   if (r != ATTN_OK) return r;
-  *bytes = paged_workspace(shape, Q_TILE);
+  *bytes = paged_workspace(shape);
   return ATTN_OK;
 }
 
@@ -244,8 +243,8 @@ attn_status_t attn_paged_fwd(const attn_shape_t* shape, const attn_pages_t* page
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   bool work = false;
   r = paged_call(shape, pages->num_pages, pages->page_size, q, k_pages, v_pages, block_table,
-                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st, Q_TILE,
-                 &p, &tQ, &work);
+                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st, &p, &tQ,
+                 &work);
   if (r != ATTN_OK || !work) return r;
   const bool bf16 = shape->dtype == ATTN_BF16;
   auto pages_map = [&](CUtensorMap* m, const void* base) {

@@ -45,6 +45,46 @@ attn_status_t check_buffers8(const attn_pages8_t* pg, const void* k_pages, const
              : ATTN_ERR_INVALID_ARG;
 }
 
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// New tokens whose rows k_paged8_rows takes.
+int few_tokens(const attn_shape_t* sh) { return PAGED8_ROWS / (sh->Hq / sh->Hkv); }
+
+// Room for the 16-bit rows of a call's chunks behind the other workspace: pages for as
+// many requests as the tokens allow to have more than few, each with all the sub-tiles
+// that its tokens may see.  pages = 0: none are wanted (or more than a map can hold).
+struct ExpandedLayout {
+  size_t status, table, k, v, total;
+  long long pages;
+  int cols;
+};
+ExpandedLayout expanded_layout(const attn_shape_t* sh, const attn_mask_desc_t* mask) {
+  ExpandedLayout L = {};
+  L.total = paged_workspace(sh);
+  const int group = sh->Hq / sh->Hkv;
+  if ((long long)sh->Sq * group <= Q_TILE) return L;
+  const long long chunks = mask->total_q / (few_tokens(sh) + 1);
+  L.cols = (sh->Skv + PAGED8_PAGE - 1) / PAGED8_PAGE;
+  long long tiles = L.cols;
+  if (mask->kind == ATTN_MASK_SLIDING || mask->kind == ATTN_MASK_SLIDING_FIRST) {
+    const long long first =
+        mask->kind == ATTN_MASK_SLIDING_FIRST && mask->first > 0 ? mask->first : 0;
+    const long long seen =
+        ((long long)mask->window + sh->Sq + PAGED8_PAGE) / PAGED8_PAGE + 1 + first / PAGED8_PAGE + 1;
+    if (seen < tiles) tiles = seen;
+  }
+  const long long pages = (chunks < sh->B ? chunks : sh->B) * tiles;
+  if (pages < 1 || pages * PAGED8_PAGE >= (1ll << 31)) return L;
+  L.pages = pages;
+  const size_t rows = (size_t)pages * sh->Hkv * PAGED8_PAGE * HEAD_DIM * 2;
+  L.status = align256(L.total);
+  L.table = align256(L.status + PAGED_MAX_CTAS * sizeof(DevStatus));
+  L.k = align256(L.table + (size_t)sh->B * L.cols * sizeof(int));
+  L.v = align256(L.k + rows);
+  L.total = align256(L.v + rows);
+  return L;
+}
+
 attn_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
 }  // namespace
@@ -95,11 +135,13 @@ attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, con
                                         static_cast<cudaStream_t>(stream)));
 }
 
-attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, size_t* bytes) {
+attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, const attn_mask_desc_t* mask,
+                                         size_t* bytes) {
   if (!bytes) return ATTN_ERR_INVALID_ARG;
   const attn_status_t r = check_paged_shape(shape);
   if (r != ATTN_OK) return r;
-  *bytes = paged_workspace(shape, PAGED8_TILE);
+  *bytes = paged_workspace(shape);
+  if (mask) *bytes = expanded_layout(shape, mask).total;
   return ATTN_OK;
 }
 
@@ -117,12 +159,12 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   Paged8Params p;
   CUtensorMap tQ, tK, tV;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // few rows (as tile_rows will have it): a kernel that reads q's rows itself
-  const bool few = (long long)shape->Sq * (shape->Hq / shape->Hkv) <= PAGED8_ROWS;
+  // every request has few rows: a kernel that reads q's rows itself
+  const bool few = shape->Sq <= few_tokens(shape);
   bool work = false;
   r = paged_call(shape, pages->num_pages, pages->page_size, q, k_pages, v_pages, block_table,
-                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st,
-                 PAGED8_TILE, &p, few ? nullptr : &tQ, &work);
+                 table_stride, max_pages, sink, mask, scale, o, lse, ws, ws_bytes, st, &p,
+                 few ? nullptr : &tQ, &work);
   if (r != ATTN_OK || !work) return r;
   r = check_buffers8(pages, k_pages, v_pages, k_scales, v_scales);
   if (r != ATTN_OK) return r;
@@ -132,13 +174,63 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
   p.scale_head_stride = pg.scale_head_stride;
   p.scale_shift = pg.shift;
   const bool bf16 = shape->dtype == ATTN_BF16, i8 = pages->code == ATTN_I8;
-  auto pages_map = [&](CUtensorMap* m, const void* base) {
-    return make_pages8_map(m, base, pg.num_pages, pg.page_size, pg.Hkv, pg.page_stride,
-                           pg.head_stride, pg.token_stride, few ? 16u : (uint32_t)p.box_rows);
+  auto pages_maps = [&](int rows) {
+    for (CUtensorMap* m : {&tK, &tV})
+      if (!make_pages8_map(m, m == &tK ? k_pages : v_pages, pg.num_pages, pg.page_size, pg.Hkv,
+                           pg.page_stride, pg.head_stride, pg.token_stride, (uint32_t)rows))
+        return false;
+    return true;
   };
-  if (!pages_map(&tK, k_pages) || !pages_map(&tV, v_pages)) return ATTN_ERR_CUDA;
-  return cuda_status(few ? launch_paged8_rows(bf16, i8, p, tK, tV, q, st)
-                         : launch_paged8_chunk(bf16, i8, p, tQ, tK, tV, st));
+  if (few) {
+    if (!pages_maps(16)) return ATTN_ERR_CUDA;
+    return cuda_status(launch_paged8_rows(bf16, i8, p, tK, tV, q, st));
+  }
+  // One query tile a request and kv head (or a workspace without room for 16-bit rows): codes
+  // become tiles inside the attention.
+  const ExpandedLayout L = expanded_layout(shape, mask);
+  if (L.pages == 0 || ws_bytes < L.total) {
+    if (!pages_maps(p.box_rows)) return ATTN_ERR_CUDA;
+    return cuda_status(launch_paged8_fwd(bf16, i8, p, tQ, tK, tV, st));
+  }
+  // Chunks: the requests with few rows first, unless the tokens leave room for none ...
+  const int small = few_tokens(shape);
+  const bool some_few = mask->total_q <= (long long)(shape->B - 1) * shape->Sq + small;
+  if (some_few && small > 0) {
+    Paged8Params f = p;
+    f.tokens_hi = small;
+    f.tile_tokens = small;
+    f.tile_rows = small * p.group;
+    if (!pages_maps(16)) return ATTN_ERR_CUDA;
+    if (launch_paged8_rows(bf16, i8, f, tK, tV, q, st) != cudaSuccess) return ATTN_ERR_CUDA;
+    p.keep_status = 1;
+  }
+  // ... then the others' rows in 16 bits, and the attention over them.
+  p.tokens_lo = small;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  Expanded e;
+  e.k = reinterpret_cast<uint16_t*>(w + L.k);
+  e.v = reinterpret_cast<uint16_t*>(w + L.v);
+  e.table = reinterpret_cast<int*>(w + L.table);
+  e.cols = L.cols;
+  e.pages = (int)L.pages;
+  e.status = reinterpret_cast<DevStatus*>(w + L.status);
+  if (launch_paged8_expand(bf16, i8, p, k_pages, v_pages, pg.page_stride, pg.head_stride,
+                           pg.token_stride, e, st) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  PagedParams d = p;
+  d.more_status = e.status;
+  d.table = e.table;
+  d.table_stride = e.cols;
+  d.num_pages = e.pages;
+  d.page_size = PAGED8_PAGE;
+  d.inv_page_size = 1.f / PAGED8_PAGE;
+  d.box_rows = PAGED8_PAGE;
+  const long long head = PAGED8_PAGE * HEAD_DIM;
+  for (CUtensorMap* m : {&tK, &tV})
+    if (!make_pages_map(m, m == &tK ? e.k : e.v, bf16, e.pages, PAGED8_PAGE, shape->Hkv,
+                        head * shape->Hkv, head, HEAD_DIM, PAGED8_PAGE))
+      return ATTN_ERR_CUDA;
+  return cuda_status(launch_paged_fwd(bf16, d, tQ, tK, tV, st));
 }
 
 }  // extern "C"

@@ -53,6 +53,12 @@ struct PagedParams {
   PagedStart* start; // [grid + 1]
   float* part;       // [2 grid, slot_floats] pieces
   int slot_floats;
+  // Requests with more than tokens_lo and at most tokens_hi new tokens take part; the
+  // call's other kernels take the rest.  more_status: [grid] statuses of a kernel before
+  // this one; keep_status: the call's status word has been written.
+  int tokens_lo, tokens_hi;
+  const DevStatus* more_status;
+  int keep_status;
 };
 
 // ... and over a cache of 8-bit codes.
@@ -68,9 +74,9 @@ attn_status_t paged_call(const attn_shape_t* shape, int num_pages, int page_size
                          const void* k_pages, const void* v_pages, const int* block_table,
                          int table_stride, int max_pages, const float* sink,
                          const attn_mask_desc_t* mask, float scale, void* o, float* lse, void* ws,
-                         size_t ws_bytes, cudaStream_t st, int tile, PagedParams* out,
-                         CUtensorMap* tQ, bool* work);
-size_t paged_workspace(const attn_shape_t* shape, int tile);
+                         size_t ws_bytes, cudaStream_t st, PagedParams* out, CUtensorMap* tQ,
+                         bool* work);
+size_t paged_workspace(const attn_shape_t* shape);
 
 cudaError_t launch_paged_plan(const attn_plan_t& p, cudaStream_t st);
 cudaError_t launch_paged_store(const attn_pages_t& pg, int T, const void* k, const void* v,
@@ -78,14 +84,29 @@ cudaError_t launch_paged_store(const attn_pages_t& pg, int T, const void* k, con
                                void* k_pages, void* v_pages, cudaStream_t st);
 cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap& tQ,
                              const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
-// Query rows (tokens times query heads of a kv head) of a call over 8-bit codes up to
-// which they go through k_paged8_rows, and of a tile of k_paged8_chunk.
+cudaError_t launch_paged8_fwd(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tQ,
+                              const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
+// Query rows (tokens times query heads of a kv head) of a request over 8-bit codes up to
+// which k_paged8_rows takes it.
 constexpr int PAGED8_ROWS = 16;
-constexpr int PAGED8_TILE = 256;
-cudaError_t launch_paged8_chunk(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tQ,
-                                const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
 cudaError_t launch_paged8_rows(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tK,
                                const CUtensorMap& tV, const void* q, cudaStream_t st);
+
+// Where the rows of the requests that k_paged8_rows does not take stand in 16 bits for a
+// call: pages of PAGED8_PAGE tokens [pages, Hkv, PAGED8_PAGE, 128], a table of them
+// [B, cols], and the statuses of the kernel that writes them.
+constexpr int PAGED8_PAGE = 64;
+struct Expanded {
+  uint16_t* k;
+  uint16_t* v;
+  int* table;
+  int cols, pages;
+  DevStatus* status;
+};
+cudaError_t launch_paged8_expand(bool bf16, bool i8, const Paged8Params& p, const void* k_pages,
+                                 const void* v_pages, long long page_stride,
+                                 long long head_stride, long long token_stride,
+                                 const Expanded& e, cudaStream_t st);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ uint32_t cluster_rank() {

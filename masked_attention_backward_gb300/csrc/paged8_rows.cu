@@ -90,13 +90,14 @@ struct Pieces {
 
 template <int NT>
 struct Rows {
-  static constexpr int WARPS = NT <= 2 ? 16 : 8;
-  static constexpr int LAG = NT <= 2 ? 1 : 2;   // slices on their way while one is worked on
+  // (NT 1 with 12 warps and two slices on their way: 64 tokens at 2000 to 16000 keys
+  // 223 us, 207 so; NT 2 with 16 and one 447, with 8 and two 332, 319 so)
+  static constexpr int WARPS = NT == 1 ? 16 : 12;
+  static constexpr int LAG = NT == 1 ? 1 : 2;   // slices on their way while one is worked on
   static constexpr int STAGES = LAG + 1;
   static constexpr bool Q_REGS = NT == 1;       // Q's fragments in registers, or shared memory
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int N = 8 * NT;              // rows of a unit at most
-  static constexpr int MERGE = 128 / WARPS;     // rows whose shares meet at a time
   static constexpr int O_STRIDE = 132;          // floats: rows on other banks
   struct Smem {
     // K's and V's rows of a slice (128B swizzle), and 16 scales of each where every
@@ -105,7 +106,7 @@ struct Rows {
     uint8_t scales[WARPS][STAGES][2][16];
     uint64_t full[WARPS][STAGES];
     uint2 q[Q_REGS ? 1 : NT][8][32];            // Q's fragments
-    float O[WARPS][MERGE][O_STRIDE];
+    float O[WARPS][8][O_STRIDE];                // eight rows meet at a time
     float ml[WARPS][N][2];                      // (M, l)
     LineSums<THREADS> sums;
     PagedStart cut[2];
@@ -397,7 +398,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
       M[t][0] = M[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.f;
     }
-    const int cnt = slices(cur);
+    const int cnt = slices(cur), rows = cur.n * p.group;
 #pragma unroll 1
     for (int i = 0; i < cnt && ok; ++i) {
       fill();
@@ -431,52 +432,65 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
       } else if (!BF16) {
         s01 = s23 = pack2<false>(sl.vs, sl.vs);
       }
-      // ---- scores: f16 products of the codes themselves
-      float sc[NT][4];
-      {
-        float s1[NT][4];  // of the second half of d: a chain of its own
+      // ---- scores: f16 products with K's codes as A fragments, bytes 16 c on of rows g
+      // and g + 8, then bytes 64 + 16 c on; two chains
+      float sc[NT][4], s1[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[t][j] = s1[t][j] = 0.f;
+        for (int j = 0; j < 4; ++j) sc[t][j] = s1[t][j] = 0.f;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          // bytes 16 c on of rows g and g + 8, then bytes 64 + 16 c on
-          const uint8_t* at = rk + ((g * 128 + ((c ^ g) << 4)) ^ (64 * hf));
-          const uint4 a = *reinterpret_cast<const uint4*>(at);
-          const uint4 b = *reinterpret_cast<const uint4*>(at + 1024);
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint8_t* at = rk + ((g * 128 + ((c ^ g) << 4)) ^ (64 * hf));
+        const uint4 a = *reinterpret_cast<const uint4*>(at);
+        const uint4 b = *reinterpret_cast<const uint4*>(at + 1024);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint2 pa = word_pairs<false, I8>(aw[j]), pb = word_pairs<false, I8>(bw[j]);
+        for (int j = 0; j < 4; ++j) {
+          const uint2 pa = word_pairs<false, I8>(aw[j]), pb = word_pairs<false, I8>(bw[j]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              uint2 q;
-              if (R::Q_REGS)
-                q = make_uint2(qf[(8 * hf + 2 * j) % 16], qf[(8 * hf + 2 * j + 1) % 16]);
-              else
-                q = s.q[t][4 * hf + j][lane];
-              mma16816<false>(hf ? s1[t] : sc[t], pa.x, pb.x, pa.y, pb.y, q.x, q.y);
-            }
+          for (int t = 0; t < NT; ++t) {
+            const uint2 q = R::Q_REGS ? make_uint2(qf[(8 * hf + 2 * j) % 16],
+                                                   qf[(8 * hf + 2 * j + 1) % 16])
+                                      : s.q[R::Q_REGS ? 0 : t][4 * hf + j][lane];
+            mma16816<false>(hf ? s1[t] : sc[t], pa.x, pb.x, pa.y, pb.y, q.x, q.y);
           }
         }
+      }
+      const bool masked = !(sl.key & WHOLE);  // some row does not see some key
+      if (masked && p.scale_shift == 0) {
+        // keys that no row sees may have any scale, and 0 * NaN is NaN (a block of 16
+        // tokens or more that holds a seen key has a scale for it)
+        const int k0 = sl.key & ~15;
+        const Walk w(p, cur.n, cur.L, 0);
+        if (BF16) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+          for (int j = 0; j < 2; ++j)
+            if (!w.sees(k0 + g + 8 * j)) vf[j] = 0.f;
+        } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            sc[t][j] = (sc[t][j] + s1[t][j]) * (kf[j >> 1] * col[t][j & 1]);
+            if (!w.sees(k0 + 2 * c + (j & 1) + 8 * (j >> 1))) {
+              uint32_t& pair = j < 2 ? s01 : s23;
+              pair &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
+            }
+        }
       }
-      // V: bytes 16 g on of rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-      const uint8_t* av = rv + 2 * c * 128 + ((g ^ (2 * c)) << 4);
-      const uint8_t* bv = rv + (2 * c + 1) * 128 + ((g ^ (2 * c + 1)) << 4);
-      uint4 v[4] = {*reinterpret_cast<const uint4*>(av), *reinterpret_cast<const uint4*>(bv),
-                    *reinterpret_cast<const uint4*>(av + 1024),
-                    *reinterpret_cast<const uint4*>(bv + 1024)};
-      if (!(sl.key & WHOLE)) {  // some row does not see some key
-        const int k0 = sl.key & ~15, rows = cur.n * p.group;
-        const Walk w(p, cur.n, cur.L, 0);
+      // probabilities for bf16 come times V's scale (a power of two, so exactly), in O's
+      // unit: at most 2^8 each, so that times 2^112 they want exponents of at most 7
+      if (BF16) {
+        const float unit = V_UNIT<I8> * (!I8 && !big ? 0x1p120f : 1.f);
+        vf[0] *= unit;
+        vf[1] *= unit;
+      }
+      uint32_t pf[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sc[t][j] = (sc[t][j] + s1[t][j]) * (kf[j >> 1] * col[t][j & 1]);
+        if (masked) {
+          const int k0 = sl.key & ~15;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int m = 8 * t + 2 * c + i;
@@ -489,35 +503,13 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
               if (!sees) sc[t][i + 2 * j] = -INFINITY;
             }
           }
-        // keys that no row sees may hold anything, and 0 * NaN is NaN (a block of 16
-        // tokens or more that holds a seen key has a scale for it)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (!w.sees(k0 + 2 * c + (j & 1) + 8 * (j >> 1))) {
-            v[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (!BF16 && p.scale_shift == 0) {
-              uint32_t& pair = j < 2 ? s01 : s23;
-              pair &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
-            }
-          }
-        if (BF16 && p.scale_shift == 0)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (!w.sees(k0 + g + 8 * j)) vf[j] = 0.f;
-      }
-      // ---- the running maximum: moved when a score exceeds it by more than 8
-      bool moves = false;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          moves = moves || fmaxf(sc[t][j], sc[t][j + 2]) > M[t][j] + RESCALE_LOG2;
-      if (__any_sync(0xffffffffu, moves)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
+        }
+        // ---- the running maximum: moved when a score exceeds it by more than 8
+        const float m0 = fmaxf(sc[t][0], sc[t][2]), m1 = fmaxf(sc[t][1], sc[t][3]);
+        if (__any_sync(0xffffffffu, m0 > M[t][0] + RESCALE_LOG2 || m1 > M[t][1] + RESCALE_LOG2)) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float mx = fmaxf(sc[t][j], sc[t][j + 2]);
+            float mx = j ? m1 : m0;
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             if (mx > M[t][j] + RESCALE_LOG2) {
@@ -531,31 +523,38 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
               }
             }
           }
-      }
-      // ---- probabilities as B fragments; for bf16 times V's scale (a power of two, so
-      // exactly), in O's unit
-      if (BF16) {
-        // at most 2^8 each, so that times 2^112 they want exponents of at most 7
-        const float unit = V_UNIT<I8> * (!I8 && !big ? 0x1p120f : 1.f);
-        vf[0] *= unit;
-        vf[1] *= unit;
-      }
-      uint32_t pf[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // a row that has seen nothing keeps its scores at -inf; 0 stands in for M
-          const float m = M[t][j & 1];
-          e[j] = fast_exp2(sc[t][j] - (m == -INFINITY ? 0.f : m));
-          l[t][j & 1] += e[j];
-          if (BF16) e[j] *= vf[j >> 1];
+        }
+        // ---- probabilities as B fragments (a row that has seen nothing keeps its scores
+        // at -inf; 0 stands in for M)
+        const float n0 = M[t][0] == -INFINITY ? 0.f : M[t][0];
+        const float n1 = M[t][1] == -INFINITY ? 0.f : M[t][1];
+        float e[4] = {fast_exp2(sc[t][0] - n0), fast_exp2(sc[t][1] - n1),
+                      fast_exp2(sc[t][2] - n0), fast_exp2(sc[t][3] - n1)};
+        l[t][0] += e[0] + e[2];
+        l[t][1] += e[1] + e[3];
+        if (BF16) {
+          e[0] *= vf[0];
+          e[1] *= vf[0];
+          e[2] *= vf[1];
+          e[3] *= vf[1];
         }
         pf[t][0] = transpose8x8(pack2<BF16>(e[0], e[1]));
         pf[t][1] = transpose8x8(pack2<BF16>(e[2], e[3]));
       }
       // ---- O^T += V^T P^T
+      // V: bytes 16 g on of rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+      const uint8_t* av = rv + 2 * c * 128 + ((g ^ (2 * c)) << 4);
+      const uint8_t* bv = rv + (2 * c + 1) * 128 + ((g ^ (2 * c + 1)) << 4);
+      uint4 v[4] = {*reinterpret_cast<const uint4*>(av), *reinterpret_cast<const uint4*>(bv),
+                    *reinterpret_cast<const uint4*>(av + 1024),
+                    *reinterpret_cast<const uint4*>(bv + 1024)};
+      if (masked) {  // what no row sees may be anything
+        const int k0 = sl.key & ~15;
+        const Walk w(p, cur.n, cur.L, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (!w.sees(k0 + 2 * c + (j & 1) + 8 * (j >> 1))) v[j] = make_uint4(0u, 0u, 0u, 0u);
+      }
       const uint32_t vw[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
                                  {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
       auto add_values = [&](auto bits) {
@@ -608,8 +607,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
       u_at = u_cnt;
     }
 
-    // ---- the piece's end: the warps' shares meet, MERGE rows at a time
-    const int rows = cur.n * p.group;
+    // ---- the piece's end: the warps' shares meet, eight rows at a time
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -617,31 +615,29 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
 #pragma unroll
         for (int d = 4; d <= 16; d <<= 1) l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], d);
 #pragma unroll
-    for (int t0 = 0; t0 < NT; t0 += R::MERGE / 8) {
-      if (8 * t0 >= rows) break;
+    for (int t = 0; t < NT; ++t) {
+      if (8 * t >= rows) break;
       __syncthreads();  // what was there is read
       // (nobody is at the unit before this one any more: its slot takes the one
       // after the next)
-      if (t0 == 0 && warp == 0) s.pieces.next(p, &s.unit[next_slot == 2 ? 0 : next_slot + 1]);
+      if (t == 0 && warp == 0) s.pieces.next(p, &s.unit[next_slot == 2 ? 0 : next_slot + 1]);
 #pragma unroll
-      for (int t = t0; t < t0 + R::MERGE / 8 && t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int n = 8 * t + 2 * c + j;
-          if (g == 0) {
-            s.ml[warp][n][0] = M[t][j];
-            s.ml[warp][n][1] = l[t][j];
-          }
-          float4* to = reinterpret_cast<float4*>(&s.O[warp][n - 8 * t0][16 * g]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            to[k] = make_float4(acc[t][2 * k][j], acc[t][2 * k][j + 2], acc[t][2 * k + 1][j],
-                                acc[t][2 * k + 1][j + 2]);
+      for (int j = 0; j < 2; ++j) {
+        const int n = 8 * t + 2 * c + j;
+        if (g == 0) {
+          s.ml[warp][n][0] = M[t][j];
+          s.ml[warp][n][1] = l[t][j];
         }
+        float4* to = reinterpret_cast<float4*>(&s.O[warp][2 * c + j][16 * g]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          to[k] = make_float4(acc[t][2 * k][j], acc[t][2 * k][j + 2], acc[t][2 * k + 1][j],
+                              acc[t][2 * k + 1][j + 2]);
+      }
       __syncthreads();
-      const int end = min(rows - 8 * t0, R::MERGE) * 64;
+      const int end = min(rows - 8 * t, 8) * 64;
       for (int i = threadIdx.x; i < end; i += R::THREADS) {
-        const int m = i >> 6, n = 8 * t0 + m, d = 2 * (i & 63);
+        const int m = i >> 6, n = 8 * t + m, d = 2 * (i & 63);
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int k = 0; k < WARPS; ++k) top = fmaxf(top, s.ml[k][n][0]);

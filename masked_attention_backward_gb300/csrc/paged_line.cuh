@@ -49,9 +49,11 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-// New tokens and keys of request b.
+// New tokens (none of a request that another kernel of the call takes) and keys of
+// request b.
 __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
-  return packed_len(p.cu_q, b, p.total_q, p.Sq);
+  const int n = packed_len(p.cu_q, b, p.total_q, p.Sq);
+  return n > p.tokens_lo && n <= p.tokens_hi ? n : 0;
 }
 __device__ __forceinline__ int keys_of(const PagedParams& p, int b) {
   return min(max(p.seqlen_k[b], 0), p.Skv);
@@ -293,18 +295,21 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedParams p) {
   grid_dependency_wait();
   if (c == p.grid - 1) {
     // the last CTA's part ends with the line: here the CTAs' statuses are
-    // passed on, the first one that is not 0
+    // passed on, the first one that is not 0 (behind those of a call's earlier kernels)
     if (blockIdx.y == 0 && threadIdx.x < 32) {
       unsigned code = 0, v[(PAGED_MAX_CTAS + 31) / 32];
 #pragma unroll
-      for (int k = 0; k < (PAGED_MAX_CTAS + 31) / 32; ++k)
+      for (int k = 0; k < (PAGED_MAX_CTAS + 31) / 32; ++k) {
         v[k] = 32 * k + lane < p.grid ? __ldcg(&p.cta_status[32 * k + lane].code) : 0u;
+        if (p.more_status && v[k] == 0u && 32 * k + lane < p.grid)
+          v[k] = __ldcg(&p.more_status[32 * k + lane].code);
+      }
 #pragma unroll
       for (int k = (PAGED_MAX_CTAS + 31) / 32 - 1; k >= 0; --k) {
         const unsigned set = __ballot_sync(0xffffffffu, v[k] != 0u);
         if (set) code = __shfl_sync(0xffffffffu, v[k], __ffs(set) - 1);
       }
-      if (lane == 0) {
+      if (lane == 0 && !(p.keep_status && p.status->code != 0u)) {
         DevStatus st{};
         st.code = code;
         *p.status = st;

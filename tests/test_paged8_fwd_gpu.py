@@ -98,9 +98,17 @@ class Case:
                              max_seqlen_q=max(max(n for n, _ in reqs), 1),
                              max_seqlen_k=max(max(L for _, L in reqs), 1))
 
-    def run(self, **kw):
-        ws = mab.paged_workspace(self.q, self.cache, self.mask)
-        ws.fill_(0xff)
+    def workspace(self, room=True):
+        """With room for the chunks' rows in 16 bits, or the least."""
+        if room:
+            ws = mab.paged_workspace(self.q, self.cache, self.mask)
+        else:
+            n = mab.attn_paged8_workspace_size(mab.paged_shape(self.q, self.cache, self.mask))[1]
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        return ws.fill_(0xff)
+
+    def run(self, room=True, **kw):
+        ws = self.workspace(room)
         out = (torch.full_like(self.q, 7.0),
                torch.full((self.Hq, self.T), 7.0, device="cuda"))
         mab.paged_fwd(self.q, self.cache, self.table, self.sink, self.mask, SCALE, ws=ws, out=out,
@@ -122,9 +130,9 @@ class Case:
         assert bool((o[t0:] == 7).all()) and bool((lse[:, t0:] == 7).all())
 
 
-def _go(*a, **kw):
+def _go(*a, room=True, **kw):
     c = Case(*a, **kw)
-    (o, lse), status = c.run()
+    (o, lse), status = c.run(room)
     assert status == mab.ATTN_OK
     c.check(o, lse)
 
@@ -139,24 +147,27 @@ def test_one_token(cuda_lib, L, form):
                                  (200, 1000), (500, 500)])
 @pytest.mark.parametrize("kind,window,first", [(CAUSAL, 0, 0), (SLIDING, 1, 0), (SLIDING, 70, 0),
                                                (FIRST, 40, 3), (FIRST, 100, 130), (NONE, 0, 0)])
-def test_chunks(cuda_lib, n, L, kind, window, first):
-    _go([(n, L)], kind=kind, window=window, first=first, seed=n + L, pad=3,
+@pytest.mark.parametrize("room", [True, False])
+def test_chunks(cuda_lib, n, L, kind, window, first, room):
+    _go([(n, L)], room=room, kind=kind, window=window, first=first, seed=n + L, pad=3,
         block=1 if n % 2 else 16, form=FORMS[(n + window) % 4])
 
 
 @pytest.mark.parametrize("layout", ["HND", "NHD"])
 @pytest.mark.parametrize("ps,block", [(16, 1), (16, 16), (32, 32), (48, 1), (48, 16), (64, 64),
                                       (80, 16), (128, 32), (128, 64), (256, 1)])
-def test_pages(cuda_lib, ps, block, layout):
-    _go([(1, 700), (5, 333), (40, 41)], ps=ps, block=block, layout=layout, seed=ps,
+@pytest.mark.parametrize("room", [True, False])
+def test_pages(cuda_lib, ps, block, layout, room):
+    _go([(1, 700), (5, 333), (90, 91)], room=room, ps=ps, block=block, layout=layout, seed=ps,
         form=FORMS[ps // 16 % 4])
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (5, 1), (8, 1), (9, 1), (16, 2), (33, 1),
                                     (64, 8), (128, 1)])
 @pytest.mark.parametrize("n", [1, 2, 4, 17])
-def test_heads(cuda_lib, Hq, Hkv, n):
-    _go([(n, 150), (1, 30)], Hq=Hq, Hkv=Hkv, seed=Hq + n, form=FORMS[n % 4], block=16)
+@pytest.mark.parametrize("room", [True, False])
+def test_heads(cuda_lib, Hq, Hkv, n, room):
+    _go([(n, 150), (1, 30)], room=room, Hq=Hq, Hkv=Hkv, seed=Hq + n, form=FORMS[n % 4], block=16)
 
 
 @pytest.mark.parametrize("form", FORMS, ids=IDS)
@@ -166,13 +177,51 @@ def test_long_context_over_many_ctas(cuda_lib, form, new):
 
 
 @pytest.mark.parametrize("kind,window,first", [(CAUSAL, 0, 0), (FIRST, 200, 5)])
-def test_ragged_batch(cuda_lib, kind, window, first):
+@pytest.mark.parametrize("room", [True, False])
+def test_ragged_batch(cuda_lib, kind, window, first, room):
     """Requests without new tokens, without keys, single tokens, chunks."""
     r = random.Random(7)
     reqs = [(1, r.randint(1, 900)) for _ in range(12)]
     reqs += [(0, 50), (0, 0), (130, 700), (3, 3), (1, 1), (9, 2000), (0, 0), (2, 511)]
     r.shuffle(reqs)
-    _go(reqs, Hq=8, Hkv=2, ps=32, block=16, kind=kind, window=window, first=first, pad=5, seed=3)
+    _go(reqs, room=room, Hq=8, Hkv=2, ps=32, block=16, kind=kind, window=window, first=first,
+        pad=5, seed=3)
+
+
+@pytest.mark.parametrize("room", [True, False])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (20, 1), (6, 2)])
+def test_few_rows_beside_chunks(cuda_lib, Hq, Hkv, room):
+    """Requests on both sides of the number of rows that makes a chunk."""
+    g = Hq // Hkv
+    few = 16 // g
+    reqs = [(max(few, 1), 100), (few + 1, 333), (1, 64), (130, 131), (0, 9), (0, 0), (few + 2, 65),
+            (max(few - 1, 1), 2000), (200, 777)]
+    _go(reqs, room=room, Hq=Hq, Hkv=Hkv, ps=16, block=16, kind=FIRST, window=90, first=20, pad=2)
+    _go(reqs, room=room, Hq=Hq, Hkv=Hkv, ps=64, block=1, form=("i8", F16))
+
+
+def test_workspace():
+    """The least need does not grow with the lengths; the room goes by what chunks see."""
+    shape = lambda **kw: mab.attn_shape_t(*[dict(dict(B=2, Hq=8, Hkv=2, Sq=1, Skv=6400, D=128,
+                                                      dtype=0, flags=0), **kw)[n]
+                                            for n in ("B", "Hq", "Hkv", "Sq", "Skv", "D", "dtype",
+                                                      "flags")])
+    least = lambda s: mab.attn_paged8_workspace_size(s)[1]
+    mask = lambda **kw: mab.attn_mask_desc_t(kind=CAUSAL, **kw)
+    full = lambda s, **kw: mab.attn_paged8_workspace_size(s, mask(**kw))[1]
+    assert least(shape(Sq=128)) == least(shape(Sq=4000, Skv=2 ** 24))
+    assert full(shape(), total_q=2) == least(shape())
+    assert full(shape(Sq=32), total_q=64) == least(shape(Sq=32))   # one tile a kv head
+    s = shape(Sq=500)
+    page = 2 * 2 * 64 * 128 * 2                                    # K and V of both heads
+    one = full(s, total_q=9) - least(s)                            # room for one chunk
+    assert 100 * page <= one < 101 * page
+    assert 200 * page <= full(s, total_q=1000) - least(s) < 201 * page
+    m = mab.attn_mask_desc_t(kind=FIRST, window=640, first=64, total_q=500)
+    seen = mab.attn_paged8_workspace_size(s, m)[1] - least(s)
+    assert 2 * 20 * page <= seen < 2 * 24 * page
+    assert mab.attn_paged8_workspace_size(shape(D=64), mask())[0] == mab.ATTN_ERR_UNSUPPORTED
+    assert mab.attn_paged8_workspace_size(shape(B=0))[0] == mab.ATTN_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("form", FORMS, ids=IDS)
@@ -189,15 +238,18 @@ def test_more_new_tokens_than_keys(cuda_lib, form):
         c.check(o, lse)
 
 
-@pytest.mark.parametrize("n", [1, 30])
-def test_bad_page(cuda_lib, n):
-    """A page outside the cache stands for zeros, and the status says so."""
-    c = Case([(n, 100)], ps=16, block=1, form=("i8", F16))
+@pytest.mark.parametrize("n", [1, 30, 90])
+@pytest.mark.parametrize("room", [True, False])
+@pytest.mark.parametrize("other", [0, 1, 100])
+def test_bad_page(cuda_lib, n, room, other):
+    """A page outside the cache stands for zeros, and the status says so, whichever
+    kernel meets it."""
+    c = Case([(n, 100), (other, 200)], ps=16, block=1, form=("i8", F16))
     for bad in (c.cache.num_pages, -1, -2 ** 31, 2 ** 31 - 1):
         c.table[0, 2] = bad
         c.k[0][32:48] = 0
         c.v[0][32:48] = 0
-        (o, lse), status = c.run()
+        (o, lse), status = c.run(room)
         assert status == mab.ATTN_ERR_INVALID_ARG
         c.check(o, lse)
 
@@ -212,8 +264,9 @@ def test_extreme_scales(cuda_lib, form, n):
 
 
 @pytest.mark.parametrize("form", FORMS, ids=IDS)
-@pytest.mark.parametrize("n", [1, 3, 40])
-def test_one_key_gives_its_value(cuda_lib, form, n):
+@pytest.mark.parametrize("n", [1, 3, 40, 100])
+@pytest.mark.parametrize("room", [True, False])
+def test_one_key_gives_its_value(cuda_lib, form, n, room):
     """A row that sees one key has that key's value, for every code and for scales
     from the least to the largest that the store writes: nothing is rounded on the
     way to O.  Row i sees key i alone (a window of one)."""
@@ -228,13 +281,13 @@ def test_one_key_gives_its_value(cuda_lib, form, n):
         pages = rows.view(1, 1, 16, 128).expand(c.cache.k_pages.shape)
         c.cache.v_pages.view(torch.uint8).copy_(pages)
         c.cache.v_scales.fill_(e + 127)
-        (o, lse), status = c.run()
+        (o, lse), status = c.run(room)
         assert status == mab.ATTN_OK
         want = rows.view(quant64.TYPES[code]).float()[torch.arange(n) % 16].double() * 2.0 ** e
         assert torch.equal(o.cpu().double(), want[:, None].expand(n, 2, 128))
 
 
-@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("n", [1, 40, 100])
 @pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -20, 2.0 ** 20, 2.0 ** 100])
 def test_query_magnitudes(cuda_lib, size, n):
     """bf16 queries of any size over keys of the opposite one."""
@@ -250,10 +303,10 @@ def test_query_magnitudes(cuda_lib, size, n):
     c.check(o, lse)
 
 
-@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("n", [1, 40, 300])
 def test_query_rows_not_finite(cuda_lib, n):
     """A row of q that is not finite gives NaN in its own o and lse alone."""
-    c = Case([(n, 200), (1, 90)], Hq=4, Hkv=1, form=("e4m3", BF16))
+    c = Case([(n, 400), (1, 90)], Hq=4, Hkv=1, form=("e4m3", BF16))
     (o0, l0), _ = c.run()
     c.q[0, 2, 5] = float("nan")
     (o, lse), status = c.run()
@@ -263,17 +316,18 @@ def test_query_rows_not_finite(cuda_lib, n):
     assert torch.equal(o, o0) and torch.equal(lse, l0)
 
 
-@pytest.mark.parametrize("n", [1, 50])
-def test_captured_with_other_lengths(cuda_lib, n):
-    a = Case([(n, 1000), (n, 64), (n, 2000)], ps=32, form=("e4m3", F16), seed=1)
-    ws = mab.paged_workspace(a.q, a.cache, a.mask)
+@pytest.mark.parametrize("n", [1, 20, 200])
+@pytest.mark.parametrize("room", [True, False])
+def test_captured_with_other_lengths(cuda_lib, n, room):
+    a = Case([(n, 1000), (n, 264), (n, 2000)], ps=32, form=("e4m3", F16), seed=1)
+    ws = a.workspace(room)
     out = (torch.full_like(a.q, 7.0), torch.full((a.Hq, a.T), 7.0, device="cuda"))
     call = lambda: mab.paged_fwd(a.q, a.cache, a.table, a.sink, a.mask, SCALE, ws=ws, out=out)
     call()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         call()
-    b = Case([(n, 300), (n, 1999), (n, 51)], ps=32, form=("e4m3", F16), seed=2)
+    b = Case([(n, 300), (n, 1999), (n, 251)], ps=32, form=("e4m3", F16), seed=2)
     P = b.cache.num_pages
     assert P <= a.cache.num_pages
     for x, y in ((a.cache.k_pages, b.cache.k_pages), (a.cache.v_pages, b.cache.v_pages)):
@@ -292,16 +346,16 @@ def test_captured_with_other_lengths(cuda_lib, n):
 
 
 def test_repeats_are_equal(cuda_lib):
-    for n in (1, 3, 70):
+    for n, room in ((1, True), (3, True), (12, True), (70, True), (70, False)):
         c = Case([(n, 5000), (n, 900), (n, 77)], Hq=8, Hkv=2, ps=32, seed=n)
-        (o0, l0), _ = c.run()
+        (o0, l0), _ = c.run(room)
         for _ in range(5):
-            (o, lse), _ = c.run()
+            (o, lse), _ = c.run(room)
             assert torch.equal(o, o0) and torch.equal(lse, l0)
 
 
 def test_no_lse_and_other_stream(cuda_lib):
-    c = Case([(1, 300), (20, 100)], form=("i8", BF16))
+    c = Case([(1, 300), (70, 100)], form=("i8", BF16))
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     o, lse = mab.paged_fwd(c.q, c.cache, c.table, c.sink, c.mask, SCALE, stream=st)
@@ -312,7 +366,7 @@ def test_no_lse_and_other_stream(cuda_lib):
     assert torch.equal(out, o)
 
 
-@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("n", [1, 40, 200])
 def test_waits_that_run_out(cuda_lib, n, monkeypatch):
     """The loader issues nothing: the call ends with a status."""
     c = Case([(n, 500)])
