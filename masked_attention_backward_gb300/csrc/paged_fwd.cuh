@@ -53,12 +53,12 @@
 // warp for V, four epilogue warps of their own (every polling warp slows the
 // softmax: a chunk 10 %), the join at the end of the last piece.
 //
-// The 8-bit cache: the loads bring codes into a ring of their own, and four
-// more warps make the 16-bit tiles of them that the matrix unit reads, a row's
-// half a thread: code times scale, exactly (quant8.cuh).  Each looks the pages
-// and scales of its 16 rows of 32 steps up a batch ahead.  They write zeros for
-// the rows that no row of the unit sees.  The softmax warps' registers come from
-// the other warps' (setmaxnreg: 512 threads at 128 are launched).
+// The 8-bit cache: the loads bring codes into a ring of their own, and eight
+// more warps make the 16-bit tiles of them that the matrix unit reads, two sets
+// that take steps in turn, each warp 16 rows of K and of V, half a row a thread:
+// code times scale, exactly (quant8.cuh), zeros for the rows that no row of the
+// unit sees.  Each looks the pages and scales of 16 of its steps up a batch ahead.
+// The softmax warps' registers come from the other warps' (setmaxnreg).
 #pragma once
 #include <type_traits>
 
@@ -77,7 +77,8 @@ constexpr int COL_O = 0;         // O accumulator of group g at COL_O + 128 g
 constexpr int COL_QA = 256;      // Q as the A operand, 64 columns of 16-bit pairs
 constexpr int COL_S = 320;       // S buffer b at COL_S + 64 b
 constexpr int SM_WARPS = 8;      // softmax warps, two groups of four
-constexpr int CV_WARPS = 8;      // converting warps, four for K and four for V
+constexpr int CV_WARPS = 8;      // converting warps, two sets of four
+constexpr int CV_BATCH = 16;     // steps of a set whose pages and scales are looked up at once
 // Warps and rings of a form.
 template <int FORM>
 struct Cfg {
@@ -97,12 +98,14 @@ static_assert(12 * Cfg<CODES_I8>::REGS_FEW + 8 * Cfg<CODES_I8>::REGS_SOFTMAX <= 
               "shares of the launch's registers");
 
 // What the converting warps add: the codes' ring (128B swizzle), and the scales
-// of each warp's 16 rows of 32 steps, two batches: [warp][batch][step][row].
+// of each warp's 16 rows, two batches: [warp][batch][step][K, V][row]; which of the
+// rows are seen (bits 0 to 15), and whether some exponent is above 7 (bit 16).
 template <int LD_STAGES>
 struct __align__(1024) Smem8 {
   uint8_t K8[LD_STAGES][Q_SUB * 128];
   uint8_t V8[LD_STAGES][Q_SUB * 128];
-  uint8_t scales[CV_WARPS][2][32][16];
+  uint8_t scales[CV_WARPS][2][CV_BATCH][2][16];
+  uint32_t seen[CV_WARPS][2][CV_BATCH];
   uint64_t bar_ld_full[LD_STAGES];
   uint64_t bar_ld_empty[LD_STAGES];
 };
@@ -174,13 +177,13 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     mbar_init(smem_u32(&s.bar_q_full), 1);
     mbar_init(smem_u32(&s.bar_qa_full), SM_WARPS);
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&s.bar_kv_full[i]), Q8 ? CV_WARPS : 1);
+      mbar_init(smem_u32(&s.bar_kv_full[i]), Q8 ? CV_WARPS / 2 : 1);
       mbar_init(smem_u32(&s.bar_kv_empty[i]), 1);
     }
     if constexpr (Q8)
       for (int i = 0; i < LD_STAGES; ++i) {
         mbar_init(smem_u32(&s.bar_ld_full[i]), 1);
-        mbar_init(smem_u32(&s.bar_ld_empty[i]), CV_WARPS);
+        mbar_init(smem_u32(&s.bar_ld_empty[i]), CV_WARPS / 2);
       }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s.bar_s_full[i >> 1][i & 1]), 1);
@@ -851,15 +854,11 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
     // ------------------------------------------------------------ converting warps
     if (warp >= C::CV_WARP0) {
       constexpr bool I8 = FORM == CODES_I8;
-      const int cw = warp - C::CV_WARP0, slice = cw & 3;
-      const bool is_v = cw >= 4;
-      const uint8_t* all_scales = is_v ? p.v_scales : p.k_scales;
+      const int cw = warp - C::CV_WARP0, slice = cw & 3, set = cw >> 2;
       // this thread's row of a step, and which half of it
       const int srow = lane >> 1, row = 16 * slice + srow, half = lane & 1;
       bool ok = true;
-      Cyc<LD_STAGES> lg;
-      Cyc<STAGES> rg;
-      int m = 0;  // step counter across units
+      int m0 = 0;  // steps of the units so far; a set takes every other one
       for (int j = 0; ok; ++j) {
         if (!mbar_wait_warp(smem_u32(&s.bar_q_full), j & 1, wc, TAG_Q)) break;
         const int N = s.unit.N, s0 = s.unit.s0, kvh = s.unit.kvh;
@@ -868,50 +867,70 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
         const int* table = p.table + (size_t)s.unit.b * p.table_stride;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.bar_unit_free));
-        // Lane l looks up step i + l of the piece: the page of this warp's 16 rows
-        // there (-1 where none of them is seen, or the page is not there), and their
+        const int first = (m0 ^ set) & 1;  // the set's first step of the piece
+        // Lanes l and l + 16 look up the set's step i + 2 l: the page of this warp's 16 rows
+        // there (-1 where none of them is seen, or the page is not there), and K's and V's
         // scales.
+        auto key_of = [&](int i) {
+          return w.tile(s0 + i + 2 * (lane & (CV_BATCH - 1))) * Q_SUB + 16 * slice;
+        };
         auto page_of = [&](int i) -> int {
-          const int k0 = w.tile(s0 + i + lane) * Q_SUB + 16 * slice;
-          if (i + lane >= N || !w.any(k0, k0 + 16)) return -1;
+          const int k0 = key_of(i);
+          if (i + 2 * (lane & (CV_BATCH - 1)) >= N || !w.any(k0, k0 + 16)) return -1;
           const int pg = __ldg(table + div_by(k0, p.page_size, p.inv_page_size));
           return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
         };
         auto scales_of = [&](int i, int pg) -> uint4 {
           if (pg < 0) return make_uint4(0u, 0u, 0u, 0u);
-          const int k0 = w.tile(s0 + i + lane) * Q_SUB + 16 * slice;
+          const int k0 = key_of(i);
           const int r = k0 - div_by(k0, p.page_size, p.inv_page_size) * p.page_size;
-          const long long at = pg * p.scale_page_stride + kvh * p.scale_head_stride +
-                               (r >> p.scale_shift);
-          if (p.scale_shift == 0) return __ldg(reinterpret_cast<const uint4*>(all_scales + at));
-          const uint32_t a = __ldg(all_scales + at) * 0x01010101u;
+          const uint8_t* at = (lane < CV_BATCH ? p.k_scales : p.v_scales) +
+                              pg * p.scale_page_stride + kvh * p.scale_head_stride +
+                              (r >> p.scale_shift);
+          if (p.scale_shift == 0) return __ldg(reinterpret_cast<const uint4*>(at));
+          const uint32_t a = __ldg(at) * 0x01010101u;
           return make_uint4(a, a, a, a);
         };
-        uint4 sc = scales_of(0, page_of(0));
-        int page = page_of(32);
-        for (int i = 0; ok && i < N; ++i, ++m, lg.next(), rg.next()) {
-          if ((i & 31) == 0) {
+        uint4 sc = scales_of(first, page_of(first));
+        int page = page_of(first + 2 * CV_BATCH);
+        int at = 0;  // own steps so far
+        for (int i = first; ok && i < N; i += 2, ++at) {
+          const int bt = (at / CV_BATCH) & 1, bi = at & (CV_BATCH - 1);
+          if (bi == 0) {
+            // which rows some row of the unit sees; unseen ones count as small
+            const int k0 = key_of(i);
+            uint32_t bits = 0;
+            const uint32_t sw[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (w.sees(k0 + r)) {
+                bits |= 1u << r;
+                if (((sw[r >> 2] >> (8 * (r & 3))) & 255u) > 127 + 7) bits |= 1u << 16;
+              }
+            bits |= __shfl_xor_sync(0xffffffffu, bits, CV_BATCH);
             __syncwarp();  // the batch before the last is read
-            *reinterpret_cast<uint4*>(s.scales[cw][(i >> 5) & 1][lane]) = sc;
+            *reinterpret_cast<uint4*>(
+                s.scales[cw][bt][lane & (CV_BATCH - 1)][lane / CV_BATCH]) = sc;
+            if (lane < CV_BATCH) s.seen[cw][bt][lane] = bits;
             __syncwarp();
-            sc = scales_of(i + 32, page);  // a batch ahead
-            page = page_of(i + 64);
+            sc = scales_of(i + 2 * CV_BATCH, page);  // a batch ahead
+            page = page_of(i + 4 * CV_BATCH);
           }
-          const int sb = s.scales[cw][(i >> 5) & 1][i & 31][srow];
-          const bool seen = w.sees(w.tile(s0 + i) * Q_SUB + row);
-          // e4m3 to bf16: one product while every exponent is at most 7
-          const bool small = BF16 && !I8 && !__any_sync(0xffffffffu, seen && sb > 127 + 7);
-          const uint32_t scale2 =
-              small ? scale_pair<BF16>(sb == SCALE_NAN ? sb : min(max(sb, 1) + 120, 254))
-                    : scale_pair<BF16>(sb);
-          ok = mbar_wait_warp(smem_u32(&s.bar_ld_full[lg.i]), lg.ph, wc, TAG_LD_FULL);
+          const int m = m0 + i, ld = m % LD_STAGES, kv = m % STAGES;
+          const uint32_t bits = s.seen[cw][bt][bi];
+          const bool small = BF16 && !I8 && !(bits >> 16);
+          ok = mbar_wait_warp(smem_u32(&s.bar_ld_full[ld]), (m / LD_STAGES) & 1, wc, TAG_LD_FULL);
           if (ok && m >= STAGES)
-            ok = mbar_wait_warp(smem_u32(&s.bar_kv_empty[rg.i]), rg.ph ^ 1u, wc, TAG_KV_EMPTY);
+            ok = mbar_wait_warp(smem_u32(&s.bar_kv_empty[kv]), (m / STAGES + 1) & 1, wc,
+                                TAG_KV_EMPTY);
           if (!ok) break;
-          const uint8_t* from = (is_v ? s.V8[lg.i] : s.K8[lg.i]) + row * 128;
-          uint8_t* to = (is_v ? s.V[rg.i] : s.K[rg.i]) + half * (Q_SUB * 128) + row * 128;
-          auto convert = [&](auto one) {
-            constexpr bool SMALL = decltype(one)::value;
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {  // K, then V
+            const int sb = s.scales[cw][bt][bi][x][srow];
+            // e4m3 to bf16: one product while every exponent is at most 7
+            uint32_t scale2 = scale_pair<BF16>(small ? min(max(sb, 1) + 120, 254) : sb);
+            const uint8_t* from = (x ? s.V8[ld] : s.K8[ld]) + row * 128;
+            uint8_t* to = (x ? s.V[kv] : s.K[kv]) + half * (Q_SUB * 128) + row * 128;
             // 16-byte units: 4 half + c of the code row become 2 c and 2 c + 1 of the
             // half's 128-byte row, both swizzled by the row; the halves take them in
             // orders that keep them off each other's banks
@@ -920,35 +939,44 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
             for (int c = 0; c < 4; ++c)
               v[c] = *reinterpret_cast<const uint4*>(
                   from + (((4 * half + (c ^ (half << 1))) ^ (row & 7)) << 4));
+            // a row that nobody sees may hold anything: zeros
+            if ((bits & 0xffffu) != 0xffffu && !((bits >> srow) & 1u)) {
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-              const int c = cc ^ (half << 1);
-              uint2 a = tile_words<BF16, I8, SMALL>(v[cc].x, scale2);
-              uint2 b = tile_words<BF16, I8, SMALL>(v[cc].y, scale2);
-              uint2 d = tile_words<BF16, I8, SMALL>(v[cc].z, scale2);
-              uint2 e = tile_words<BF16, I8, SMALL>(v[cc].w, scale2);
-              if (!seen) a = b = d = e = make_uint2(0u, 0u);
-              *reinterpret_cast<uint4*>(to + (((2 * c) ^ (row & 7)) << 4)) =
-                  make_uint4(a.x, a.y, b.x, b.y);
-              *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ (row & 7)) << 4)) =
-                  make_uint4(d.x, d.y, e.x, e.y);
+              for (int c = 0; c < 4; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
+              scale2 = 0u;
             }
-          };
-          if constexpr (BF16 && !I8) {
-            if (small)
-              convert(std::true_type());
-            else
+            auto convert = [&](auto one) {
+              constexpr bool SMALL = decltype(one)::value;
+#pragma unroll
+              for (int cc = 0; cc < 4; ++cc) {
+                const int c = cc ^ (half << 1);
+                const uint2 a = tile_words<BF16, I8, SMALL>(v[cc].x, scale2);
+                const uint2 b = tile_words<BF16, I8, SMALL>(v[cc].y, scale2);
+                const uint2 d = tile_words<BF16, I8, SMALL>(v[cc].z, scale2);
+                const uint2 e = tile_words<BF16, I8, SMALL>(v[cc].w, scale2);
+                *reinterpret_cast<uint4*>(to + (((2 * c) ^ (row & 7)) << 4)) =
+                    make_uint4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ (row & 7)) << 4)) =
+                    make_uint4(d.x, d.y, e.x, e.y);
+              }
+            };
+            if constexpr (BF16 && !I8) {
+              if (small)
+                convert(std::true_type());
+              else
+                convert(std::false_type());
+            } else {
               convert(std::false_type());
-          } else {
-            convert(std::false_type());
+            }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(smem_u32(&s.bar_kv_full[rg.i]));
-            mbar_arrive(smem_u32(&s.bar_ld_empty[lg.i]));
+            mbar_arrive(smem_u32(&s.bar_kv_full[kv]));
+            mbar_arrive(smem_u32(&s.bar_ld_empty[ld]));
           }
         }
+        m0 += N;
       }
     }
   }
