@@ -49,6 +49,8 @@
  * time of the call.  Test hooks, off unless set in the environment at the time
  * of a call: MASKATTN_TEST_NO_LOADS=1 makes the kernels' loader warps issue
  * nothing, so the call's waits run out and it ends with ATTN_ERR_TIMEOUT;
+ * MASKATTN_PAGED8_ROOM=1 makes attn_paged8_fwd use room for its chunks' rows
+ * however little work there is (and attn_paged8_workspace_size ask for it);
  * MASKATTN_DKDV_SCHEDULE=tile or =units forces the per-tile or the persistent
  * form of the dK/dV kernel (otherwise chosen by the walk lengths; the results
  * are the same bit for bit).
@@ -428,9 +430,10 @@ attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, con
  * attn_paged_workspace_size; with the call's mask (of which kind, window, first and
  * total_q are read) with room besides for the rows that chunks see, in 16 bits: 512
  * bytes for each key (up to Skv, or those of the window) of each kv head and request
- * that may have a chunk.  With that much attn_paged8_fwd writes them there once, where
- * with less every query tile makes them anew: chunks of 1900 tokens over 8000 keys take
- * half the time.  The results of both differ by roundings. */
+ * that may have a chunk, where the bounds say that there is work enough.  With that much
+ * attn_paged8_fwd writes them there once; with less every query tile makes them anew
+ * (chunks of 1900 tokens over 8000 keys: 389 and 626 us).  The results of both differ by
+ * roundings. */
 attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, const attn_mask_desc_t* mask,
                                          size_t* bytes);
 

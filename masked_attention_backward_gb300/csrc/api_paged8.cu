@@ -1,6 +1,8 @@
 // api_paged8.cu -- the C ABI of the 8-bit cache (declared in
 // include/maskattn.h): argument checks, then the launches, on the caller's
 // stream.  Nothing is allocated and nothing is read back.
+#include <stdlib.h>
+
 #include "paged.h"
 #include "paged8.h"
 #include "tmap.h"
@@ -47,8 +49,21 @@ attn_status_t check_buffers8(const attn_pages8_t* pg, const void* k_pages, const
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// Test hook, read at each call: room for 16-bit rows is used however few steps there are.
+bool test_paged8_room() {
+  const char* e = getenv("MASKATTN_PAGED8_ROOM");
+  return e && e[0] == '1';
+}
+
 // New tokens whose rows k_paged8_rows takes.
 int few_tokens(const attn_shape_t* sh) { return PAGED8_ROWS / (sh->Hq / sh->Hkv); }
+
+// Steps (64 keys of a query tile) that an SM has at least, going by the call's bounds,
+// when its chunks' rows are written in 16 bits first.  Four chunks of 256 tokens over 2000
+// keys, 32/8 heads, 54 steps: 64 us so, 74 with tiles made inside the attention; 15 single
+// tokens and a chunk of 500 under a window of 1024, 24 steps: 68 and 56 (two kernels more,
+// and two joins, for the single tokens).
+constexpr int EXPAND_STEPS = 40;
 
 // Room for the 16-bit rows of a call's chunks behind the other workspace: pages for as
 // many requests as the tokens allow to have more than few, each with all the sub-tiles
@@ -73,6 +88,9 @@ ExpandedLayout expanded_layout(const attn_shape_t* sh, const attn_mask_desc_t* m
         ((long long)mask->window + sh->Sq + PAGED8_PAGE) / PAGED8_PAGE + 1 + first / PAGED8_PAGE + 1;
     if (seen < tiles) tiles = seen;
   }
+  const long long steps =
+      ((long long)mask->total_q * group + Q_TILE - 1) / Q_TILE * tiles * sh->Hkv / PAGED_MAX_CTAS;
+  if (steps < EXPAND_STEPS && !test_paged8_room()) return L;
   const long long pages = (chunks < sh->B ? chunks : sh->B) * tiles;
   if (pages < 1 || pages * PAGED8_PAGE >= (1ll << 31)) return L;
   L.pages = pages;

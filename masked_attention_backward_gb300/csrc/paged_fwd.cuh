@@ -91,7 +91,7 @@ struct Cfg {
   static constexpr int AHEAD = 8;               // steps of a unit issued before the next one's Q
   // registers of the warps that wait and convert (12), and of the softmax warps (8):
   // of 20 * 96 that are launched
-  static constexpr int REGS_FEW = 56, REGS_SOFTMAX = 152;
+  static constexpr int REGS_FEW = 72, REGS_SOFTMAX = 128;
 };
 static_assert(12 * Cfg<CODES_I8>::REGS_FEW + 8 * Cfg<CODES_I8>::REGS_SOFTMAX <= 20 * 96 &&
                   Cfg<CODES_I8>::NUM_THREADS == 20 * 32,

@@ -23,6 +23,12 @@ FORMS = [("e4m3", F16), ("e4m3", BF16), ("i8", F16), ("i8", BF16)]
 IDS = ["e4m3-f16", "e4m3-bf16", "i8-f16", "i8-bf16"]
 
 
+@pytest.fixture(autouse=True)
+def _use_room(monkeypatch):
+    """Chunks of any size use room in the workspace."""
+    monkeypatch.setenv("MASKATTN_PAGED8_ROOM", "1")
+
+
 class Case:
     """reqs: (new tokens, keys) of each request."""
 
@@ -100,12 +106,9 @@ class Case:
 
     def workspace(self, room=True):
         """With room for the chunks' rows in 16 bits, or the least."""
-        if room:
-            ws = mab.paged_workspace(self.q, self.cache, self.mask)
-        else:
-            n = mab.attn_paged8_workspace_size(mab.paged_shape(self.q, self.cache, self.mask))[1]
-            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
-        return ws.fill_(0xff)
+        shape = mab.paged_shape(self.q, self.cache, self.mask)
+        n = mab.attn_paged8_workspace_size(shape, self.mask.desc() if room else None)[1]
+        return torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
 
     def run(self, room=True, **kw):
         ws = self.workspace(room)
@@ -200,7 +203,7 @@ def test_few_rows_beside_chunks(cuda_lib, Hq, Hkv, room):
     _go(reqs, room=room, Hq=Hq, Hkv=Hkv, ps=64, block=1, form=("i8", F16))
 
 
-def test_workspace():
+def test_workspace(monkeypatch):
     """The least need does not grow with the lengths; the room goes by what chunks see."""
     shape = lambda **kw: mab.attn_shape_t(*[dict(dict(B=2, Hq=8, Hkv=2, Sq=1, Skv=6400, D=128,
                                                       dtype=0, flags=0), **kw)[n]
@@ -220,6 +223,10 @@ def test_workspace():
     m = mab.attn_mask_desc_t(kind=FIRST, window=640, first=64, total_q=500)
     seen = mab.attn_paged8_workspace_size(s, m)[1] - least(s)
     assert 2 * 20 * page <= seen < 2 * 24 * page
+    # without the hook: where the bounds promise 40 steps an SM, of
+    # ceil(total_q * 4 / 128) * 100 * 2 / 152
+    monkeypatch.delenv("MASKATTN_PAGED8_ROOM")
+    assert full(s, total_q=960) == least(s) and full(s, total_q=1000) > least(s)
     assert mab.attn_paged8_workspace_size(shape(D=64), mask())[0] == mab.ATTN_ERR_UNSUPPORTED
     assert mab.attn_paged8_workspace_size(shape(B=0))[0] == mab.ATTN_ERR_INVALID_ARG
 
