@@ -106,6 +106,7 @@ struct Rows {
     uint8_t scales[WARPS][STAGES][2][16];
     uint64_t full[WARPS][STAGES];
     uint2 q[Q_REGS ? 1 : NT][8][32];            // Q's fragments
+    uint4 rows[2][N][16];                       // the rows of q of a unit and of the next
     float O[WARPS][8][O_STRIDE];                // eight rows meet at a time
     float ml[WARPS][N][2];                      // (M, l)
     LineSums<THREADS> sums;
@@ -140,6 +141,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// 16 bytes to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Unit of a bf16 unit's O: probabilities that meet e4m3's moved bits (2^120 too
@@ -204,7 +217,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
   int u_slot = 0, u_cnt = 0, u_at = 0;
   auto slices = [&](const Unit& x) { return x.N < 0 ? 0 : (4 * x.N - warp + WARPS - 1) / WARPS; };
   // Lane l looks slice i + l up: its page (-1: no seen key, or no such page) ...
-  constexpr int WHOLE = 1, NONE = 2, BIG = 4;  // flags below the slice's first key
+  constexpr int WHOLE = 1, NONE = 2;  // flags below the slice's first key
   auto first_key = [&](const Unit& u, const Walk& w, int i) {
     const int sl = warp + WARPS * (i + lane);
     return w.tile(u.s0 + (sl >> 2)) * Q_SUB + 16 * (sl & 3);
@@ -221,11 +234,12 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
     return -1;
   };
   // ... and where its rows and scales are: batch of the 32 slices from u_at on.
-  // (Flags: every row sees all 16 keys; no page, zeros stand in; V's exponent is past
-  // what the moved bits take.)
+  // (Flags: every row sees all 16 keys; no page, zeros stand in.)
   int b_key = 0, b_page = 0, b_row = 0, page_next = -1;
   long long b_sat = 0;            // a scale a token: their offset
-  float b_ks = 1.f, b_vs = 1.f;   // a scale for 16 tokens or more: the scales
+  // a scale for 16 tokens or more: the scales, V's negative where its exponent is past
+  // what the moved bits take
+  float b_ks = 1.f, b_vs = 1.f;
   auto batch = [&](int page) {
     const Unit& u = s.unit[u_slot];
     const Walk w(p, u.n, u.L, 0);
@@ -246,7 +260,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
         const int v = __ldg(p.v_scales + sat);
         b_ks = scale_float<BF16>(__ldg(p.k_scales + sat));
         b_vs = scale_float<BF16>(v);
-        if (v > 127 + 7) b_key |= BIG;
+        if (v > 127 + 7) b_vs = -b_vs;
       }
     }
     page_next = page_of(u, u_at + 32);
@@ -315,21 +329,35 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
       if (on_way == i && bring(way[i])) on_way = i + 1;
   };
 
+  // Brings the rows of q of unit x (the block; there once its copies are waited for and
+  // the block has met); rows that are no token's are left as they are, nobody reads them.
+  auto bring_q = [&](const Unit& x, int to) {
+    const int rows = x.N > 0 ? x.n * p.group : 0;
+    for (int i = threadIdx.x; i < rows * 16; i += R::THREADS) {
+      const int n = i >> 4, tl = n / p.group;
+      copy16(&s.rows[to][n][i & 15],
+             q_rows + ((long long)(x.off + tl) * p.Hq + x.kvh * p.group + (n - tl * p.group)) *
+                          HEAD_DIM + 8 * (i & 15));
+    }
+    copies_commit();
+  };
+  bring_q(s.unit[0], 0);
+  copies_wait();
+  __syncthreads();
   // Q's fragment words of row n = g of eight t: the elements of this thread's codes.
   // f16 products take K's codes as they are, so a bf16 row comes times 2^sh, which
-  // puts its largest element below 2^15: exact but for elements 2^-32 of that.
+  // puts its largest element below 2^15: exact but for elements 2^-31 of that.
+  int parity = 0;  // of s.rows
   auto q_row = [&](const Unit& x, int t, uint4 (&v)[4]) {
     const int n = 8 * t + g;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
     if (n < x.n * p.group && x.N > 0) {
-      const int tl = n / p.group;
-      const uint16_t* q = q_rows + ((long long)(x.off + tl) * p.Hq + x.kvh * p.group +
-                                 (n - tl * p.group)) * HEAD_DIM + 16 * c;
-      v[0] = __ldg(reinterpret_cast<const uint4*>(q));
-      v[1] = __ldg(reinterpret_cast<const uint4*>(q + 8));
-      v[2] = __ldg(reinterpret_cast<const uint4*>(q + 64));
-      v[3] = __ldg(reinterpret_cast<const uint4*>(q + 72));
+      const uint4* q = &s.rows[parity][n][2 * c];
+      v[0] = q[0];
+      v[1] = q[1];
+      v[2] = q[8];
+      v[3] = q[9];
     }
   };
   for (int slot = 0; s.unit[slot].N >= 0;) {
@@ -341,6 +369,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
       u_cnt = slices(cur);
       if (u_cnt > 0) batch(page_nxt);
     }
+    bring_q(s.unit[next_slot], parity ^ 1);
     more = s.unit[next_slot].N >= 0;
     page_nxt = more ? page_of(s.unit[next_slot], 0) : -1;
     uint32_t qf[R::Q_REGS ? 16 : 1];
@@ -409,28 +438,28 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
       const uint8_t* rv = s.ring[warp][from_stage][1];
       // scales of keys g and g + 8 of K, and of V: of these, or (f16) of 2 c, 2 c + 1,
       // 2 c + 8 and 2 c + 9 as pairs
-      float kf[2] = {sl.ks, sl.ks}, vf[2] = {sl.vs, sl.vs};
-      bool big = sl.key & BIG;
+      float kf[2] = {sl.ks, sl.ks}, vf[2] = {fabsf(sl.vs), fabsf(sl.vs)};
+      bool big = !(sl.vs > 0.f);
       uint32_t s01 = 0, s23 = 0;
       if (p.scale_shift == 0) {
-        const uint8_t* sk = s.scales[warp][from_stage][0];
-        const uint8_t* sv = s.scales[warp][from_stage][1];
-        const bool none = sl.key & NONE;
-        kf[0] = none ? 1.f : scale_float<BF16>(sk[g]);
-        kf[1] = none ? 1.f : scale_float<BF16>(sk[g + 8]);
+        // lane l makes the scale of K's key l, or V's key l - 16, of the bytes
+        const int sb = sl.key & NONE ? 127 : (&s.scales[warp][from_stage][0][0])[lane];
+        const float sf = scale_float<BF16>(sb);
+        kf[0] = __shfl_sync(0xffffffffu, sf, g);
+        kf[1] = __shfl_sync(0xffffffffu, sf, g + 8);
         if (BF16) {
-          const int lo = none ? 127 : sv[g], hi = none ? 127 : sv[g + 8];
-          vf[0] = scale_float<true>(lo);
-          vf[1] = scale_float<true>(hi);
-          if (!I8) big = __any_sync(0xffffffffu, max(lo, hi) > 127 + 7);
+          vf[0] = __shfl_sync(0xffffffffu, sf, g + 16);
+          vf[1] = __shfl_sync(0xffffffffu, sf, g + 24);
+          if (!I8) big = __any_sync(0xffffffffu, lane >= 16 && sb > 127 + 7);
         } else {
-          const uint32_t a = none ? 0x7f7fu : *reinterpret_cast<const uint16_t*>(sv + 2 * c);
-          const uint32_t b = none ? 0x7f7fu : *reinterpret_cast<const uint16_t*>(sv + 2 * c + 8);
-          s01 = (scale_pair<false>(a & 255) & 0xffffu) | (scale_pair<false>(a >> 8) << 16);
-          s23 = (scale_pair<false>(b & 255) & 0xffffu) | (scale_pair<false>(b >> 8) << 16);
+          const uint32_t h = scale_pair<false>(sb);
+          s01 = __byte_perm(__shfl_sync(0xffffffffu, h, 2 * c + 16),
+                            __shfl_sync(0xffffffffu, h, 2 * c + 17), 0x5410);
+          s23 = __byte_perm(__shfl_sync(0xffffffffu, h, 2 * c + 24),
+                            __shfl_sync(0xffffffffu, h, 2 * c + 25), 0x5410);
         }
       } else if (!BF16) {
-        s01 = s23 = pack2<false>(sl.vs, sl.vs);
+        s01 = s23 = pack2<false>(vf[0], vf[0]);
       }
       // ---- scores: f16 products with K's codes as A fragments, bytes 16 c on of rows g
       // and g + 8, then bytes 64 + 16 c on; two chains
@@ -607,7 +636,9 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
       u_at = u_cnt;
     }
 
-    // ---- the piece's end: the warps' shares meet, eight rows at a time
+    // ---- the piece's end: the warps' shares meet, eight rows at a time (and the next
+    // unit's rows of q are there behind the meeting)
+    copies_wait();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -679,6 +710,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
     }
     if (!R::Q_REGS) __syncthreads();  // Q is read by all
     slot = next_slot;
+    parity ^= 1;
   }
   __syncthreads();
   if (threadIdx.x == 0 && s.bad_page) atomicCAS(&wc.status->code, 0u, (unsigned)ATTN_ERR_INVALID_ARG);

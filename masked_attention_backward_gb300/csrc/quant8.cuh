@@ -144,10 +144,10 @@ __device__ __forceinline__ void cross_pairs(uint32_t a, uint32_t b, uint32_t (&d
       d[2 * i + 1] =
           add16x2<true>((z & 0x007f007fu) | 0x43004300u, (z & 0x00800080u) | 0xc300c300u);
     } else {
-      // byte << 4, its sign on from bit 11 to 15 (products, off the busier pipe); the
-      // other byte of the half comes down instead
+      // byte << 4, its sign on from bit 11 to 15 (products, off the busier pipe)
+      const uint32_t z = __byte_perm(y, 0, 0x4341);
       uint32_t e = (y & 0x00ff00ffu) * 16u + (y & 0x00800080u) * 240u;
-      uint32_t o = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
+      uint32_t o = z * 16u + (z & 0x00800080u) * 240u;
       if (!BITS) {
         e = mul16x2<true>(e, 0x7b807b80u);  // 2^120
         o = mul16x2<true>(o, 0x7b807b80u);
