@@ -19,6 +19,19 @@
 // Warps share nothing while they walk a unit's keys, 16 at a time each in turn:
 // each brings its own slices into a ring of its own.  At a piece's end the warps'
 // O, M and l meet in shared memory.
+//
+// mma.sync is the slow way on this chip: an m16n8k16 occupies its quarter of the SM for
+// about 32 cycles, so eight rows (16 of them a slice) take 128 cycles of the 176 that a
+// slice has at the copy rate, sixteen rows 256 and forty 640.  Up to eight rows that is
+// under the HBM time; to sixteen it is still less than the tiles of the tcgen05 kernel
+// cost (paged_fwd.cuh: 64 requests of five tokens, 40 rows, 420 us there and 780 here).
+//
+// Measured (one GB300), 64 single tokens at 9000 keys on average, 64/8 heads, 1.14 GB: e4m3
+// bf16 197 us, 5.8 TB/s (copy rate 6.7), e4m3 fp16 188, int8 fp16 200, int8 bf16 225, a
+// scale a token 244; two tokens each 318.  One token at 1000 keys 15 us: the line 2.5, the
+// first slices, the join.  On the way there: the tcgen05 kernel 719 us; this one with
+// cp.async of 16 bytes a lane, every code times 2^120 and bf16 scores 329; with f16 scores
+// of the codes themselves and V's codes as moved bits 237; slices by TMA 202.
 #include <type_traits>
 
 #include "paged_line.cuh"

@@ -59,6 +59,15 @@
 // code times scale, exactly (quant8.cuh), zeros for the rows that no row of the
 // unit sees.  Each looks the pages and scales of 16 of its steps up a batch ahead.
 // The softmax warps' registers come from the other warps' (setmaxnreg).
+// Bound by these warps: 1500 cycles a step where the products and softmax want 950
+// (codes in and out of shared memory and tiles in, 64 KB a step, and some 340
+// instructions a thread every other step).  Measured: 2 requests of 4 and 5 tokens at
+// 100000 keys, 32/4 heads, int8, 109 us (68 without the conversion); chunks of 1900
+// tokens over 8000 keys 626 us (435), which is why chunks take paged8_expand.cu where the
+// workspace has room.  Kept out: K's and V's tiles in rings of their own, 3 and 5 stages
+// (768); 256 query rows in two halves that share the tiles, one S buffer each (619 when
+// this took 813, but 120 for the two requests), or S beside P with half of Q in shared
+// memory (839).
 #pragma once
 #include <type_traits>
 
