@@ -897,8 +897,8 @@ def paged_workspace(q: torch.Tensor, cache, mask: Mask,
 def paged_fwd(q, cache, block_table, sink, mask: Mask, scale: float,
               ws: Optional[torch.Tensor] = None, out=None, stream=None):
     """Attention of the packed new tokens q [total_q, Hq, 128] over the cache, a
-    PagedCache or PagedCache8; returns (o, lse).  out: (o, lse) to write, of which lse may be None;
-    without it they belong to `stream`, as fwd's results do."""
+    PagedCache or PagedCache8; returns (o, lse).  out: (o, lse) to write, of which
+    lse may be None; without it they belong to `stream`, as fwd's results do."""
     cu, lens = mask.cu_seqlens_q, mask.seqlen_k
     if cu is None or lens is None or cu.numel() != lens.numel() + 1:
         raise ValueError("the mask needs cu_seqlens_q [B + 1] and seqlen_k [B]")

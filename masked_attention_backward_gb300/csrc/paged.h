@@ -86,8 +86,8 @@ cudaError_t launch_paged_fwd(bool bf16, const PagedParams& p, const CUtensorMap&
                              const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
 cudaError_t launch_paged8_fwd(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tQ,
                               const CUtensorMap& tK, const CUtensorMap& tV, cudaStream_t st);
-// Query rows (tokens times query heads of a kv head) of a request over 8-bit codes up to
-// which k_paged8_rows takes it.
+// Query rows (tokens times query heads of a kv head) over 8-bit codes up to which
+// k_paged8_rows takes a call, and requests beside chunks.
 constexpr int PAGED8_ROWS = 16;
 cudaError_t launch_paged8_rows(bool bf16, bool i8, const Paged8Params& p, const CUtensorMap& tK,
                                const CUtensorMap& tV, const void* q, cudaStream_t st);

@@ -20,18 +20,20 @@
 // each brings its own slices into a ring of its own.  At a piece's end the warps'
 // O, M and l meet in shared memory.
 //
-// mma.sync is the slow way on this chip: an m16n8k16 occupies its quarter of the SM for
-// about 32 cycles, so eight rows (16 of them a slice) take 128 cycles of the 176 that a
-// slice has at the copy rate, sixteen rows 256 and forty 640.  Up to eight rows that is
-// under the HBM time; to sixteen it is still less than the tiles of the tcgen05 kernel
-// cost (paged_fwd.cuh: 64 requests of five tokens, 40 rows, 420 us there and 780 here).
+// An m16n8k16 occupies its quarter of the SM for 8 cycles: eight rows want 128 of the
+// 706 that a quarter has for a slice at the copy rate, and the conversions and the rest
+// 466 instructions, 198 of them on the half-rate integer pipe.  Sixteen rows leave 12
+// warps' registers, forty 8, whose latencies then show: 64 requests of five tokens (40
+// rows) took 551 us in this form, 420 with the tiles of the tcgen05 kernel
+// (paged_fwd.cuh), which takes more than 16.
 //
 // Measured (one GB300), 64 single tokens at 9000 keys on average, 64/8 heads, 1.14 GB: e4m3
-// bf16 197 us, 5.8 TB/s (copy rate 6.7), e4m3 fp16 188, int8 fp16 200, int8 bf16 225, a
-// scale a token 244; two tokens each 318.  One token at 1000 keys 15 us: the line 2.5, the
+// bf16 197 us, 5.8 TB/s (copy rate 6.7), e4m3 fp16 187, int8 fp16 203, int8 bf16 228, a
+// scale a token 246; two tokens each 293.  One token at 1000 keys 15 us: the line 2.5, the
 // first slices, the join.  On the way there: the tcgen05 kernel 719 us; this one with
 // cp.async of 16 bytes a lane, every code times 2^120 and bf16 scores 329; with f16 scores
 // of the codes themselves and V's codes as moved bits 237; slices by TMA 202.
+#include <cfloat>
 #include <type_traits>
 
 #include "paged_line.cuh"
@@ -104,7 +106,8 @@ struct Pieces {
 template <int NT>
 struct Rows {
   // (NT 1 with 12 warps and two slices on their way: 64 tokens at 2000 to 16000 keys
-  // 223 us, 207 so; NT 2 with 16 and one 447, with 8 and two 332, 319 so)
+  // 223 us when this took 207; NT 2 with 16 and one 447, with 8 and two 332, when this
+  // took 319)
   static constexpr int WARPS = NT == 1 ? 16 : 12;
   static constexpr int LAG = NT == 1 ? 1 : 2;   // slices on their way while one is worked on
   static constexpr int STAGES = LAG + 1;
@@ -167,6 +170,10 @@ __device__ __forceinline__ void copies_commit() {
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
+
+// The maximum of a row that has seen nothing: above no finite score, and finite, so that
+// -inf less it is -inf.
+constexpr float NO_MAX = -FLT_MAX;
 
 // Unit of a bf16 unit's O: probabilities that meet e4m3's moved bits (2^120 too
 // small) come times 2^112.
@@ -386,7 +393,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
     more = s.unit[next_slot].N >= 0;
     page_nxt = more ? page_of(s.unit[next_slot], 0) : -1;
     uint32_t qf[R::Q_REGS ? 16 : 1];
-    float col[NT][2];  // what the scores of this thread's two rows are multiplied by
+    float col[NT][2];  // what the scores of this thread's two rows of each eight are multiplied by
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       uint4 v[4];
@@ -437,7 +444,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[t][i][j] = 0.f;
-      M[t][0] = M[t][1] = -INFINITY;
+      M[t][0] = M[t][1] = NO_MAX;
       l[t][0] = l[t][1] = 0.f;
     }
     const int cnt = slices(cur), rows = cur.n * p.group;
@@ -475,12 +482,12 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
         s01 = s23 = pack2<false>(vf[0], vf[0]);
       }
       // ---- scores: f16 products with K's codes as A fragments, bytes 16 c on of rows g
-      // and g + 8, then bytes 64 + 16 c on; two chains
-      float sc[NT][4], s1[NT][4];
+      // and g + 8, then bytes 64 + 16 c on; one tile in two chains
+      float sc[NT][4], s1[4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[t][j] = s1[t][j] = 0.f;
+        for (int j = 0; j < 4; ++j) sc[t][j] = s1[j] = 0.f;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint8_t* at = rk + ((g * 128 + ((c ^ g) << 4)) ^ (64 * hf));
@@ -495,7 +502,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
             const uint2 q = R::Q_REGS ? make_uint2(qf[(8 * hf + 2 * j) % 16],
                                                    qf[(8 * hf + 2 * j + 1) % 16])
                                       : s.q[R::Q_REGS ? 0 : t][4 * hf + j][lane];
-            mma16816<false>(hf ? s1[t] : sc[t], pa.x, pb.x, pa.y, pb.y, q.x, q.y);
+            mma16816<false>(NT == 1 && hf ? s1 : sc[t], pa.x, pb.x, pa.y, pb.y, q.x, q.y);
           }
         }
       }
@@ -525,14 +532,16 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
         vf[0] *= unit;
         vf[1] *= unit;
       }
-      uint32_t pf[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          sc[t][j] = (sc[t][j] + s1[t][j]) * (kf[j >> 1] * col[t][j & 1]);
-        if (masked) {
-          const int k0 = sl.key & ~15;
+          sc[t][j] = (NT == 1 ? sc[t][j] + s1[j] : sc[t][j]) * (kf[j >> 1] * col[t][j & 1]);
+      }
+      if (masked) {
+        const int k0 = sl.key & ~15;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int m = 8 * t + 2 * c + i;
@@ -545,17 +554,24 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
               if (!sees) sc[t][i + 2 * j] = -INFINITY;
             }
           }
-        }
-        // ---- the running maximum: moved when a score exceeds it by more than 8
-        const float m0 = fmaxf(sc[t][0], sc[t][2]), m1 = fmaxf(sc[t][1], sc[t][3]);
-        if (__any_sync(0xffffffffu, m0 > M[t][0] + RESCALE_LOG2 || m1 > M[t][1] + RESCALE_LOG2)) {
+      }
+      // ---- the running maxima: moved when a score exceeds one by more than 8
+      bool moves = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          moves = moves || fmaxf(sc[t][j], sc[t][j + 2]) > M[t][j] + RESCALE_LOG2;
+      if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float mx = j ? m1 : m0;
+            float mx = fmaxf(sc[t][j], sc[t][j + 2]);
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             if (mx > M[t][j] + RESCALE_LOG2) {
-              const float alpha = M[t][j] == -INFINITY ? 1.f : fast_exp2(M[t][j] - mx);
+              const float alpha = fast_exp2(M[t][j] - mx);
               M[t][j] = mx;
               l[t][j] *= alpha;
 #pragma unroll
@@ -565,13 +581,14 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
               }
             }
           }
-        }
-        // ---- probabilities as B fragments (a row that has seen nothing keeps its scores
-        // at -inf; 0 stands in for M)
-        const float n0 = M[t][0] == -INFINITY ? 0.f : M[t][0];
-        const float n1 = M[t][1] == -INFINITY ? 0.f : M[t][1];
-        float e[4] = {fast_exp2(sc[t][0] - n0), fast_exp2(sc[t][1] - n1),
-                      fast_exp2(sc[t][2] - n0), fast_exp2(sc[t][3] - n1)};
+      }
+      // ---- probabilities as B fragments
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = fast_exp2(sc[t][j] - M[t][j & 1]);
         l[t][0] += e[0] + e[2];
         l[t][1] += e[1] + e[3];
         if (BF16) {
@@ -597,14 +614,16 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
         for (int j = 0; j < 4; ++j)
           if (!w.sees(k0 + 2 * c + (j & 1) + 8 * (j >> 1))) v[j] = make_uint4(0u, 0u, 0u, 0u);
       }
-      const uint32_t vw[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
-                                 {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
       auto add_values = [&](auto bits) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = k == 0 ? v[j].x : k == 1 ? v[j].y : k == 2 ? v[j].z : v[j].w;
           uint32_t lo[4], hi[4];
-          cross_pairs<BF16, I8, decltype(bits)::value>(vw[0][k], vw[1][k], lo);
-          cross_pairs<BF16, I8, decltype(bits)::value>(vw[2][k], vw[3][k], hi);
+          cross_pairs<BF16, I8, decltype(bits)::value>(w[0], w[1], lo);
+          cross_pairs<BF16, I8, decltype(bits)::value>(w[2], w[3], hi);
           if (!BF16) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
