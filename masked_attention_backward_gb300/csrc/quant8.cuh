@@ -44,8 +44,12 @@ __device__ __forceinline__ float exp2_int(int e) {  // 2^e, -127 <= e <= 127
 template <bool I8>
 __device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d) {
   if (I8) {
-    return (uint32_t)(__float2int_rn(a) & 0xff) | (uint32_t)(__float2int_rn(b) & 0xff) << 8 |
-           (uint32_t)(__float2int_rn(c) & 0xff) << 16 | (uint32_t)__float2int_rn(d) << 24;
+    // 1.5 * 2^23 has a unit of 1 in its last place: the sum's rounding is the code's,
+    // and its low byte the code (conversions go at a quarter of the adds' rate)
+    constexpr float UNIT = 12582912.f;
+    const uint32_t lo = __byte_perm(__float_as_uint(a + UNIT), __float_as_uint(b + UNIT), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(c + UNIT), __float_as_uint(d + UNIT), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
   }
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
          (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
