@@ -190,8 +190,7 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
   using R = Rows<NT>;
   constexpr int WARPS = R::WARPS, STAGES = R::STAGES, LAG = R::LAG;
   extern __shared__ uint8_t smem_raw[];
-  typename R::Smem& s = *reinterpret_cast<typename R::Smem*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  typename R::Smem& s = *reinterpret_cast<typename R::Smem*>(smem_align1024(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;  // row and column pair of the fragments
   grid_launch_dependents();               // the join's blocks may wait beside this grid

@@ -174,8 +174,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   constexpr int STAGES = C::STAGES, LD_STAGES = C::LD_STAGES;
   constexpr int SM_WARP0 = C::SM_WARP0, AHEAD = C::AHEAD;
   extern __shared__ uint8_t smem_raw[];
-  Smem<FORM>& s = *reinterpret_cast<Smem<FORM>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                     ~uintptr_t(1023));
+  Smem<FORM>& s = *reinterpret_cast<Smem<FORM>*>(smem_align1024(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this CTA's own status word, which the join passes on
   WaitCtx wc{p.cta_status + blockIdx.x, &s.abort_flag, p.timeout_ns};

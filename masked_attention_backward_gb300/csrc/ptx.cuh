@@ -40,6 +40,13 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// The first 1024-byte boundary of dynamic shared memory.  An offset, not a rounded
+// pointer: the compiler then knows that accesses through it are to shared memory, and
+// makes them such, where a rounded one has generic accesses with 64-bit addresses.
+__device__ __forceinline__ uint8_t* smem_align1024(uint8_t* raw) {
+  return raw + (-smem_u32(raw) & 1023u);
+}
+
 // -------------------------------------------------------------- mbarrier ----
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
