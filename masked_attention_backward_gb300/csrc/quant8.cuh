@@ -90,6 +90,18 @@ __device__ __forceinline__ uint32_t add16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// (w & mask) | set in one instruction (the compiler takes two for two constants).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t set) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(set));
+  return d;
+}
+// int8 codes at the foot of w's halves as bf16: 128 + the low bits, less 128, or 256
+// for a set sign.
+__device__ __forceinline__ uint32_t bf16_of_i8(uint32_t w) {
+  return add16x2<true>(and_or(w, 0x007f007fu, 0x43004300u), and_or(w, 0x00800080u, 0xc300c300u));
+}
+
 // Codes to 16-bit values, exactly.
 //   int8: the byte becomes the low bits of a number whose exponent makes its
 //     unit 1 (f16: 1024 + (c + 128); bf16, which has seven bits below the first:
@@ -106,10 +118,8 @@ __device__ __forceinline__ uint2 word_pairs(uint32_t w) {
                       add16x2<false>(__byte_perm(u, 0x64646464u, 0x4342), 0xe480e480u));
   }
   if (I8) {
-    // 128 + low bits, less 128, or 256 for a set sign
-    const uint32_t a = __byte_perm(w, 0, 0x4140), b = __byte_perm(w, 0, 0x4342);
-    return make_uint2(add16x2<true>((a & 0x007f007fu) | 0x43004300u, (a & 0x00800080u) | 0xc300c300u),
-                      add16x2<true>((b & 0x007f007fu) | 0x43004300u, (b & 0x00800080u) | 0xc300c300u));
+    return make_uint2(bf16_of_i8(__byte_perm(w, 0, 0x4140)),
+                      bf16_of_i8(__byte_perm(w, 0, 0x4342)));
   }
   if (!BF16) {
     uint2 d;
@@ -121,8 +131,8 @@ __device__ __forceinline__ uint2 word_pairs(uint32_t w) {
   }
   const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
   return make_uint2(
-      mul16x2<true>(((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), 0x7b807b80u),  // 2^120
-      mul16x2<true>(((b >> 4) & 0x07f007f0u) | (b & 0x80008000u), 0x7b807b80u));
+      mul16x2<true>(and_or(a, 0x80008000u, (a >> 4) & 0x07f007f0u), 0x7b807b80u),  // 2^120
+      mul16x2<true>(and_or(b, 0x80008000u, (b >> 4) & 0x07f007f0u), 0x7b807b80u));
 }
 
 // The codes of words a and b as pairs (a's byte i, b's byte i).
@@ -143,10 +153,8 @@ __device__ __forceinline__ void cross_pairs(uint32_t a, uint32_t b, uint32_t (&d
       d[2 * i] = add16x2<false>(__byte_perm(u, 0x64646464u, 0x4240), 0xe480e480u);
       d[2 * i + 1] = add16x2<false>(__byte_perm(u, 0x64646464u, 0x4341), 0xe480e480u);
     } else if (I8) {
-      const uint32_t z = y >> 8;
-      d[2 * i] = add16x2<true>((y & 0x007f007fu) | 0x43004300u, (y & 0x00800080u) | 0xc300c300u);
-      d[2 * i + 1] =
-          add16x2<true>((z & 0x007f007fu) | 0x43004300u, (z & 0x00800080u) | 0xc300c300u);
+      d[2 * i] = bf16_of_i8(y);
+      d[2 * i + 1] = bf16_of_i8(y >> 8);
     } else {
       // byte << 4, its sign on from bit 11 to 15 (products, off the busier pipe)
       const uint32_t z = __byte_perm(y, 0, 0x4341);
@@ -172,12 +180,11 @@ __device__ __forceinline__ uint2 tile_words(uint32_t w, uint32_t scale2) {
   if (!BF16) {
     v = word_pairs<false, I8>(w);
   } else if (I8) {
-    const uint32_t z = w >> 8;
-    v.x = add16x2<true>((w & 0x007f007fu) | 0x43004300u, (w & 0x00800080u) | 0xc300c300u);
-    v.y = add16x2<true>((z & 0x007f007fu) | 0x43004300u, (z & 0x00800080u) | 0xc300c300u);
+    v.x = bf16_of_i8(w);
+    v.y = bf16_of_i8(w >> 8);
   } else {
     v.x = (w & 0x00ff00ffu) * 16u + (w & 0x00800080u) * 240u;
-    v.y = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+    v.y = and_or(w, 0x80008000u, (w >> 4) & 0x07f007f0u);
     if (!SMALL) {
       v.x = mul16x2<true>(v.x, 0x7b807b80u);  // 2^120
       v.y = mul16x2<true>(v.y, 0x7b807b80u);
