@@ -58,7 +58,6 @@
 // that take steps in turn, each warp 16 rows of K and of V, half a row a thread:
 // code times scale, exactly (quant8.cuh), zeros for the rows that no row of the
 // unit sees.  Each looks the pages and scales of 16 of its steps up a batch ahead.
-// The softmax warps' registers come from the other warps' (setmaxnreg).
 // Bound by these warps: 1500 cycles a step where the products and softmax want 950
 // (codes in and out of shared memory and tiles in, 64 KB a step, and some 340
 // instructions a thread every other step).  Measured: 2 requests of 4 and 5 tokens at
@@ -94,17 +93,17 @@ struct Cfg {
   static constexpr bool Q8 = FORM != ROWS16;
   static constexpr int STAGES = Q8 ? 4 : 5;     // ring of 16-bit K / V tiles
   static constexpr int LD_STAGES = Q8 ? 3 : 5;  // ring that the loads go to
+  // Barriers of the loads: step m's is m % LD_BARS.  A warp may wait for a phase only
+  // when it has seen the one before it complete (a parity says no more), and the two
+  // converting sets take steps in turn: an even number gives each its own barriers.
+  // (With one a stage a set came to the third step after another one's whose load was
+  // still under way, took it for complete, and freed a stage that was being filled.)
+  static constexpr int LD_BARS = Q8 ? 2 * LD_STAGES : LD_STAGES;
   static constexpr int SM_WARP0 = Q8 ? 4 : 3;   // first softmax warp
   static constexpr int CV_WARP0 = SM_WARP0 + SM_WARPS;
   static constexpr int NUM_THREADS = 32 * (CV_WARP0 + (Q8 ? CV_WARPS : 0));
   static constexpr int AHEAD = 8;               // steps of a unit issued before the next one's Q
-  // registers of the warps that wait and convert (12), and of the softmax warps (8):
-  // of 20 * 96 that are launched
-  static constexpr int REGS_FEW = 72, REGS_SOFTMAX = 128;
 };
-static_assert(12 * Cfg<CODES_I8>::REGS_FEW + 8 * Cfg<CODES_I8>::REGS_SOFTMAX <= 20 * 96 &&
-                  Cfg<CODES_I8>::NUM_THREADS == 20 * 32,
-              "shares of the launch's registers");
 
 // What the converting warps add: the codes' ring (128B swizzle), and the scales
 // of each warp's 16 rows, two batches: [warp][batch][step][K, V][row]; which of the
@@ -115,7 +114,7 @@ struct __align__(1024) Smem8 {
   uint8_t V8[LD_STAGES][Q_SUB * 128];
   uint8_t scales[CV_WARPS][2][CV_BATCH][2][16];
   uint32_t seen[CV_WARPS][2][CV_BATCH];
-  uint64_t bar_ld_full[LD_STAGES];
+  uint64_t bar_ld_full[2 * LD_STAGES];
   uint64_t bar_ld_empty[LD_STAGES];
 };
 struct Smem16 {};
@@ -189,9 +188,9 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       mbar_init(smem_u32(&s.bar_kv_empty[i]), 1);
     }
     if constexpr (Q8)
-      for (int i = 0; i < LD_STAGES; ++i) {
+      for (int i = 0; i < C::LD_BARS; ++i) {
         mbar_init(smem_u32(&s.bar_ld_full[i]), 1);
-        mbar_init(smem_u32(&s.bar_ld_empty[i]), CV_WARPS / 2);
+        if (i < LD_STAGES) mbar_init(smem_u32(&s.bar_ld_empty[i]), CV_WARPS / 2);
       }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s.bar_s_full[i >> 1][i & 1]), 1);
@@ -240,6 +239,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   // that is free; midway() before step AHEAD.
   int m_load = 0;  // steps issued, across units
   Cyc<LD_STAGES> rg_load;
+  Cyc<C::LD_BARS> rg_bar;
   uint64_t *ld_full = s.bar_kv_full, *ld_empty = s.bar_kv_empty;
   if constexpr (Q8) {
     ld_full = s.bar_ld_full;
@@ -265,7 +265,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       return seen(i, k0) ? __ldg(row + idx) : p.num_pages;
     };
     int page = p.num_pages, prow = 0, next = pages_of(s0), next_row = row0, left = 0;
-    for (int i = s0; i < s0 + N; ++i, ++m_load, rg_load.next(), --left) {
+    for (int i = s0; i < s0 + N; ++i, ++m_load, rg_load.next(), rg_bar.next(), --left) {
       const int st = rg_load.i;
       if (i == s0 + AHEAD && !midway()) return false;
       if (left == 0) {
@@ -284,7 +284,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
           !mbar_wait_sleep_warp(smem_u32(&ld_empty[st]), rg_load.ph ^ 1u, wc,
                                 Q8 ? TAG_LD_EMPTY : TAG_KV_EMPTY, LOAD_SLEEP_NS))
         return false;
-      const uint32_t fb = smem_u32(&ld_full[st]);
+      const uint32_t fb = smem_u32(&ld_full[rg_bar.i]);
       if (lane == 0) mbar_arrive_expect_tx(fb, (Q8 ? 2 : 4) * Q_SUB * 128);
       __syncwarp();
       uint32_t dst_k, dst_v;
@@ -311,15 +311,8 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
   // a CTA that gives up lets the copies still in flight land first
   auto drain_loads = [&]() {
     for (int k = m_load > LD_STAGES ? m_load - LD_STAGES : 0; k < m_load; ++k)
-      mbar_drain_warp(smem_u32(&ld_full[k % LD_STAGES]), (k / LD_STAGES) & 1, wc.timeout_ns);
+      mbar_drain_warp(smem_u32(&ld_full[k % C::LD_BARS]), (k / C::LD_BARS) & 1, wc.timeout_ns);
   };
-
-  if constexpr (Q8) {
-    if (warp >= SM_WARP0 && warp < C::CV_WARP0)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_FEW));
-  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ loader of Q and K
@@ -767,20 +760,44 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
           return false;
         const float nm = minus_max();
         const float2 nm2 = make_float2(nm, nm);
-        uint32_t pk[32];
-        float2 lp[4];
+        if constexpr (Q8) {
+          // the logits are read again, 32 at a time: 64 beside their probabilities are
+          // more than the registers of 20 warps hold
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) lp[c] = make_float2(0.f, 0.f);
+          for (int q = 0; q < 2; ++q) {
+            float v[32];
+            tmem_ld32(col + 32 * q, v);
+            tmem_wait_ld_regs(v);
+            uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 xx = ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nm2);
-          const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
-          lp[c & 3] = fadd2(lp[c & 3], pp);
-          pk[c] = pack2<BF16>(pp.x, pp.y);
+            for (int c = 0; c < 16; ++c) {
+              const float2 xx = ffma2(make_float2(v[2 * c], v[2 * c + 1]), sc2, nm2);
+              const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+              ls[c & 1] = fadd2(ls[c & 1], pp);
+              pk[c] = pack2<BF16>(pp.x, pp.y);
+            }
+            // over columns that have been read: 16 q + 15 < 32 q + 32
+            tmem_st16(col + 16 * q, pk);
+          }
+          const float2 x = fadd2(ls[0], ls[1]);
+          l += x.x + x.y;
+        } else {
+          uint32_t pk[32];
+          float2 lp[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) lp[c] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float2 xx = ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nm2);
+            const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+            lp[c & 3] = fadd2(lp[c & 3], pp);
+            pk[c] = pack2<BF16>(pp.x, pp.y);
+          }
+          const float2 ls = fadd2(fadd2(lp[0], lp[1]), fadd2(lp[2], lp[3]));
+          l += ls.x + ls.y;
+          tmem_st32(col, pk);
         }
-        const float2 ls = fadd2(fadd2(lp[0], lp[1]), fadd2(lp[2], lp[3]));
-        l += ls.x + ls.y;
-        tmem_st32(col, pk);
         tmem_wait_st();
         return true;
       };
@@ -866,6 +883,7 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       // this thread's row of a step, and which half of it
       const int srow = lane >> 1, row = 16 * slice + srow, half = lane & 1;
       bool ok = true;
+      static_assert(STAGES % 2 == 0 && C::LD_BARS % 2 == 0, "a barrier belongs to one set");
       int m0 = 0;  // steps of the units so far; a set takes every other one
       for (int j = 0; ok; ++j) {
         if (!mbar_wait_warp(smem_u32(&s.bar_q_full), j & 1, wc, TAG_Q)) break;
@@ -927,7 +945,8 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
           const int m = m0 + i, ld = m % LD_STAGES, kv = m % STAGES;
           const uint32_t bits = s.seen[cw][bt][bi];
           const bool small = BF16 && !I8 && !(bits >> 16);
-          ok = mbar_wait_warp(smem_u32(&s.bar_ld_full[ld]), (m / LD_STAGES) & 1, wc, TAG_LD_FULL);
+          ok = mbar_wait_warp(smem_u32(&s.bar_ld_full[m % C::LD_BARS]), (m / C::LD_BARS) & 1, wc,
+                              TAG_LD_FULL);
           if (ok && m >= STAGES)
             ok = mbar_wait_warp(smem_u32(&s.bar_kv_empty[kv]), (m / STAGES + 1) & 1, wc,
                                 TAG_KV_EMPTY);

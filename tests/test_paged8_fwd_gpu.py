@@ -361,6 +361,49 @@ def test_repeats_are_equal(cuda_lib):
             assert torch.equal(o, o0) and torch.equal(lse, l0)
 
 
+@pytest.mark.parametrize("reqs,Hq,Hkv,window,code", [
+    ([(500, 9826)] + [(1 + i % 4, 1700 + 900 * i) for i in range(15)], 32, 8, 1024, "e4m3"),
+    ([(5, 60000), (4, 50000)], 32, 4, 0, "i8"),
+    ([(1, 3000 + 1000 * i) for i in range(12)], 32, 8, 0, "e4m3")])
+def test_repeats_are_equal_from_cold_memory(cuda_lib, monkeypatch, reqs, Hq, Hkv, window, code):
+    """Calls one behind another over caches that push one another out of the L2, so
+    that loads arrive late and out of their order."""
+    monkeypatch.delenv("MASKATTN_PAGED8_ROOM")
+    g = torch.Generator("cuda").manual_seed(3)
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    ps = 32
+    held = [-(-L // ps) for _, L in reqs]
+    new = [n for n, _ in reqs]
+    cu = [sum(new[:b]) for b in range(len(new) + 1)]
+    mask = mab.Mask(kind=FIRST if window else CAUSAL, window=window, first=4 if window else 0,
+                    cu_seqlens_q=i(cu), seqlen_k=i([L for _, L in reqs]), total_q=sum(new),
+                    max_seqlen_q=max(new), max_seqlen_k=max(L for _, L in reqs))
+    states = []
+    for _ in range(3):
+        P = sum(held) + 900
+        cache = mab.PagedCache8.empty(P, Hkv, ps, 1, torch.int8 if code == "i8" else
+                                      torch.float8_e4m3fn, F16, "NHD")
+        for t in (cache.k_pages, cache.v_pages):
+            u = torch.randint(0, 120, t.shape, generator=g, device="cuda", dtype=torch.uint8)
+            t.view(torch.uint8).copy_(u | torch.randint(0, 2, t.shape, generator=g, device="cuda",
+                                                        dtype=torch.uint8) << 7)
+        for t in (cache.k_scales, cache.v_scales):
+            t.copy_(torch.randint(116, 121, t.shape, generator=g, device="cuda"))
+        ids = torch.randperm(P, generator=g, device="cuda").int()
+        table = torch.zeros(len(reqs), max(held), dtype=torch.int32, device="cuda")
+        for b, h in enumerate(held):
+            table[b, :h] = ids[sum(held[:b]):sum(held[:b]) + h]
+        q = torch.randn(sum(new), Hq, 128, generator=g, device="cuda").to(F16)
+        states.append((q, cache, table))
+    run = lambda st: mab.paged_fwd(st[0], st[1], st[2], None, mask, SCALE)
+    first = [run(st) for st in states]
+    for _ in range(8):
+        again = [run(states[k % 3]) for k in range(48)]
+        for k, (o, lse) in enumerate(again):
+            assert torch.equal(o, first[k % 3][0]) and torch.equal(lse, first[k % 3][1])
+        del again
+
+
 def test_no_lse_and_other_stream(cuda_lib):
     c = Case([(1, 300), (70, 100)], form=("i8", BF16))
     st = torch.cuda.Stream()
