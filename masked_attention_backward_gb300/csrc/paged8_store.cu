@@ -51,20 +51,23 @@ template <bool BF16, bool I8>
 __device__ __forceinline__ uint2 quantise(uint4 v, int s) {
   if (s == SCALE_NAN) return make_uint2(0u, 0u);
   const float unit = exp2_int(127 - s);
-  float f[8];
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // (two ways, so that the usual one has product and int8 rounding in one instruction:
+  // the product is exact)
+  auto codes = [&](auto top) {
+    uint32_t r[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = unpack2<BF16>(w[i]);
-    f[2 * i] = x.x * unit;
-    f[2 * i + 1] = x.y * unit;
-  }
+    for (int i = 0; i < 2; ++i) {
+      const float2 x = unpack2<BF16>(w[2 * i]), y = unpack2<BF16>(w[2 * i + 1]);
+      r[i] = codes_of<I8>(top(x.x * unit), top(x.y * unit), top(y.x * unit), top(y.y * unit));
+    }
+    return make_uint2(r[0], r[1]);
+  };
   if (s >= CodeRange<BF16, I8>::big) {
     constexpr float T = CodeRange<BF16, I8>::big_top;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i], -T), T);
+    return codes([](float f) { return fminf(fmaxf(f, -T), T); });
   }
-  return make_uint2(codes_of<I8>(f[0], f[1], f[2], f[3]), codes_of<I8>(f[4], f[5], f[6], f[7]));
+  return codes([](float f) { return f; });
 }
 
 // Eight codes moved from scale byte s0 to s1 > s0.
