@@ -60,8 +60,8 @@ int few_tokens(const attn_shape_t* sh) { return PAGED8_ROWS / (sh->Hq / sh->Hkv)
 
 // Steps (64 keys of a query tile) that an SM has at least, going by the call's bounds,
 // when its chunks' rows are written in 16 bits first.  Four chunks of 256 tokens over 2000
-// keys, 32/8 heads, 54 steps: 64 us so, 74 with tiles made inside the attention; 15 single
-// tokens and a chunk of 500 under a window of 1024, 24 steps: 68 and 56 (two kernels more,
+// keys, 32/8 heads, 54 steps: 63 us so, 72 with tiles made inside the attention; 15 single
+// tokens and a chunk of 500 under a window of 1024, 24 steps: 64 and 52 (two kernels more,
 // and two joins, for the single tokens).
 constexpr int EXPAND_STEPS = 40;
 

@@ -28,8 +28,8 @@
 // (paged_fwd.cuh), which takes more than 16.
 //
 // Measured (one GB300), 64 single tokens at 9000 keys on average, 64/8 heads, 1.14 GB: e4m3
-// bf16 197 us, 5.8 TB/s (copy rate 6.7), e4m3 fp16 187, int8 fp16 203, int8 bf16 228, a
-// scale a token 246; two tokens each 293.  One token at 1000 keys 15 us: the line 2.5, the
+// bf16 195 us, 5.9 TB/s (copy rate 6.7), e4m3 fp16 184, int8 fp16 193, int8 bf16 197, a
+// scale a token 212; two tokens each 293.  One token at 1000 keys 15 us: the line 2.5, the
 // first slices, the join.  On the way there: the tcgen05 kernel 719 us; this one with
 // cp.async of 16 bytes a lane, every code times 2^120 and bf16 scores 329; with f16 scores
 // of the codes themselves and V's codes as moved bits 237; slices by TMA 202.

@@ -58,15 +58,21 @@
 // that take steps in turn, each warp 16 rows of K and of V, half a row a thread:
 // code times scale, exactly (quant8.cuh), zeros for the rows that no row of the
 // unit sees.  Each looks the pages and scales of 16 of its steps up a batch ahead.
-// Bound by these warps: 1500 cycles a step where the products and softmax want 950
-// (codes in and out of shared memory and tiles in, 64 KB a step, and some 340
-// instructions a thread every other step).  Measured: 2 requests of 4 and 5 tokens at
-// 100000 keys, 32/4 heads, int8, 109 us (68 without the conversion); chunks of 1900
-// tokens over 8000 keys 626 us (435), which is why chunks take paged8_expand.cu where the
-// workspace has room.  Kept out: K's and V's tiles in rings of their own, 3 and 5 stages
-// (768); 256 query rows in two halves that share the tiles, one S buffer each (619 when
-// this took 813, but 120 for the two requests), or S beside P with half of Q in shared
-// memory (839).
+// Bound by these warps beside the softmax: 3200 warp instructions a step, half of
+// them theirs, on pipes of half rate, and a chain of tile, S, softmax and P V over
+// four tiles (a step takes 1600 cycles; its bytes 700, the products 540).
+// Measured: 2 requests of 4 and 5 tokens at 100000 keys, 32/4 heads, int8, 88 us;
+// 64 requests of 5 tokens at 9000, 64/8 heads, e4m3, 403; chunks of 1900 tokens over
+// 8000 keys 603 us, which is why chunks take paged8_expand.cu where the workspace has
+// room.  What made the two requests 109 to 88: shared memory reached as such
+// (smem_align1024) 93, int8's masks in one instruction each 88.  Kept out: K's and V's
+// tiles in rings of their own, 3 and 5 stages (chunks 768 when this took 626); three
+// tiles and five stages of codes (two requests 118 of 109); a warp to K or to V alone,
+// every step (122 of 109); K's tile reported before V's (113 of 109); the codes read
+// ahead so that their stage is free sooner (93 of 88); more registers to the softmax
+// warps from the others (setmaxnreg; 88 and 88, 64 requests 413 and 403); 256 query rows
+// in two halves that share the tiles, one S buffer each (chunks 619 of 813, the two
+// requests 120), or S beside P with half of Q in shared memory (839).
 #pragma once
 #include <type_traits>
 
