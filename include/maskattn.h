@@ -432,14 +432,14 @@ attn_status_t attn_paged8_load(const attn_pages8_t* pages, int B, int total, con
  * bytes for each key (up to Skv, or those of the window) of each kv head and request
  * that may have a chunk, where the bounds say that there is work enough.  With that much
  * attn_paged8_fwd writes them there once; with less every query tile makes them anew
- * (chunks of 1900 tokens over 8000 keys: 389 and 626 us).  The results of both differ by
+ * (chunks of 1900 tokens over 8000 keys: 389 and 603 us).  The results of both differ by
  * roundings. */
 attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, const attn_mask_desc_t* mask,
                                          size_t* bytes);
 
 /* attn_paged_fwd over an 8-bit cache: the attention over the values that the codes
- * and scales stand for, exactly (attn_paged8_load gives the same ones); masks, lengths, results and statuses as attn_paged_fwd
- * has them.  A block whose scale is 255 reads as NaN, which a new token must not see,
+ * and scales stand for, exactly (attn_paged8_load gives the same ones); masks,
+ * lengths, results and statuses as attn_paged_fwd has them.  A block whose scale is 255 reads as NaN, which a new token must not see,
  * as it must not see other values that are not finite. */
 attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pages, const void* q,
                               const void* k_pages, const void* v_pages, const uint8_t* k_scales,
