@@ -439,8 +439,9 @@ attn_status_t attn_paged8_workspace_size(const attn_shape_t* shape, const attn_m
 
 /* attn_paged_fwd over an 8-bit cache: the attention over the values that the codes
  * and scales stand for, exactly (attn_paged8_load gives the same ones); masks,
- * lengths, results and statuses as attn_paged_fwd has them.  A block whose scale is 255 reads as NaN, which a new token must not see,
- * as it must not see other values that are not finite. */
+ * lengths, results and statuses as attn_paged_fwd has them.  A block whose scale is
+ * 255 reads as NaN, which a new token must not see, as it must not see other values
+ * that are not finite. */
 attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pages, const void* q,
                               const void* k_pages, const void* v_pages, const uint8_t* k_scales,
                               const uint8_t* v_scales, const int* block_table, int table_stride,

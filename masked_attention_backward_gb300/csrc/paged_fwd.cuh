@@ -43,7 +43,7 @@
 //
 // Measured (one GB300, bf16 unless stated): 64 single tokens at 9000 keys, 64/8
 // heads, 0.345 ms, 6.84 TB/s (16-token pages, [page, row, head], 6.6); 2 at
-// 100000 keys, 32/4 heads, 73 us, 5.6 TB/s; 200 at 300 keys, 32/8 heads, 67 us,
+// 100000 keys, 32/4 heads, 73 us, 5.6 TB/s; 200 at 300 keys, 32/8 heads, 65 us,
 // latency bound (a unit's start and end, about 5000 cycles, beside 5 steps);
 // chunks of 2048 over 9000 keys, 32/8 heads, 0.44 ms, 1215 TFLOP/s, bound by
 // the latency of S, softmax and P V over three buffers (tensor pipe 56 %
@@ -62,16 +62,17 @@
 // them theirs, on pipes of half rate, and a chain of tile, S, softmax and P V over
 // four tiles (a step takes 1600 cycles; its bytes 700, the products 540).
 // Measured: 2 requests of 4 and 5 tokens at 100000 keys, 32/4 heads, int8, 88 us;
-// 64 requests of 5 tokens at 9000, 64/8 heads, e4m3, 403; chunks of 1900 tokens over
-// 8000 keys 603 us, which is why chunks take paged8_expand.cu where the workspace has
+// 64 requests of 5 tokens at 9000, 64/8 heads, e4m3, 403; 15 requests of 1 to 4 tokens
+// and a chunk of 500 under a window of 1024, 32/8 heads, fp16, 51; chunks of 1900 tokens
+// over 8000 keys 603, which is why chunks take paged8_expand.cu where the workspace has
 // room.  What made the two requests 109 to 88: shared memory reached as such
 // (smem_align1024) 93, int8's masks in one instruction each 88.  Kept out: K's and V's
 // tiles in rings of their own, 3 and 5 stages (chunks 768 when this took 626); three
 // tiles and five stages of codes (two requests 118 of 109); a warp to K or to V alone,
-// every step (122 of 109); K's tile reported before V's (113 of 109); the codes read
-// ahead so that their stage is free sooner (93 of 88); more registers to the softmax
-// warps from the others (setmaxnreg; 88 and 88, 64 requests 413 and 403); 256 query rows
-// in two halves that share the tiles, one S buffer each (chunks 619 of 813, the two
+// every step (122 of 109); K's tile reported before V's (90 of 88.7, the window of 1024
+// 54 of 51); the codes read ahead so that their stage is free sooner (91 of 88.7,
+// 64 requests 400 of 403); more registers to the softmax warps from the others
+// (setmaxnreg; 88 and 88, 64 requests 413 and 403); 256 query rows in two halves that share the tiles, one S buffer each (chunks 619 of 813, the two
 // requests 120), or S beside P with half of Q in shared memory (839).
 #pragma once
 #include <type_traits>
