@@ -72,8 +72,9 @@
 // every step (122 of 109); K's tile reported before V's (90 of 88.7, the window of 1024
 // 54 of 51); the codes read ahead so that their stage is free sooner (91 of 88.7,
 // 64 requests 400 of 403); more registers to the softmax warps from the others
-// (setmaxnreg; 88 and 88, 64 requests 413 and 403); 256 query rows in two halves that share the tiles, one S buffer each (chunks 619 of 813, the two
-// requests 120), or S beside P with half of Q in shared memory (839).
+// (setmaxnreg; 88 and 88, 64 requests 413 and 403); 256 query rows in two halves that
+// share the tiles, one S buffer each (chunks 619 of 813, the two requests 120), or S
+// beside P with half of Q in shared memory (839).
 #pragma once
 #include <type_traits>
 
