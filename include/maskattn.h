@@ -406,9 +406,10 @@ typedef struct {
  * undefined, nothing else).  Where they begin at the block's row 0 the block begins
  * anew, whatever it held.  Where they begin at a row r > 0 its rows before r stay:
  * the block keeps the larger of its scale and the one that the new rows need, and if
- * that is the new one the earlier rows' codes are rounded in units of it.  Rows of
- * the block past the new ones mean nothing afterwards.  A value that is not finite
- * makes the scale 255: the block reads as NaN until it begins anew. */
+ * that is the new one the earlier rows' codes are rounded in units of it, held back
+ * as the new ones are.  Rows of the block past the new ones mean nothing afterwards.
+ * A value that is not finite makes the scale 255: the block reads as NaN until it
+ * begins anew. */
 attn_status_t attn_paged8_store(const attn_pages8_t* pages, int T, const void* k, const void* v,
                                 long long k_stride, long long v_stride, const long long* slot_map,
                                 void* k_pages, void* v_pages, uint8_t* k_scales,

@@ -71,10 +71,13 @@ __device__ __forceinline__ uint2 quantise(uint4 v, int s) {
   return codes([](float f) { return f; });
 }
 
-// Eight codes moved from scale byte s0 to s1 > s0.
-template <bool I8>
+// Eight codes moved from scale byte s0 to s1 > s0.  (int8's 127 becomes 63.5, which rounds to
+// 64: held back like the new rows' codes where 64 has no finite value.  e4m3's 448 becomes 224,
+// below its 240.)
+template <bool BF16, bool I8>
 __device__ __forceinline__ uint2 rescale(uint2 c, int s0, int s1) {
   const float unit = exp2_int(max(s0 - s1, -126));
+  const float top = s1 >= CodeRange<BF16, I8>::big ? CodeRange<BF16, I8>::big_top : 127.f;
   uint32_t r[2];
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
@@ -86,6 +89,10 @@ __device__ __forceinline__ uint2 rescale(uint2 c, int s0, int s1) {
     f[1] = x.y * unit;
     f[2] = y.x * unit;
     f[3] = y.y * unit;
+    if (I8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = fminf(fmaxf(f[j], -top), top);
+    }
     r[i] = codes_of<I8>(f[0], f[1], f[2], f[3]);
   }
   return make_uint2(r[0], r[1]);
@@ -204,7 +211,7 @@ k_paged8_store_blocks(const Pages8 pg, const uint4* __restrict__ k, const uint4*
       // the rows that were there, in units of the new scale
       for (int r = half; r < r0; r += 2) {
         uint2* c = reinterpret_cast<uint2*>(at - (r0 - r) * pg.token_stride) + l16;
-        *c = rescale<I8>(*c, had, s);
+        *c = rescale<BF16, I8>(*c, had, s);
       }
     }
     __syncwarp();  // every lane has read the old scale
