@@ -210,10 +210,14 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
     if (!pages_maps(p.box_rows)) return ATTN_ERR_CUDA;
     return cuda_status(launch_paged8_fwd(bf16, i8, p, tQ, tK, tV, st));
   }
-  // Chunks: the requests with few rows first, unless the tokens leave room for none ...
+  // Chunks: the requests with few rows first, unless q has rows enough for every request to
+  // have more.  (It may have rows that no request owns, as a captured call's does: its lengths
+  // may be any then too, and the kernels behind take every request.  The room holds them: more
+  // than (B - 1) Sq + small rows, Sq > small, are B (small + 1) at least, so it was made for B.)
   const int small = few_tokens(shape);
-  const bool some_few = mask->total_q <= (long long)(shape->B - 1) * shape->Sq + small;
-  if (some_few && small > 0) {
+  const bool split =
+      small > 0 && mask->total_q <= (long long)(shape->B - 1) * shape->Sq + small;
+  if (split) {
     Paged8Params f = p;
     f.tokens_hi = small;
     f.tile_tokens = small;
@@ -223,7 +227,7 @@ attn_status_t attn_paged8_fwd(const attn_shape_t* shape, const attn_pages8_t* pa
     p.keep_status = 1;
   }
   // ... then the others' rows in 16 bits, and the attention over them.
-  p.tokens_lo = small;
+  p.tokens_lo = split ? small : 0;
   uint8_t* w = static_cast<uint8_t*>(ws);
   Expanded e;
   e.k = reinterpret_cast<uint16_t*>(w + L.k);
