@@ -10,6 +10,7 @@ import contextlib
 import ctypes
 import functools
 import math
+import os
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -866,7 +867,9 @@ PAGED8_ROOM = 2 << 30
 
 
 @functools.lru_cache(maxsize=256)
-def _paged_workspace_bytes(shape, mask) -> int:
+def _paged_workspace_bytes(shape, mask, most=0, hook=None) -> int:
+    """mask: what of it the 8-bit cache's workspace depends on; most: PAGED8_ROOM; hook:
+    MASKATTN_PAGED8_ROOM, which the library reads."""
     sh = attn_shape_t(*shape, 0)
     if mask is None:
         r, n = attn_paged_workspace_size(sh)
@@ -876,7 +879,7 @@ def _paged_workspace_bytes(shape, mask) -> int:
             kind, window, first, total_q = mask
             _, more = attn_paged8_workspace_size(
                 sh, attn_mask_desc_t(kind=kind, window=window, first=first, total_q=total_q))
-            n = more if more - n <= PAGED8_ROOM else n
+            n = more if more - n <= most else n
     if r != ATTN_OK:
         raise AttnError(r, "attn_paged_workspace_size" if mask is None else
                         "attn_paged8_workspace_size")
@@ -888,9 +891,12 @@ def paged_workspace(q: torch.Tensor, cache, mask: Mask,
     """A workspace of paged_fwd; for a PagedCache8 and chunks with room for the rows
     that they see in 16 bits, up to PAGED8_ROOM bytes."""
     sh = shape or paged_shape(q, cache, mask)
-    n = _paged_workspace_bytes((sh.B, sh.Hq, sh.Hkv, sh.Sq, sh.Skv, sh.D, sh.dtype),
-                               (mask.kind, mask.window, mask.first, mask.total_q)
-                               if isinstance(cache, PagedCache8) else None)
+    sizes = (sh.B, sh.Hq, sh.Hkv, sh.Sq, sh.Skv, sh.D, sh.dtype)
+    if isinstance(cache, PagedCache8):
+        n = _paged_workspace_bytes(sizes, (mask.kind, mask.window, mask.first, mask.total_q),
+                                   PAGED8_ROOM, os.environ.get("MASKATTN_PAGED8_ROOM"))
+    else:
+        n = _paged_workspace_bytes(sizes, None)
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
