@@ -867,44 +867,51 @@ PAGED8_ROOM = 2 << 30
 
 
 @functools.lru_cache(maxsize=256)
-def _paged_workspace_bytes(shape, mask, most=0, hook=None) -> int:
-    """mask: what of it the 8-bit cache's workspace depends on; most: PAGED8_ROOM; hook:
-    MASKATTN_PAGED8_ROOM, which the library reads."""
+def _paged_workspace_bytes(shape, mask, most=0, hook=None):
+    """(the least, what is asked for).  mask: what of it the 8-bit cache's workspace depends
+    on; most: PAGED8_ROOM; hook: MASKATTN_PAGED8_ROOM, which the library reads."""
     sh = attn_shape_t(*shape, 0)
-    if mask is None:
-        r, n = attn_paged_workspace_size(sh)
-    else:
-        r, n = attn_paged8_workspace_size(sh)
-        if r == ATTN_OK:
-            kind, window, first, total_q = mask
-            _, more = attn_paged8_workspace_size(
-                sh, attn_mask_desc_t(kind=kind, window=window, first=first, total_q=total_q))
-            n = more if more - n <= most else n
+    size, name = (attn_paged_workspace_size, "attn_paged_workspace_size") if mask is None else \
+        (attn_paged8_workspace_size, "attn_paged8_workspace_size")
+    r, least = size(sh)
     if r != ATTN_OK:
-        raise AttnError(r, "attn_paged_workspace_size" if mask is None else
-                        "attn_paged8_workspace_size")
-    return n
+        raise AttnError(r, name)
+    if mask is None:
+        return least, least
+    kind, window, first, total_q = mask
+    _, n = attn_paged8_workspace_size(
+        sh, attn_mask_desc_t(kind=kind, window=window, first=first, total_q=total_q))
+    return least, n if n - least <= most else least
 
 
 def paged_workspace(q: torch.Tensor, cache, mask: Mask,
                     shape: Optional[attn_shape_t] = None) -> torch.Tensor:
-    """A workspace of paged_fwd; for a PagedCache8 and chunks with room for the rows
-    that they see in 16 bits, up to PAGED8_ROOM bytes."""
+    """A workspace of paged_fwd.  For a PagedCache8 and chunks with room for the rows
+    that they see in 16 bits, up to PAGED8_ROOM bytes; where the allocator has no
+    memory for that the least, with which the call takes longer."""
     sh = shape or paged_shape(q, cache, mask)
     sizes = (sh.B, sh.Hq, sh.Hkv, sh.Sq, sh.Skv, sh.D, sh.dtype)
     if isinstance(cache, PagedCache8):
-        n = _paged_workspace_bytes(sizes, (mask.kind, mask.window, mask.first, mask.total_q),
-                                   PAGED8_ROOM, os.environ.get("MASKATTN_PAGED8_ROOM"))
+        least, n = _paged_workspace_bytes(sizes,
+                                          (mask.kind, mask.window, mask.first, mask.total_q),
+                                          PAGED8_ROOM, os.environ.get("MASKATTN_PAGED8_ROOM"))
     else:
-        n = _paged_workspace_bytes(sizes, None)
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+        least, n = _paged_workspace_bytes(sizes, None)
+    if n > least:
+        try:
+            return torch.empty(n, dtype=torch.uint8, device=q.device)
+        except torch.OutOfMemoryError:
+            pass
+    return torch.empty(least, dtype=torch.uint8, device=q.device)
 
 
 def paged_fwd(q, cache, block_table, sink, mask: Mask, scale: float,
               ws: Optional[torch.Tensor] = None, out=None, stream=None):
     """Attention of the packed new tokens q [total_q, Hq, 128] over the cache, a
     PagedCache or PagedCache8; returns (o, lse).  out: (o, lse) to write, of which
-    lse may be None; without it they belong to `stream`, as fwd's results do."""
+    lse may be None; without it they belong to `stream`, as fwd's results do.  ws: a
+    workspace; without it the call takes paged_workspace's from the allocator, for
+    chunks over a PagedCache8 up to PAGED8_ROOM bytes (2 GiB) and the least."""
     cu, lens = mask.cu_seqlens_q, mask.seqlen_k
     if cu is None or lens is None or cu.numel() != lens.numel() + 1:
         raise ValueError("the mask needs cu_seqlens_q [B + 1] and seqlen_k [B]")

@@ -1,4 +1,5 @@
 """Workspaces of attention over the 8-bit cache: how much the binding asks for."""
+import pytest
 import torch
 
 from masked_attention_backward_gb300 import binding as mab
@@ -50,3 +51,45 @@ def test_the_most_that_is_asked_for(monkeypatch):
     assert c.given() == least
     monkeypatch.setattr(mab, "PAGED8_ROOM", room - least)
     assert c.given() == room
+
+
+def test_the_least_where_there_is_no_memory_for_more(monkeypatch):
+    monkeypatch.delenv("MASKATTN_PAGED8_ROOM", raising=False)
+    c = Call()
+    least, room = c.sizes()
+    empty = torch.empty
+
+    def short(n, *a, **kw):
+        if n > least:
+            raise torch.OutOfMemoryError("no memory")
+        return empty(n, *a, **kw)
+
+    monkeypatch.setattr(torch, "empty", short)
+    assert c.given() == least
+    # ... and where there is not even that, the allocator's error
+    least -= 1
+    with pytest.raises(torch.OutOfMemoryError):
+        c.given()
+
+
+@pytest.mark.gpu
+def test_a_call_where_there_is_no_memory_for_more(cuda_lib, monkeypatch):
+    """Goes on with the least workspace, with that workspace's results."""
+    import test_paged8_fwd_gpu as fwd
+    monkeypatch.setenv("MASKATTN_PAGED8_ROOM", "1")
+    c = fwd.Case([(300, 700), (1, 90)], ps=32)
+    (o, lse), _ = c.run(room=False)
+    least = c.workspace(room=False).numel()
+    assert c.workspace().numel() > least
+    empty, refused = torch.empty, []
+
+    def short(*a, **kw):
+        if kw.get("dtype") == torch.uint8 and a[0] > least:
+            refused.append(a[0])
+            raise torch.OutOfMemoryError("no memory")
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", short)
+    got = mab.paged_fwd(c.q, c.cache, c.table, c.sink, c.mask, fwd.SCALE)
+    assert refused and torch.equal(got[0], o) and torch.equal(got[1], lse)
+    c.check(*got)
