@@ -101,3 +101,11 @@ def test_captured(cuda_lib, monkeypatch, B):
         torch.cuda.synchronize()
         assert mab.device_status(ws) == mab.ATTN_OK
         b.check(*out)
+
+
+@pytest.mark.parametrize("reqs", [[(100, 30)], [(150, 149), (9, 0), (3, 1)], [(130, 64), (1, 200)]])
+@pytest.mark.parametrize("room", [True, False])
+def test_more_tokens_than_keys(cuda_lib, monkeypatch, reqs, room):
+    """Tokens before position zero see nothing, in every kernel."""
+    monkeypatch.setenv("MASKATTN_PAGED8_ROOM", "1")
+    go(padded(reqs, 150, form=("i8", F16), sink=len(reqs) != 1), room)
