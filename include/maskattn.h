@@ -409,7 +409,12 @@ typedef struct {
  * that is the new one the earlier rows' codes are rounded in units of it, held back
  * as the new ones are.  Rows of the block past the new ones mean nothing afterwards.
  * A value that is not finite makes the scale 255: the block reads as NaN until it
- * begins anew. */
+ * begins anew.
+ *
+ * So a block does not forget tokens that are taken back (speculated ones that failed):
+ * those stored in their place share the scale that they left, and are rounded in its
+ * units, or read as NaN after a value that was not finite, until the block is stored
+ * from row 0 again.  With block 1 every row begins its block. */
 attn_status_t attn_paged8_store(const attn_pages8_t* pages, int T, const void* k, const void* v,
                                 long long k_stride, long long v_stride, const long long* slot_map,
                                 void* k_pages, void* v_pages, uint8_t* k_scales,

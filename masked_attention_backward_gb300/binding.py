@@ -785,7 +785,8 @@ def paged_store(cache, k, v, slot_map, stream=None) -> None:
     """Rows of k and v ([T, Hkv, 128], possibly slices of a larger tensor) into
     their slots of the cache, a PagedCache or PagedCache8 (int64 [T]; negative:
     skipped).  A PagedCache8 wants the rows of each block of tokens consecutive,
-    as a plan's slot_map has them."""
+    as a plan's slot_map has them; its blocks keep the scale of tokens that are
+    taken back until they are stored from their first row again."""
     T = slot_map.numel()
     for t, n in ((k, "k"), (v, "v")):
         if t.dtype != cache.dtype or tuple(t.shape) != (T, cache.Hkv, 128) or \
@@ -888,7 +889,8 @@ def paged_workspace(q: torch.Tensor, cache, mask: Mask,
                     shape: Optional[attn_shape_t] = None) -> torch.Tensor:
     """A workspace of paged_fwd.  For a PagedCache8 and chunks with room for the rows
     that they see in 16 bits, up to PAGED8_ROOM bytes; where the allocator has no
-    memory for that the least, with which the call takes longer."""
+    memory for that the least, with which the call takes longer (and differs by
+    roundings)."""
     sh = shape or paged_shape(q, cache, mask)
     sizes = (sh.B, sh.Hq, sh.Hkv, sh.Sq, sh.Skv, sh.D, sh.dtype)
     if isinstance(cache, PagedCache8):

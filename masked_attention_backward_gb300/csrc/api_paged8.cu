@@ -59,10 +59,17 @@ bool test_paged8_room() {
 int few_tokens(const attn_shape_t* sh) { return PAGED8_ROWS / (sh->Hq / sh->Hkv); }
 
 // Steps (64 keys of a query tile) that an SM has at least, going by the call's bounds,
-// when its chunks' rows are written in 16 bits first.  Four chunks of 256 tokens over 2000
-// keys, 32/8 heads, 54 steps: 63 us so, 72 with tiles made inside the attention; 15 single
-// tokens and a chunk of 500 under a window of 1024, 24 steps: 64 and 52 (two kernels more,
-// and two joins, for the single tokens).
+// when its chunks' rows are written in 16 bits first.  Measured at 32/8 heads, e4m3, us with
+// tiles made inside the attention and with rows written first:
+//   four chunks of 256 over 500 to 4000 keys: 13 steps 35 and 33, 26 52 and 45, 40 64 and 53,
+//     53 75 and 63, 106 116 and 97;
+//   one chunk of 128, 256, 512 over 8000: 26 steps 40 and 45, 52 62 and 58, 105 105 and 84;
+//   15 single tokens and a chunk of 500 over 1000, 2000, 3000: 14 steps 48 and 61, 28 72 and 83,
+//     42 92 and 105 (two kernels more, and two joins, for the single tokens);
+//   the same under a window of 1024, chunks of 500, 1000, 2000: 23 steps 60 and 66, 57 79 and 82,
+//     165 110 and 109.
+// So chunks alone gain from 10 to 50 steps on, chunks beside single tokens from some 150; which
+// of a call's requests are chunks only the device knows, and 40 is between for the former.
 constexpr int EXPAND_STEPS = 40;
 
 // Room for the 16-bit rows of a call's chunks behind the other workspace: pages for as

@@ -24,12 +24,12 @@
 // 706 that a quarter has for a slice at the copy rate, and the conversions and the rest
 // 466 instructions, 198 of them on the half-rate integer pipe.  Sixteen rows leave 12
 // warps' registers, forty 8, whose latencies then show: 64 requests of five tokens (40
-// rows) took 551 us in this form, 420 with the tiles of the tcgen05 kernel
+// rows) took 551 us in this form, 404 with the tiles of the tcgen05 kernel
 // (paged_fwd.cuh), which takes more than 16.
 //
 // Measured (one GB300), 64 single tokens at 9000 keys on average, 64/8 heads, 1.14 GB: e4m3
 // bf16 195 us, 5.9 TB/s (copy rate 6.7), e4m3 fp16 184, int8 fp16 193, int8 bf16 197, a
-// scale a token 212; two tokens each 293.  One token at 1000 keys 15 us: the line 2.5, the
+// scale a token 211; two tokens each 295.  One token at 1000 keys 15 us: the line 2.5, the
 // first slices, the join.  On the way there: the tcgen05 kernel 719 us; this one with
 // cp.async of 16 bytes a lane, every code times 2^120 and bf16 scores 329; with f16 scores
 // of the codes themselves and V's codes as moved bits 237; slices by TMA 202.
@@ -581,7 +581,10 @@ k_paged8_rows(const __grid_constant__ CUtensorMap tK, const __grid_constant__ CU
             }
           }
       }
-      // ---- probabilities as B fragments
+      // ---- probabilities as B fragments: rounded to 16 bits, as the products take them (l sums
+      // the unrounded ones).  With o's own rounding o is off by 2.0e-3 of its norm in bf16 and
+      // 2.5e-4 in fp16; 32-bit probabilities, 1.7e-3 and 2.1e-4, would take a second product
+      // of what the rounding leaves.
       uint32_t pf[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {

@@ -14,8 +14,10 @@
 // other way when read back), a launch for single tokens.
 // Measured (one GB300, 8 heads): 16800 tokens to int8 with a scale each, 16-token pages,
 // 19.6 us, 5.3 TB/s (two rows a half-warp 23.3 when this took 20.5), 76 % of the issue
-// slots; 32 tokens of blocks that hold others 3.2 us;
-// 70000 rows of 64-token blocks back to 16 bits 67.8 us, 6.4 TB/s; 16800 14.7.
+// slots; into 64-token pages 22.5, and with a scale for 16, 32 or 64 tokens 30, 32 and 37
+// (3.4 to 2.8 TB/s: a run's rows past the 16th are read twice); 32 tokens of blocks that
+// hold others 3.3 us; 70000 rows of 64-token blocks back to 16 bits 68 us, 6.3 TB/s; 16800
+// 14.7.
 #include "paged8.h"
 #include "quant8.cuh"
 

@@ -61,7 +61,7 @@
 // Bound by these warps beside the softmax: 3200 warp instructions a step, half of
 // them theirs, on pipes of half rate, and a chain of tile, S, softmax and P V over
 // four tiles (a step takes 1600 cycles; its bytes 700, the products 540).
-// Measured: 2 requests of 4 and 5 tokens at 100000 keys, 32/4 heads, int8, 88 us;
+// Measured: 2 requests of 5 and 4 tokens at 99770 and 107923 keys, 32/4 heads, int8, 89 us;
 // 64 requests of 5 tokens at 9000, 64/8 heads, e4m3, 403; 15 requests of 1 to 4 tokens
 // and a chunk of 500 under a window of 1024, 32/8 heads, fp16, 51; chunks of 1900 tokens
 // over 8000 keys 603, which is why chunks take paged8_expand.cu where the workspace has
@@ -751,7 +751,10 @@ k_paged_fwd(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUte
       auto minus_max = [&]() { return M == -INFINITY ? 0.f : -M; };
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
       // A sub-tile that every row sees whole, from TMEM buffer column `col`: P
-      // packed over it.
+      // packed over it, rounded to 16 bits as O += P V takes it (l sums the unrounded
+      // ones).  With o's own rounding o is off by 2.1e-3 of its norm in bf16 and 2.6e-4 in
+      // fp16; 32-bit probabilities, 1.7e-3 and 2.1e-4, would take a second product of
+      // what the rounding leaves.
       auto whole_step = [&](int i, uint32_t col) -> bool {
         float sv[64];
         tmem_ld32(col, *reinterpret_cast<float(*)[32]>(&sv[0]));

@@ -15,8 +15,8 @@
 // heads, so its eight angles are computed once; eight lanes cover a row.  (Two heads
 // at a time and 24 blocks an SM; four at a time and 8 blocks: 29.1 and 18.6 us below,
 // and 16 blocks 29.0 and 15.9.)
-// Measured (one GB300): 8192 tokens of 40 heads, bf16, 27.9 us, 6.0 TB/s; the gradient of
-// 5003 packed tokens of 32 heads, half of the head, fp16, 16.5 us, 5.0 TB/s; eight tokens
+// Measured (one GB300): 8192 tokens of 40 heads, bf16, 27.8 us, 6.0 TB/s; the gradient of
+// 5003 packed tokens of 32 heads, half of the head, fp16, 14.9 us, 5.5 TB/s; eight tokens
 // 2.7 us, the launch.
 #include <math.h>
 
