@@ -24,7 +24,7 @@
 // 706 that a quarter has for a slice at the copy rate, and the conversions and the rest
 // 466 instructions, 198 of them on the half-rate integer pipe.  Sixteen rows leave 12
 // warps' registers, forty 8, whose latencies then show: 64 requests of five tokens (40
-// rows) took 551 us in this form, 404 with the tiles of the tcgen05 kernel
+// rows) took 551 us in this form, 403 with the tiles of the tcgen05 kernel
 // (paged_fwd.cuh), which takes more than 16.
 //
 // Measured (one GB300), 64 single tokens at 9000 keys on average, 64/8 heads, 1.14 GB: e4m3
